@@ -12,6 +12,15 @@ call fails if the library reports an error.
     o, lse = attn_decode_paged(q, k_pages, v_pages, page_table, seqlens, num_splits=8)
     o, lse = attn_fwd_ex_sink(q, k, v, sink_logit, causal=True)   # sink_logit [Hq] fp32
     o, lse = attn_decode_paged_sink(q, k_pages, v_pages, page_table, seqlens, sink_logit)
+
+Around the attention calls, rotary positions and the paged cache's upkeep:
+
+    inv_freq = attn_rope_inv_freq(128, base=10000.0)              # fp64 [64]
+    q, k = attn_rope(q, k, inv_freq)                              # attn_rope_bwd for gradients
+    attn_pages_resize(page_table, seqlens, new_seqlens, refs, k_pages, v_pages)
+    q = attn_append_paged(q, k, v, k_pages, v_pages, page_table, seqlens, inv_freq=inv_freq)
+    attn_pages_fork(page_table, seqlens, refs, src, dst, k_pages, v_pages)
+    new_index, num_live = attn_pages_compact(page_table, seqlens, refs, k_pages, v_pages)
 """
 from __future__ import annotations
 
@@ -23,10 +32,12 @@ from . import _build
 
 __all__ = [
     "ATTN_OK", "ATTN_ERR_INVALID_ARG", "ATTN_ERR_UNSUPPORTED", "ATTN_ERR_CUDA", "ATTN_ERR_TIMEOUT",
-    "ATTN_ERR_BAD_INPUT", "AttnError", "attn_fwd", "attn_fwd_ex", "attn_fwd_ex_sink",
+    "ATTN_ERR_BAD_INPUT", "ATTN_ERR_NO_PAGES", "AttnError", "attn_fwd", "attn_fwd_ex", "attn_fwd_ex_sink",
     "attn_fwd_paged", "attn_fwd_strided", "attn_bwd", "attn_bwd_ex", "attn_bwd_ex_sink",
     "attn_bwd_workspace_size",
     "attn_decode_workspace_size", "attn_decode_paged", "attn_decode_paged_sink", "attn_device_status", "attn_check_wait_timeout", "attn_status_string",
+    "attn_rope_inv_freq", "attn_rope", "attn_rope_bwd", "attn_append_paged",
+    "attn_pages_workspace_size", "attn_pages_resize", "attn_pages_fork", "attn_pages_compact",
     "attn_last_error", "library_path", "lib",
 ]
 
@@ -36,6 +47,7 @@ ATTN_ERR_UNSUPPORTED = 2
 ATTN_ERR_CUDA = 3
 ATTN_ERR_TIMEOUT = 4
 ATTN_ERR_BAD_INPUT = 5
+ATTN_ERR_NO_PAGES = 6
 
 
 def _load() -> ctypes.CDLL:
@@ -71,6 +83,18 @@ def _load() -> ctypes.CDLL:
                                     vp]
     L.attn_decode_paged_sink.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp,
                                          vp, sz, vp]
+    dbl = ctypes.c_double
+    L.attn_rope_inv_freq.argtypes = [i, dbl, i, dbl, dbl, dbl, dbl, vp]
+    L.attn_rope.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f, i64p, i64p, i64p, i64p,
+                            vp]
+    L.attn_rope_bwd.argtypes = L.attn_rope.argtypes
+    L.attn_append_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f,
+                                    i, i, i, i64p, i64p, i64p, i64p, vp]
+    L.attn_pages_workspace_size.argtypes = [i, i]
+    L.attn_pages_workspace_size.restype = sz
+    L.attn_pages_resize.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp, sz, vp]
+    L.attn_pages_fork.argtypes = [vp, vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, i, i, vp, sz, vp]
+    L.attn_pages_compact.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp, sz, vp]
     L.attn_device_status.argtypes = [vp]
     L.attn_check_wait_timeout.argtypes = [i, vp]
     L.attn_status_string.argtypes = [i]
@@ -80,7 +104,9 @@ def _load() -> ctypes.CDLL:
     for fn in ("attn_fwd", "attn_fwd_ex", "attn_fwd_ex_sink", "attn_fwd_paged", "attn_fwd_strided",
                "attn_bwd", "attn_bwd_ex", "attn_bwd_ex_sink",
                "attn_decode_paged",
-               "attn_decode_paged_sink", "attn_device_status", "attn_check_wait_timeout"):
+               "attn_decode_paged_sink", "attn_rope_inv_freq", "attn_rope", "attn_rope_bwd",
+               "attn_append_paged", "attn_pages_resize", "attn_pages_fork", "attn_pages_compact",
+               "attn_device_status", "attn_check_wait_timeout"):
         getattr(L, fn).restype = ctypes.c_int
     return L
 
@@ -501,6 +527,325 @@ def _decode(q, k_pages, v_pages, page_table, seqlens, sink_logit, o, lse, num_sp
                                         _ptr(sink_logit), _ptr(workspace), wbytes, _stream(stream))
         _check(rc, "attn_decode_paged_sink")
     return o, lse
+
+
+# ---------------------------------------------------------------- around the attention calls
+
+class _Call:
+    """Device and stream of one call: the tensors' device is current inside, and
+    tensors made inside belong to the stream that the call runs on."""
+    __slots__ = ("raw", "_contexts")
+
+    def __init__(self, index, stream):
+        torch = _torch()
+        self._contexts = ()
+        if index != torch.cuda.current_device():
+            self._contexts = (torch.cuda.device(index),)
+        if stream is None:
+            self.raw = torch._C._cuda_getCurrentRawStream(index)
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            raw = int(getattr(stream, "cuda_stream", stream))
+            stream = torch.cuda.ExternalStream(raw, device=index) if raw else \
+                torch.cuda.default_stream(index)
+        self.raw = stream.cuda_stream
+        self._contexts += (torch.cuda.stream(stream),)
+
+    def __enter__(self):
+        for c in self._contexts:
+            c.__enter__()
+        return self.raw
+
+    def __exit__(self, *exc):
+        for c in reversed(self._contexts):
+            c.__exit__(*exc)
+
+
+def _rows_tensor(t, name, dims, index):
+    """bf16 on device `index`, `dims` dimensions, the last one contiguous."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16 or not t.is_cuda:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor")
+    if t.dim() not in dims:
+        raise ValueError(f"{name} must have {' or '.join(map(str, dims))} dimensions")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
+def _int_tensor(t, name, shape, index):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.int32 or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on cuda:{index}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _frequencies(inv_freq, d, index):
+    torch = _torch()
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype is not torch.float64 or \
+            inv_freq.dim() != 1 or inv_freq.get_device() != index or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq must be a contiguous float64 vector on cuda:{index}")
+    rot = 2 * inv_freq.shape[0]
+    if rot > d:
+        raise ValueError(f"inv_freq holds {rot // 2} pairs, a head has {d // 2}")
+    return rot
+
+
+def _stride_array(t, n):
+    """The first n of the last n + 1 strides as a C array, or None if t is contiguous."""
+    if t is None or t.is_contiguous():
+        return None
+    return (ctypes.c_longlong * n)(*t.stride()[-n - 1:-1])
+
+
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
+
+
+def attn_rope_inv_freq(rotary_dim: int, base: float = 10000.0, *, scaling: str = "none",
+                       factor: float = 1.0, original_length: float = 0.0, ramp=(1.0, 32.0),
+                       device="cuda"):
+    """Radians per position of each rotated pair, base^(-2i/rotary_dim), as the fp64
+    tensor [rotary_dim / 2] that attn_rope and attn_append_paged take.  scaling
+    stretches it for contexts longer than the trained one: "linear" (every
+    frequency / factor), "base" (a larger base: the slowest pair / factor) or
+    "ramp" (pairs that turn more than ramp[1] times over original_length are
+    kept, those that turn less than ramp[0] times / factor)."""
+    torch = _torch()
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}")
+    out = torch.empty(max(int(rotary_dim) // 2, 0), dtype=torch.float64)
+    _check(lib.attn_rope_inv_freq(int(rotary_dim), float(base), _ROPE_SCALINGS[scaling],
+                                  float(factor), float(original_length), float(ramp[0]),
+                                  float(ramp[1]), out.data_ptr()), "attn_rope_inv_freq")
+    return out.to(device)
+
+
+def attn_rope(q, k, inv_freq, positions=None, *, interleaved=False, amplitude=1.0, q_out=None,
+              k_out=None, stream=None):
+    """Rotary positions: q [B,S,Hq,d] and k [B,S,Hkv,d] (or packed [T,H,d]) bf16, any
+    strides with d contiguous, turned by positions [B,S] ([T]) int32 (default: the
+    row's index) times inv_freq fp64 [rotary_dim / 2] -> (q_out, k_out).  Either of q
+    and k may be None.  In place: q_out=q, k_out=k."""
+    return _rope(lib.attn_rope, "attn_rope", ("q", "k"), q, k, inv_freq, positions, interleaved,
+                 amplitude, q_out, k_out, stream)
+
+
+def attn_rope_bwd(dq, dk, inv_freq, positions=None, *, interleaved=False, amplitude=1.0,
+                  dq_out=None, dk_out=None, stream=None):
+    """Gradients of attn_rope: from dq, dk of its outputs those of its inputs, with the
+    forward's inv_freq, positions, interleaved and amplitude -> (dq_out, dk_out)."""
+    return _rope(lib.attn_rope_bwd, "attn_rope_bwd", ("dq", "dk"), dq, dk, inv_freq, positions,
+                 interleaved, amplitude, dq_out, dk_out, stream)
+
+
+def _rope(fn, what, names, q, k, inv_freq, positions, interleaved, amplitude, q_out, k_out,
+          stream):
+    torch = _torch()
+    lead = q if q is not None else k
+    if lead is None:
+        raise ValueError(f"{names[0]} or {names[1]} must be given")
+    index = None
+    for t, n in ((q, names[0]), (k, names[1])):
+        if t is not None:
+            _rows_tensor(t, n, (3, 4), index)
+            index = t.get_device()
+    shape = lead.shape
+    if q is not None and k is not None and (
+            k.dim() != q.dim() or k.shape[:-2] != shape[:-2] or k.shape[-1] != shape[-1]):
+        raise ValueError(f"{names[0]} and {names[1]} shapes disagree")
+    d = shape[-1]
+    B, S = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
+    rot = _frequencies(inv_freq, d, index)
+    if positions is not None:
+        _int_tensor(positions, "positions", None, index)
+        if positions.numel() != B * S:
+            raise ValueError(f"positions must hold {B * S} values")
+    with _Call(index, stream) as raw:
+        args = []
+        for t, o, n in ((q, q_out, names[0]), (k, k_out, names[1])):
+            if t is None:
+                o = None
+            elif o is None:
+                o = torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
+            else:
+                _rows_tensor(o, n + "_out", (t.dim(),), index)
+                if o.shape != t.shape:
+                    raise ValueError(f"{n}_out must be shaped like {n}")
+            args.append(o)
+        q_out, k_out = args
+        # packed rows have row and head strides only: a leading 0 is their batch stride
+        sq, sk, sqo, sko = ((_stride_array(t, 3) if t is None or t.dim() == 4 or
+                             t.is_contiguous() else
+                             (ctypes.c_longlong * 3)(0, t.stride(0), t.stride(1)))
+                            for t in (q, k, q_out, k_out))
+        _check(fn(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(positions),
+                  inv_freq.data_ptr(), B, S, 0 if q is None else q.shape[-2],
+                  0 if k is None else k.shape[-2], d, rot, 1 if interleaved else 0, amplitude, sq,
+                  sk, sqo, sko, raw), what)
+    return q_out, k_out
+
+
+def attn_append_paged(q, k, v, k_pages, v_pages, page_table, seqlens_k, cu_seqlens_q=None,
+                      inv_freq=None, *, interleaved=False, amplitude=1.0, q_out=None, stream=None):
+    """New tokens of a serving step: k, v [T,Hkv,d] written to their slots of the paged
+    cache k_pages, v_pages [P,16,Hkv,d], k rotated on the way; returns q [T,Hq,d]
+    rotated (None if q is None).  page_table [B,maxP], seqlens_k [B] (lengths WITH
+    the new tokens) and cu_seqlens_q [B+1] int32; without cu_seqlens_q every
+    sequence has one new token (T = B).  inv_freq None: nothing is rotated."""
+    torch = _torch()
+    _rows_tensor(k, "k", (3,), None)
+    index = k.get_device()
+    _rows_tensor(v, "v", (3,), index)
+    _rows_tensor(k_pages, "k_pages", (4,), index)
+    _rows_tensor(v_pages, "v_pages", (4,), index)
+    T, Hkv, d = k.shape
+    P, page = k_pages.shape[0], k_pages.shape[1]
+    if v.shape != k.shape or k_pages.shape[2:] != k.shape[1:] or v_pages.shape != k_pages.shape:
+        raise ValueError("k, v, k_pages and v_pages shapes disagree")
+    if not k_pages.is_contiguous() or not v_pages.is_contiguous():
+        raise ValueError("k_pages and v_pages must be contiguous")
+    B = seqlens_k.numel()
+    _int_tensor(seqlens_k, "seqlens_k", (B,), index)
+    _int_tensor(page_table, "page_table", None, index)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B, max_pages]")
+    if cu_seqlens_q is not None:
+        _int_tensor(cu_seqlens_q, "cu_seqlens_q", (B + 1,), index)
+    elif T != B:
+        raise ValueError("without cu_seqlens_q every sequence has one new token")
+    Hq = 0
+    if q is not None:
+        _rows_tensor(q, "q", (3,), index)
+        if q.shape[0] != T or q.shape[2] != d:
+            raise ValueError("q and k shapes disagree")
+        Hq = q.shape[1]
+    rot = 0 if inv_freq is None else _frequencies(inv_freq, d, index)
+    with _Call(index, stream) as raw:
+        if q is None:
+            q_out = None
+        elif q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        else:
+            _rows_tensor(q_out, "q_out", (3,), index)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must be shaped like q")
+        _check(lib.attn_append_paged(
+            _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), k_pages.data_ptr(),
+            v_pages.data_ptr(), page_table.data_ptr(), _ptr(cu_seqlens_q), seqlens_k.data_ptr(),
+            _ptr(inv_freq), B, Hq, Hkv, T, d, rot, 1 if interleaved else 0, amplitude, page,
+            page_table.shape[1], P, _stride_array(q, 2), _stride_array(k, 2),
+            _stride_array(v, 2), _stride_array(q_out, 2), raw), "attn_append_paged")
+    return q_out
+
+
+def attn_pages_workspace_size(rows: int, num_pages: int) -> int:
+    return int(lib.attn_pages_workspace_size(int(rows), int(num_pages)))
+
+
+def _cache_tables(page_table, seqlens, refs):
+    torch = _torch()
+    if not isinstance(refs, torch.Tensor) or not refs.is_cuda or refs.dim() != 1:
+        raise ValueError("refs must be a CUDA vector")
+    index = refs.get_device()
+    _int_tensor(refs, "refs", None, index)
+    _int_tensor(page_table, "page_table", None, index)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    _int_tensor(seqlens, "seqlens", page_table.shape[:1], index)
+    return index
+
+
+def _cache_pools(k_pages, v_pages, pages, index):
+    """(layers, page size, Hkv, d) of pools [layers, P, 16, Hkv, d] or [P, 16, Hkv, d]."""
+    _rows_tensor(k_pages, "k_pages", (4, 5), index)
+    _rows_tensor(v_pages, "v_pages", (4, 5), index)
+    shape = k_pages.shape
+    if v_pages.shape != shape or shape[-4] != pages:
+        raise ValueError(f"k_pages and v_pages must hold the {pages} pages that refs counts")
+    if not k_pages.is_contiguous() or not v_pages.is_contiguous():
+        raise ValueError("k_pages and v_pages must be contiguous")
+    return shape[0] if len(shape) == 5 else 1, shape[-3], shape[-2], shape[-1]
+
+
+def _workspace(workspace, rows, pages, index):
+    torch = _torch()
+    if workspace is None:
+        return torch.empty(attn_pages_workspace_size(rows, pages), dtype=torch.uint8,
+                           device=torch.device("cuda", index))
+    if not workspace.is_cuda or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    return workspace
+
+
+def attn_pages_resize(page_table, seqlens, new_seqlens, refs, k_pages=None, v_pages=None, *,
+                      workspace=None, stream=None) -> None:
+    """Sets every row's length, in place: pages past a shorter row's end are given back
+    (0 frees the row), a longer row gets the lowest free pages; one that grows
+    inside a last page it shares gets a copy of that page first.  page_table
+    [B,maxP], seqlens, new_seqlens [B], refs [P] int32; k_pages, v_pages [P,16,Hkv,d]
+    or [layers,P,16,Hkv,d], None for a cache that shares no pages.  A row that finds
+    too few free pages keeps its length (ATTN_ERR_NO_PAGES)."""
+    index = _cache_tables(page_table, seqlens, refs)
+    B, P = page_table.shape[0], refs.shape[0]
+    _int_tensor(new_seqlens, "new_seqlens", seqlens.shape, index)
+    layers, page, Hkv, d = 1, 16, 1, 64
+    if k_pages is not None or v_pages is not None:
+        if k_pages is None or v_pages is None:
+            raise ValueError("k_pages and v_pages must both be given, or neither")
+        layers, page, Hkv, d = _cache_pools(k_pages, v_pages, P, index)
+    with _Call(index, stream) as raw:
+        ws = _workspace(workspace, B, P, index)
+        _check(lib.attn_pages_resize(
+            page_table.data_ptr(), seqlens.data_ptr(), new_seqlens.data_ptr(), refs.data_ptr(),
+            _ptr(k_pages), _ptr(v_pages), B, layers, Hkv, d, page, page_table.shape[1], P,
+            ws.data_ptr(), ws.numel() * ws.element_size(), raw), "attn_pages_resize")
+
+
+def attn_pages_fork(page_table, seqlens, refs, src, dst, k_pages, v_pages, *, workspace=None,
+                    stream=None) -> None:
+    """Rows dst [n] become copies of rows src [n] (int32), in place: whole pages shared,
+    a last page that is not full copied in every layer.  Rows dst must be empty
+    (length 0).  Other arguments as attn_pages_resize's."""
+    index = _cache_tables(page_table, seqlens, refs)
+    B, P = page_table.shape[0], refs.shape[0]
+    n = src.numel()
+    _int_tensor(src, "src", (n,), index)
+    _int_tensor(dst, "dst", (n,), index)
+    layers, page, Hkv, d = _cache_pools(k_pages, v_pages, P, index)
+    with _Call(index, stream) as raw:
+        ws = _workspace(workspace, n, P, index)
+        _check(lib.attn_pages_fork(
+            page_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(), src.data_ptr(),
+            dst.data_ptr(), n, k_pages.data_ptr(), v_pages.data_ptr(), B, layers, Hkv, d, page,
+            page_table.shape[1], P, ws.data_ptr(), ws.numel() * ws.element_size(), raw),
+            "attn_pages_fork")
+
+
+def attn_pages_compact(page_table, seqlens, refs, k_pages, v_pages, *, workspace=None,
+                       stream=None):
+    """Moves the live pages (refs > 0) to the front of the pool, in place, in every layer,
+    and renames them in the table -> (new_index [P], num_live [1]) int32: where each
+    page is now (-1: free) and how many are live."""
+    torch = _torch()
+    index = _cache_tables(page_table, seqlens, refs)
+    B, P = page_table.shape[0], refs.shape[0]
+    layers, page, Hkv, d = _cache_pools(k_pages, v_pages, P, index)
+    with _Call(index, stream) as raw:
+        ws = _workspace(workspace, 0, P, index)
+        out = torch.empty(P + 1, dtype=torch.int32, device=refs.device)
+        new_index, num_live = out[:P], out[P:]
+        _check(lib.attn_pages_compact(
+            page_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(), new_index.data_ptr(),
+            num_live.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), B, layers, Hkv, d, page,
+            page_table.shape[1], P, ws.data_ptr(), ws.numel() * ws.element_size(), raw),
+            "attn_pages_compact")
+    return new_index, num_live
 
 
 def attn_device_status(stream=None) -> int:

@@ -22,6 +22,8 @@ __device__ int g_attn_status;
 
 thread_local std::string t_last_error;
 
+}  // namespace
+
 int set_error(int code, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -35,6 +37,10 @@ int set_error(int code, const char* fmt, ...) {
 int cuda_error(cudaError_t e, const char* what) {
   return set_error(ATTN_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+
+void clear_error() { t_last_error.clear(); }
+
+namespace {
 
 // ---------------------------------------------------------------- per-device state
 constexpr int kMaxDevices = 64;
@@ -117,7 +123,20 @@ int make_map(CUtensorMap* m, const void* ptr, uint64_t d, uint64_t n1, uint64_t 
   return ATTN_OK;
 }
 
+}  // namespace
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int device_info(int* num_sms, int** status) {
+  DeviceState* s = nullptr;
+  const int rc = device_state(&s);
+  if (rc != ATTN_OK) return rc;
+  *num_sms = s->num_sms;
+  *status = s->status;
+  return ATTN_OK;
+}
+
+namespace {
 
 // ---------------------------------------------------------------- timeout check
 __global__ void wait_timeout_check_kernel(int* status, uint64_t limit_ns) {
@@ -165,6 +184,7 @@ ATTN_API const char* attn_status_string(int status) {
     case ATTN_ERR_CUDA: return "CUDA error";
     case ATTN_ERR_TIMEOUT: return "a kernel's bounded wait ran out";
     case ATTN_ERR_BAD_INPUT: return "out-of-range device data (page index or sequence offsets)";
+    case ATTN_ERR_NO_PAGES: return "the page pool had too few free pages for a row";
     default: return "unknown status";
   }
 }
@@ -724,6 +744,7 @@ ATTN_API int attn_device_status(void* stream) {
   if (word & kStatusTimeout) return ATTN_ERR_TIMEOUT;
   if (word & kStatusBadInput) return ATTN_ERR_BAD_INPUT;
   if (word & kStatusLayout) return ATTN_ERR_UNSUPPORTED;
+  if (word & kStatusNoPages) return ATTN_ERR_NO_PAGES;
   return ATTN_OK;
 }
 

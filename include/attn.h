@@ -70,9 +70,23 @@ typedef enum attn_status {
   ATTN_ERR_UNSUPPORTED = 2, /* head dim not supported by the call, page size not 16, device not sm_103 */
   ATTN_ERR_CUDA = 3,        /* a CUDA runtime/driver call or a launch failed */
   ATTN_ERR_TIMEOUT = 4,     /* a kernel's bounded wait ran out (device status) */
-  ATTN_ERR_BAD_INPUT = 5    /* a kernel met out-of-range device data, e.g. a page
+  ATTN_ERR_BAD_INPUT = 5,   /* a kernel met out-of-range device data, e.g. a page
                                index outside [0, num_pages_total) (device status) */
+  ATTN_ERR_NO_PAGES = 6     /* too few free pages for a row of attn_pages_resize or
+                               attn_pages_fork, which was left as it was (device status) */
 } attn_status;
+
+/* How attn_rope_inv_freq stretches the positions for contexts longer than the
+   trained one. */
+typedef enum attn_rope_scaling {
+  ATTN_ROPE_NONE = 0,   /* f_i = base^(-2 i / r) */
+  ATTN_ROPE_LINEAR = 1, /* f_i / factor */
+  ATTN_ROPE_BASE = 2,   /* base * factor^(r / (r - 2)): the fastest pair keeps its
+                           frequency, the slowest is stretched by factor */
+  ATTN_ROPE_RAMP = 3    /* by the turns t_i = original_length f_i / 2 pi a pair makes
+                           over the trained length: f_i kept from t_i = ramp_high up,
+                           f_i / factor up to ramp_low, linear in t_i between */
+} attn_rope_scaling;
 
 /*
  * Dense attention forward, BSHD layout.
@@ -351,11 +365,191 @@ ATTN_API int attn_decode_paged_noalloc(const void* q, const void* k_pages, const
                                        float scale, void* stream);
 
 /*
+ * Rotary positions.  There is no counterpart on the source pages, which take
+ * q and k as given: this and the calls below, up to attn_pages_compact, are
+ * additions of this library for what stands around its attention calls.
+ *   Pair i of a head's first rotary_dim elements turns by p f_i, p the row's
+ * position and f_i = inv_freq[i]:
+ *     x' = amplitude (x cos(p f_i) - y sin(p f_i))
+ *     y' = amplitude (x sin(p f_i) + y cos(p f_i)),
+ * where (x, y) are elements (i, i + rotary_dim / 2) of the head, or
+ * (2 i, 2 i + 1) if interleaved.  Elements from rotary_dim on are passed
+ * through.  The angle is exact to 1e-6 radians for every int32 position and
+ * |f_i| <= 1 (formed in 64 bits); products and sums are fp32, rounded once.
+ *
+ * attn_rope_inv_freq fills the HOST array inv_freq [rotary_dim / 2] with
+ * f_i = base^(-2 i / rotary_dim), stretched as `scaling` says (factor for all
+ * but ATTN_ROPE_NONE; original_length, ramp_low and ramp_high for
+ * ATTN_ROPE_RAMP).  Host only, no CUDA call.
+ */
+ATTN_API int attn_rope_inv_freq(int rotary_dim, double base, int scaling, double factor,
+                                double original_length, double ramp_low, double ramp_high,
+                                double* inv_freq);
+
+/*
+ * Rotates q and k of a dense batch, or of packed rows as B = 1, S = rows.
+ *   q, q_out [B, S, Hq, d]   k, k_out [B, S, Hkv, d]   bf16, d 64, 128 or 256
+ *     Either may be left out: Hq or Hkv 0 and null pointers.
+ *   positions: DEVICE int32 [B * S], any value, or NULL: row s of each
+ *     sequence is at position s.
+ *   inv_freq: DEVICE fp64 [rotary_dim / 2], finite.
+ *   rotary_dim: even, 0 (a plain copy) to d.  Multiples of 16 run on 16-byte
+ *     loads and stores, others on 2-byte ones.
+ *   q_strides .. k_out_strides: HOST arrays of three int64 strides in elements,
+ *     {batch, row, head}; NULL means contiguous.  The d elements of a head are
+ *     contiguous, strides are multiples of 8, positive for outputs; an input
+ *     may have stride 0 (a broadcast gradient).  The stride of a dimension of
+ *     size one is ignored.
+ *   In place: q_out == q and k_out == k, each with the input's strides.  Other
+ *   overlaps of outputs with inputs or one another give undefined contents.
+ */
+ATTN_API int attn_rope(const void* q, const void* k, void* q_out, void* k_out,
+                       const int* positions, const double* inv_freq, int B, int S, int Hq,
+                       int Hkv, int d, int rotary_dim, int interleaved, float amplitude,
+                       const long long* q_strides, const long long* k_strides,
+                       const long long* q_out_strides, const long long* k_out_strides,
+                       void* stream);
+
+/*
+ * Backward of attn_rope: from the gradients dq, dk of its outputs, those of
+ * its inputs, the transposed turn (by -p f_i, the same amplitude).  Arguments
+ * as attn_rope's.
+ */
+ATTN_API int attn_rope_bwd(const void* dq, const void* dk, void* dq_out, void* dk_out,
+                           const int* positions, const double* inv_freq, int B, int S, int Hq,
+                           int Hkv, int d, int rotary_dim, int interleaved, float amplitude,
+                           const long long* dq_strides, const long long* dk_strides,
+                           const long long* dq_out_strides, const long long* dk_out_strides,
+                           void* stream);
+
+/*
+ * New tokens of a serving step: q and k rotated by their positions, k and v
+ * written to their slots of a paged cache (the layout of attn_decode_paged and
+ * attn_fwd_paged, whose q the rotated q_out is).
+ *   q, q_out [total_q, Hq, d]   k, v [total_q, Hkv, d]   bf16.  q may be left
+ *     out (Hq 0, null pointers).
+ *   cu_seqlens_q: DEVICE int32 [B + 1], sequence b's new tokens at rows
+ *     cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1; or NULL: one token each
+ *     (total_q = B).
+ *   seqlens_k: DEVICE int32 [B], keys of sequence b WITH the new tokens: new
+ *     token i of n is at position and slot t = seqlens_k[b] - n + i, in page
+ *     page_table[b][t / 16], row t % 16.
+ *   rotary_dim 0 (inv_freq may be NULL): q and k are stored as they are.
+ *   q_strides .. q_out_strides: HOST arrays of two int64 strides in elements,
+ *     {row, head}, rules as for attn_rope; NULL means contiguous.  q_out may be
+ *     q, with q's strides.
+ * Rows in no sequence (before cu_seqlens_q[0], from cu_seqlens_q[B] on) are
+ * left as they were.  A token with t < 0 (more new tokens than keys; a decode
+ * row with seqlens_k 0) has no slot: its q is rotated by t, its k and v are
+ * not stored.
+ * Device-side checks (ATTN_ERR_BAD_INPUT): a sequence whose seqlens_k is
+ * negative or above max_pages_per_seq * 16 is skipped; a token whose page is
+ * outside [0, num_pages_total) is not stored (its q is rotated); offsets that
+ * decrease or leave [0, total_q] are reported, and which rows of such a list
+ * are done is not defined (nothing outside the named buffers is written).
+ * Two tokens with one slot (a page held by two growing sequences) race; see
+ * attn_pages_resize, which gives every growing sequence a last page of its own.
+ */
+ATTN_API int attn_append_paged(const void* q, const void* k, const void* v, void* q_out,
+                               void* k_pages, void* v_pages, const int* page_table,
+                               const int* cu_seqlens_q, const int* seqlens_k,
+                               const double* inv_freq, int B, int Hq, int Hkv, int total_q, int d,
+                               int rotary_dim, int interleaved, float amplitude, int page_size,
+                               int max_pages_per_seq, int num_pages_total,
+                               const long long* q_strides, const long long* k_strides,
+                               const long long* v_strides, const long long* q_out_strides,
+                               void* stream);
+
+/*
+ * Pages of a paged cache: handed out, given back, shared and moved on the
+ * device, without a host synchronisation.
+ *   page_table [B, max_pages_per_seq], seqlens [B]: DEVICE int32, as the
+ *     attention calls read them; row b holds ceil(seqlens[b] / 16) pages, its
+ *     entries from there on are neither read nor, except to add pages, written.
+ *   refs [num_pages_total] DEVICE int32: in how many of those entries page p
+ *     stands (plus holds of the caller's own, if any).  refs[p] <= 0: page p is
+ *     free.  A fresh cache has refs, seqlens 0.  The calls keep refs in step
+ *     with the table; a table and refs that disagree give undefined contents,
+ *     never an access outside the buffers.
+ *   k_pages, v_pages: the pools of `layers` layers that share the table,
+ *     [layers, num_pages_total, 16, Hkv, d] bf16 (layer l's pool is what the
+ *     attention calls take).
+ *   Pages are taken lowest index first, by the rows in order, so equal calls
+ *     give equal tables.
+ *   workspace: DEVICE, 16-byte aligned, attn_pages_workspace_size(rows,
+ *     num_pages_total) bytes (rows: B for a resize, n for a fork, 0 for a
+ *     compaction), overwritten; calls that may overlap need one each.
+ * Calls on one cache, attention calls among them, must be ordered (one
+ * stream, or events).  At most 8192 rows and 2^23 pages a call
+ * (ATTN_ERR_INVALID_ARG).  attn_pages_workspace_size: 0 on invalid sizes.
+ */
+ATTN_API size_t attn_pages_workspace_size(int rows, int num_pages_total);
+
+/*
+ * Sets the length of every row: new_seqlens [B] DEVICE int32, 0 to
+ * max_pages_per_seq * 16.
+ *   Shorter: the pages past the new end are given back (refs - 1); 0 frees the
+ *     row.  All rows' pages are given back before any are taken.
+ *   Longer: pages are added (refs = 1); attn_append_paged then fills them.  A
+ *     row that grows inside a last page which another row holds too first gets
+ *     a copy of it in every layer, and drops its hold; where several rows that
+ *     share it grow in one call, each gets a copy.
+ *   Too few free pages: rows are served in order while the pages last; a row
+ *     that asks for pages past them keeps its table entries and length
+ *     (ATTN_ERR_NO_PAGES, and seqlens[b] != new_seqlens[b]), also when a
+ *     later, smaller wish would still fit.
+ *   k_pages and v_pages may be NULL for a cache whose rows share no pages: no
+ *     last page is then copied (layers, Hkv and d must still be valid).
+ * A row with a length out of range, or whose last page is out of range when
+ * it would grow inside it, keeps its length (ATTN_ERR_BAD_INPUT).
+ */
+ATTN_API int attn_pages_resize(int* page_table, int* seqlens, const int* new_seqlens, int* refs,
+                               void* k_pages, void* v_pages, int B, int layers, int Hkv, int d,
+                               int page_size, int max_pages_per_seq, int num_pages_total,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Row dst[i] becomes a copy of row src[i], for i < n (DEVICE int32; one src
+ * may stand many times).  Whole pages are shared (refs + 1); where the source
+ * ends inside a page, that page is copied to a free one in every layer.
+ * seqlens[dst[i]] must be 0 before the call and becomes seqlens[src[i]].
+ *   ATTN_ERR_NO_PAGES: forks are served in order while the pages last; one past
+ *     them leaves its row empty.
+ *   ATTN_ERR_BAD_INPUT, and row dst[i] as it was: an index out of [0, B),
+ *     dst[i] == src[i], a row that is not empty, a row forked into a second
+ *     time (the first fork stands), a source with a length or last page out of
+ *     range.  A source that is itself some dst counts as empty.
+ */
+ATTN_API int attn_pages_fork(int* page_table, int* seqlens, int* refs, const int* src,
+                             const int* dst, int n, void* k_pages, void* v_pages, int B,
+                             int layers, int Hkv, int d, int page_size, int max_pages_per_seq,
+                             int num_pages_total, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * Moves the L live pages (refs > 0) to indices 0 .. L-1, in every layer: the
+ * k-th live page at or past L goes to the k-th free page before L, with its
+ * count, and the table follows.  Pages already before L stay.
+ *   new_index [num_pages_total] DEVICE int32 (out): where page p is now, -1 if
+ *     it is free (for pages the caller holds outside the table).
+ *   num_live [1] DEVICE int32 (out): L.
+ *   An entry that is no page, or a free one, stays (ATTN_ERR_BAD_INPUT), as do
+ *   the entries of a row whose length is out of range.
+ */
+ATTN_API int attn_pages_compact(int* page_table, const int* seqlens, int* refs, int* new_index,
+                                int* num_live, void* k_pages, void* v_pages, int B, int layers,
+                                int Hkv, int d, int page_size, int max_pages_per_seq,
+                                int num_pages_total, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
  * Synchronises `stream`, then returns and clears the device-side status word
- * of the current device (ATTN_OK, ATTN_ERR_TIMEOUT, ATTN_ERR_BAD_INPUT, or
+ * of the current device (ATTN_OK, ATTN_ERR_TIMEOUT, ATTN_ERR_BAD_INPUT,
+ * ATTN_ERR_NO_PAGES, or
  * ATTN_ERR_UNSUPPORTED when a kernel found its dynamic shared memory off the
  * 1024-byte boundary its layout assumes and wrote nothing), or ATTN_ERR_CUDA
- * if the synchronisation itself failed.
+ * if the synchronisation itself failed.  Where several were recorded, the
+ * first of TIMEOUT, BAD_INPUT, UNSUPPORTED, NO_PAGES is returned.
  */
 ATTN_API int attn_device_status(void* stream);
 

@@ -25,6 +25,7 @@ Around the attention calls, rotary positions and the paged cache's upkeep:
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -136,9 +137,15 @@ def _check(rc: int, what: str) -> None:
         raise AttnError(rc, what)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream):
@@ -530,60 +537,73 @@ def _decode(q, k_pages, v_pages, page_table, seqlens, sink_logit, o, lse, num_sp
 
 
 # ---------------------------------------------------------------- around the attention calls
+# A decode step makes several of these calls a layer, each a few microseconds
+# on the GPU, so their checks are kept to a few attribute reads; the text of a
+# refusal is worked out only once one has failed.
 
 class _Call:
-    """Device and stream of one call: the tensors' device is current inside, and
-    tensors made inside belong to the stream that the call runs on."""
-    __slots__ = ("raw", "_contexts")
+    """Makes the tensors' device and the call's stream current (and with them where
+    tensors made inside belong)."""
+    __slots__ = ("_contexts",)
 
     def __init__(self, index, stream):
         torch = _torch()
-        self._contexts = ()
-        if index != torch.cuda.current_device():
-            self._contexts = (torch.cuda.device(index),)
-        if stream is None:
-            self.raw = torch._C._cuda_getCurrentRawStream(index)
-            return
-        if not isinstance(stream, torch.cuda.Stream):
-            raw = int(getattr(stream, "cuda_stream", stream))
-            stream = torch.cuda.ExternalStream(raw, device=index) if raw else \
-                torch.cuda.default_stream(index)
-        self.raw = stream.cuda_stream
-        self._contexts += (torch.cuda.stream(stream),)
+        self._contexts = (torch.cuda.device(index),)
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                raw = int(getattr(stream, "cuda_stream", stream))
+                stream = torch.cuda.ExternalStream(raw, device=index) if raw else \
+                    torch.cuda.default_stream(index)
+            self._contexts += (torch.cuda.stream(stream),)
 
     def __enter__(self):
         for c in self._contexts:
             c.__enter__()
-        return self.raw
 
     def __exit__(self, *exc):
         for c in reversed(self._contexts):
             c.__exit__(*exc)
 
 
+def _elsewhere(index, stream):
+    """Whether a call has to switch to another device or stream first."""
+    return stream is not None or index != _torch()._C._cuda_getDevice()
+
+
+def _raw_stream(index):
+    return _torch()._C._cuda_getCurrentRawStream(index)
+
+
 def _rows_tensor(t, name, dims, index):
     """bf16 on device `index`, `dims` dimensions, the last one contiguous."""
     torch = _torch()
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() in dims and \
+            index >= 0 and t.get_device() == index and (t.is_contiguous() or t.stride(-1) == 1):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not torch.bfloat16 or not t.is_cuda:
         raise ValueError(f"{name} must be a bf16 CUDA tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.dim() not in dims:
         raise ValueError(f"{name} must have {' or '.join(map(str, dims))} dimensions")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.shape[-1] > 1:
         raise ValueError(f"{name} must have a contiguous last dimension")
-    if index is not None and t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _int_tensor(t, name, shape, index):
+def _int_tensor(t, name, index):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not torch.int32 or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor on cuda:{index}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _int_vector(t, name, n, index):
+    _int_tensor(t, name, index)
+    if t.dim() != 1 or t.numel() != n:
+        raise ValueError(f"{name} must be [{n}], got {list(t.shape)}")
 
 
 def _frequencies(inv_freq, d, index):
@@ -591,17 +611,19 @@ def _frequencies(inv_freq, d, index):
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype is not torch.float64 or \
             inv_freq.dim() != 1 or inv_freq.get_device() != index or not inv_freq.is_contiguous():
         raise ValueError(f"inv_freq must be a contiguous float64 vector on cuda:{index}")
-    rot = 2 * inv_freq.shape[0]
+    rot = 2 * inv_freq.numel()
     if rot > d:
         raise ValueError(f"inv_freq holds {rot // 2} pairs, a head has {d // 2}")
     return rot
 
 
-def _stride_array(t, n):
-    """The first n of the last n + 1 strides as a C array, or None if t is contiguous."""
+def _strides(t, n):
+    """{[batch,] row, head} strides as a C array of n, or None if t is contiguous.  Packed
+    rows have no batch stride."""
     if t is None or t.is_contiguous():
         return None
-    return (ctypes.c_longlong * n)(*t.stride()[-n - 1:-1])
+    st = t.stride()[:-1]
+    return (ctypes.c_longlong * n)(*(st if len(st) == n else (0, *st)))
 
 
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
@@ -647,47 +669,47 @@ def attn_rope_bwd(dq, dk, inv_freq, positions=None, *, interleaved=False, amplit
 def _rope(fn, what, names, q, k, inv_freq, positions, interleaved, amplitude, q_out, k_out,
           stream):
     torch = _torch()
-    lead = q if q is not None else k
+    lead = k if q is None else q
     if lead is None:
         raise ValueError(f"{names[0]} or {names[1]} must be given")
-    index = None
-    for t, n in ((q, names[0]), (k, names[1])):
-        if t is not None:
-            _rows_tensor(t, n, (3, 4), index)
-            index = t.get_device()
+    index = lead.get_device() if isinstance(lead, torch.Tensor) else -1
+    _rows_tensor(lead, names[q is None], (3, 4), index)
     shape = lead.shape
-    if q is not None and k is not None and (
-            k.dim() != q.dim() or k.shape[:-2] != shape[:-2] or k.shape[-1] != shape[-1]):
-        raise ValueError(f"{names[0]} and {names[1]} shapes disagree")
-    d = shape[-1]
-    B, S = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
+    B, S, H, d = shape if len(shape) == 4 else (1, *shape)
+    Hq, Hkv = (H, 0) if q is not None else (0, H)
+    if q is not None and k is not None:
+        _rows_tensor(k, names[1], (len(shape),), index)
+        other = k.shape
+        Hkv = other[-2]
+        if other[0] != shape[0] or other[-1] != d or (len(shape) == 4 and other[1] != S):
+            raise ValueError(f"{names[0]} and {names[1]} shapes disagree")
     rot = _frequencies(inv_freq, d, index)
     if positions is not None:
-        _int_tensor(positions, "positions", None, index)
+        _int_tensor(positions, "positions", index)
         if positions.numel() != B * S:
             raise ValueError(f"positions must hold {B * S} values")
-    with _Call(index, stream) as raw:
-        args = []
-        for t, o, n in ((q, q_out, names[0]), (k, k_out, names[1])):
-            if t is None:
-                o = None
-            elif o is None:
-                o = torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
-            else:
-                _rows_tensor(o, n + "_out", (t.dim(),), index)
-                if o.shape != t.shape:
-                    raise ValueError(f"{n}_out must be shaped like {n}")
-            args.append(o)
-        q_out, k_out = args
-        # packed rows have row and head strides only: a leading 0 is their batch stride
-        sq, sk, sqo, sko = ((_stride_array(t, 3) if t is None or t.dim() == 4 or
-                             t.is_contiguous() else
-                             (ctypes.c_longlong * 3)(0, t.stride(0), t.stride(1)))
-                            for t in (q, k, q_out, k_out))
-        _check(fn(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(positions),
-                  inv_freq.data_ptr(), B, S, 0 if q is None else q.shape[-2],
-                  0 if k is None else k.shape[-2], d, rot, 1 if interleaved else 0, amplitude, sq,
-                  sk, sqo, sko, raw), what)
+    if _elsewhere(index, stream):
+        with _Call(index, stream):
+            return _rope(fn, what, names, q, k, inv_freq, positions, interleaved, amplitude,
+                         q_out, k_out, None)
+    for t, o, n in ((q, q_out, names[0]), (k, k_out, names[1])):
+        if t is not None and o is not None:
+            _rows_tensor(o, n + "_out", (len(shape),), index)
+            if o.shape != t.shape:
+                raise ValueError(f"{n}_out must be shaped like {n}")
+    if q is None:
+        q_out = None
+    elif q_out is None:
+        q_out = torch.empty_like(q)
+    if k is None:
+        k_out = None
+    elif k_out is None:
+        k_out = torch.empty_like(k)
+    rc = fn(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(positions), inv_freq.data_ptr(), B, S,
+            Hq, Hkv, d, rot, 1 if interleaved else 0, amplitude, _strides(q, 3), _strides(k, 3),
+            _strides(q_out, 3), _strides(k_out, 3), _raw_stream(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, what)
     return q_out, k_out
 
 
@@ -699,66 +721,74 @@ def attn_append_paged(q, k, v, k_pages, v_pages, page_table, seqlens_k, cu_seqle
     the new tokens) and cu_seqlens_q [B+1] int32; without cu_seqlens_q every
     sequence has one new token (T = B).  inv_freq None: nothing is rotated."""
     torch = _torch()
-    _rows_tensor(k, "k", (3,), None)
-    index = k.get_device()
+    index = k.get_device() if isinstance(k, torch.Tensor) else -1
+    _rows_tensor(k, "k", (3,), index)
     _rows_tensor(v, "v", (3,), index)
     _rows_tensor(k_pages, "k_pages", (4,), index)
     _rows_tensor(v_pages, "v_pages", (4,), index)
     T, Hkv, d = k.shape
-    P, page = k_pages.shape[0], k_pages.shape[1]
-    if v.shape != k.shape or k_pages.shape[2:] != k.shape[1:] or v_pages.shape != k_pages.shape:
+    P, page, Hp, dp = pool = k_pages.shape
+    if v.shape != k.shape or Hp != Hkv or dp != d or v_pages.shape != pool:
         raise ValueError("k, v, k_pages and v_pages shapes disagree")
-    if not k_pages.is_contiguous() or not v_pages.is_contiguous():
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
         raise ValueError("k_pages and v_pages must be contiguous")
     B = seqlens_k.numel()
-    _int_tensor(seqlens_k, "seqlens_k", (B,), index)
-    _int_tensor(page_table, "page_table", None, index)
+    _int_vector(seqlens_k, "seqlens_k", B, index)
+    _int_tensor(page_table, "page_table", index)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B, max_pages]")
     if cu_seqlens_q is not None:
-        _int_tensor(cu_seqlens_q, "cu_seqlens_q", (B + 1,), index)
+        _int_vector(cu_seqlens_q, "cu_seqlens_q", B + 1, index)
     elif T != B:
         raise ValueError("without cu_seqlens_q every sequence has one new token")
     Hq = 0
     if q is not None:
         _rows_tensor(q, "q", (3,), index)
-        if q.shape[0] != T or q.shape[2] != d:
+        Tq, Hq, dq = q.shape
+        if Tq != T or dq != d:
             raise ValueError("q and k shapes disagree")
-        Hq = q.shape[1]
     rot = 0 if inv_freq is None else _frequencies(inv_freq, d, index)
-    with _Call(index, stream) as raw:
-        if q is None:
-            q_out = None
-        elif q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        else:
-            _rows_tensor(q_out, "q_out", (3,), index)
-            if q_out.shape != q.shape:
-                raise ValueError("q_out must be shaped like q")
-        _check(lib.attn_append_paged(
-            _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), k_pages.data_ptr(),
-            v_pages.data_ptr(), page_table.data_ptr(), _ptr(cu_seqlens_q), seqlens_k.data_ptr(),
-            _ptr(inv_freq), B, Hq, Hkv, T, d, rot, 1 if interleaved else 0, amplitude, page,
-            page_table.shape[1], P, _stride_array(q, 2), _stride_array(k, 2),
-            _stride_array(v, 2), _stride_array(q_out, 2), raw), "attn_append_paged")
+    if _elsewhere(index, stream):
+        with _Call(index, stream):
+            return attn_append_paged(q, k, v, k_pages, v_pages, page_table, seqlens_k,
+                                     cu_seqlens_q, inv_freq, interleaved=interleaved,
+                                     amplitude=amplitude, q_out=q_out)
+    if q is None:
+        q_out = None
+    elif q_out is None:
+        q_out = torch.empty_like(q)
+    else:
+        _rows_tensor(q_out, "q_out", (3,), index)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must be shaped like q")
+    rc = lib.attn_append_paged(
+        _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), k_pages.data_ptr(), v_pages.data_ptr(),
+        page_table.data_ptr(), _ptr(cu_seqlens_q), seqlens_k.data_ptr(), _ptr(inv_freq), B, Hq,
+        Hkv, T, d, rot, 1 if interleaved else 0, amplitude, page, page_table.shape[1], P,
+        _strides(q, 2), _strides(k, 2), _strides(v, 2), _strides(q_out, 2), _raw_stream(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_append_paged")
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
 def attn_pages_workspace_size(rows: int, num_pages: int) -> int:
     return int(lib.attn_pages_workspace_size(int(rows), int(num_pages)))
 
 
 def _cache_tables(page_table, seqlens, refs):
+    """(device index, B, max_pages, P)"""
     torch = _torch()
-    if not isinstance(refs, torch.Tensor) or not refs.is_cuda or refs.dim() != 1:
-        raise ValueError("refs must be a CUDA vector")
-    index = refs.get_device()
-    _int_tensor(refs, "refs", None, index)
-    _int_tensor(page_table, "page_table", None, index)
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    _int_tensor(seqlens, "seqlens", page_table.shape[:1], index)
-    return index
+    index = refs.get_device() if isinstance(refs, torch.Tensor) else -1
+    if index < 0:
+        raise ValueError("refs must be a CUDA tensor")
+    _int_tensor(refs, "refs", index)
+    _int_tensor(page_table, "page_table", index)
+    if page_table.dim() != 2 or refs.dim() != 1:
+        raise ValueError("page_table must be [B, max_pages], refs [P]")
+    B, W = page_table.shape
+    _int_vector(seqlens, "seqlens", B, index)
+    return index, B, W, refs.numel()
 
 
 def _cache_pools(k_pages, v_pages, pages, index):
@@ -766,20 +796,21 @@ def _cache_pools(k_pages, v_pages, pages, index):
     _rows_tensor(k_pages, "k_pages", (4, 5), index)
     _rows_tensor(v_pages, "v_pages", (4, 5), index)
     shape = k_pages.shape
-    if v_pages.shape != shape or shape[-4] != pages:
+    layers, P, page, Hkv, d = shape if len(shape) == 5 else (1, *shape)
+    if v_pages.shape != shape or P != pages:
         raise ValueError(f"k_pages and v_pages must hold the {pages} pages that refs counts")
-    if not k_pages.is_contiguous() or not v_pages.is_contiguous():
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
         raise ValueError("k_pages and v_pages must be contiguous")
-    return shape[0] if len(shape) == 5 else 1, shape[-3], shape[-2], shape[-1]
+    return layers, page, Hkv, d
 
 
-def _workspace(workspace, rows, pages, index):
+def _workspace(workspace, rows, pages, refs):
     torch = _torch()
     if workspace is None:
         return torch.empty(attn_pages_workspace_size(rows, pages), dtype=torch.uint8,
-                           device=torch.device("cuda", index))
-    if not workspace.is_cuda or workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+                           device=refs.device)
+    if workspace.get_device() != refs.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {refs.device}")
     return workspace
 
 
@@ -791,20 +822,24 @@ def attn_pages_resize(page_table, seqlens, new_seqlens, refs, k_pages=None, v_pa
     [B,maxP], seqlens, new_seqlens [B], refs [P] int32; k_pages, v_pages [P,16,Hkv,d]
     or [layers,P,16,Hkv,d], None for a cache that shares no pages.  A row that finds
     too few free pages keeps its length (ATTN_ERR_NO_PAGES)."""
-    index = _cache_tables(page_table, seqlens, refs)
-    B, P = page_table.shape[0], refs.shape[0]
-    _int_tensor(new_seqlens, "new_seqlens", seqlens.shape, index)
+    index, B, W, P = _cache_tables(page_table, seqlens, refs)
+    _int_vector(new_seqlens, "new_seqlens", B, index)
     layers, page, Hkv, d = 1, 16, 1, 64
     if k_pages is not None or v_pages is not None:
         if k_pages is None or v_pages is None:
             raise ValueError("k_pages and v_pages must both be given, or neither")
         layers, page, Hkv, d = _cache_pools(k_pages, v_pages, P, index)
-    with _Call(index, stream) as raw:
-        ws = _workspace(workspace, B, P, index)
-        _check(lib.attn_pages_resize(
-            page_table.data_ptr(), seqlens.data_ptr(), new_seqlens.data_ptr(), refs.data_ptr(),
-            _ptr(k_pages), _ptr(v_pages), B, layers, Hkv, d, page, page_table.shape[1], P,
-            ws.data_ptr(), ws.numel() * ws.element_size(), raw), "attn_pages_resize")
+    if _elsewhere(index, stream):
+        with _Call(index, stream):
+            return attn_pages_resize(page_table, seqlens, new_seqlens, refs, k_pages, v_pages,
+                                     workspace=workspace)
+    ws = _workspace(workspace, B, P, refs)
+    rc = lib.attn_pages_resize(
+        page_table.data_ptr(), seqlens.data_ptr(), new_seqlens.data_ptr(), refs.data_ptr(),
+        _ptr(k_pages), _ptr(v_pages), B, layers, Hkv, d, page, W, P, ws.data_ptr(), ws.nbytes,
+        _raw_stream(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_pages_resize")
 
 
 def attn_pages_fork(page_table, seqlens, refs, src, dst, k_pages, v_pages, *, workspace=None,
@@ -812,19 +847,22 @@ def attn_pages_fork(page_table, seqlens, refs, src, dst, k_pages, v_pages, *, wo
     """Rows dst [n] become copies of rows src [n] (int32), in place: whole pages shared,
     a last page that is not full copied in every layer.  Rows dst must be empty
     (length 0).  Other arguments as attn_pages_resize's."""
-    index = _cache_tables(page_table, seqlens, refs)
-    B, P = page_table.shape[0], refs.shape[0]
+    index, B, W, P = _cache_tables(page_table, seqlens, refs)
     n = src.numel()
-    _int_tensor(src, "src", (n,), index)
-    _int_tensor(dst, "dst", (n,), index)
+    _int_vector(src, "src", n, index)
+    _int_vector(dst, "dst", n, index)
     layers, page, Hkv, d = _cache_pools(k_pages, v_pages, P, index)
-    with _Call(index, stream) as raw:
-        ws = _workspace(workspace, n, P, index)
-        _check(lib.attn_pages_fork(
-            page_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(), src.data_ptr(),
-            dst.data_ptr(), n, k_pages.data_ptr(), v_pages.data_ptr(), B, layers, Hkv, d, page,
-            page_table.shape[1], P, ws.data_ptr(), ws.numel() * ws.element_size(), raw),
-            "attn_pages_fork")
+    if _elsewhere(index, stream):
+        with _Call(index, stream):
+            return attn_pages_fork(page_table, seqlens, refs, src, dst, k_pages, v_pages,
+                                   workspace=workspace)
+    ws = _workspace(workspace, n, P, refs)
+    rc = lib.attn_pages_fork(
+        page_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(), src.data_ptr(),
+        dst.data_ptr(), n, k_pages.data_ptr(), v_pages.data_ptr(), B, layers, Hkv, d, page, W, P,
+        ws.data_ptr(), ws.nbytes, _raw_stream(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_pages_fork")
 
 
 def attn_pages_compact(page_table, seqlens, refs, k_pages, v_pages, *, workspace=None,
@@ -832,19 +870,22 @@ def attn_pages_compact(page_table, seqlens, refs, k_pages, v_pages, *, workspace
     """Moves the live pages (refs > 0) to the front of the pool, in place, in every layer,
     and renames them in the table -> (new_index [P], num_live [1]) int32: where each
     page is now (-1: free) and how many are live."""
-    torch = _torch()
-    index = _cache_tables(page_table, seqlens, refs)
-    B, P = page_table.shape[0], refs.shape[0]
+    index, B, W, P = _cache_tables(page_table, seqlens, refs)
     layers, page, Hkv, d = _cache_pools(k_pages, v_pages, P, index)
-    with _Call(index, stream) as raw:
-        ws = _workspace(workspace, 0, P, index)
-        out = torch.empty(P + 1, dtype=torch.int32, device=refs.device)
-        new_index, num_live = out[:P], out[P:]
-        _check(lib.attn_pages_compact(
-            page_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(), new_index.data_ptr(),
-            num_live.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), B, layers, Hkv, d, page,
-            page_table.shape[1], P, ws.data_ptr(), ws.numel() * ws.element_size(), raw),
-            "attn_pages_compact")
+    if _elsewhere(index, stream):
+        with _Call(index, stream):
+            return attn_pages_compact(page_table, seqlens, refs, k_pages, v_pages,
+                                      workspace=workspace)
+    torch = _torch()
+    ws = _workspace(workspace, 0, P, refs)
+    new_index = torch.empty_like(refs)
+    num_live = torch.empty(1, dtype=torch.int32, device=refs.device)
+    rc = lib.attn_pages_compact(
+        page_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(), new_index.data_ptr(),
+        num_live.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), B, layers, Hkv, d, page, W,
+        P, ws.data_ptr(), ws.nbytes, _raw_stream(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_pages_compact")
     return new_index, num_live
 
 

@@ -16,13 +16,13 @@
 // of the fraction, as half turns in [-1, 1), go through sincospif in fp32.
 // Products and sums are fp32 and are rounded once, to bf16.
 //
-// Layout.  A CTA takes a few consecutive rows (tokens) with all their heads:
-// the row's cos and sin are formed once, kept in shared memory and used by
-// every head (40 heads in a GQA 32/8 call), so no table is read from memory
-// and the bytes are those of q and k alone.  A thread's unit is eight pairs,
-// two 16-byte loads and two 16-byte stores; the loads of a thread's first
-// units are issued before the angles are formed, which hides the position's
-// and frequencies' latency.
+// Layout.  A warp takes a row (token) and up to 16 of its heads (at d = 128):
+// the row's cos and sin are formed once by its lanes, passed round through
+// shared memory and held in registers for every head, so no table is read
+// from memory and the bytes are those of q and k alone.  A lane's unit is
+// eight pairs, two 16-byte loads and two 16-byte stores; all its loads are
+// issued before the angles are formed, which hides the position's and
+// frequencies' latency.  Nothing waits on another warp.
 #include "attn_internal.h"
 #include "sm103_ptx.cuh"
 
@@ -31,9 +31,9 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kBatch = 4;          // units in flight per thread
-constexpr int kMaxRowsPerCta = 32;
+constexpr int kThreads = 64;
+constexpr int kBatch = 4;  // units (passes over heads) of a lane, all in flight at once
+constexpr int kWarpsPerSm = 16;
 
 struct RowInfo {
   long long slot;  // append: element offset of the row's cache slot, or -1
@@ -163,72 +163,90 @@ __device__ __forceinline__ RowInfo append_row(const AppendArgs& p, int row) {
 
 // ---------------------------------------------------------------- rows and heads
 
-// Heads are numbered q, then k, then (append) v.
+// Heads are numbered q, then k, then (append) v.  A row's three pieces, each
+// at its first head:
+struct RowSource {
+  const __nv_bfloat16 *q, *k, *v;
+};
+struct RowTarget {
+  __nv_bfloat16 *q, *k, *v;  // null: not written
+};
+
+__device__ __forceinline__ void split_row(const RopeArgs& p, int row, int* b, int* s) {
+  *b = p.B > 1 ? row / p.S : 0;
+  *s = row - *b * p.S;
+}
+
+template <bool kAppend>
+__device__ __forceinline__ RowSource row_source(const RopeArgs& p, const AppendArgs& ap, int row) {
+  int b, s;
+  split_row(p, row, &b, &s);
+  RowSource r;
+  r.q = p.q + b * p.q_s[0] + s * p.q_s[1];
+  r.k = p.k + b * p.k_s[0] + s * p.k_s[1];
+  r.v = kAppend ? ap.v + s * ap.v_s[0] : nullptr;
+  return r;
+}
+
+template <bool kAppend>
+__device__ __forceinline__ RowTarget row_target(const RopeArgs& p, const AppendArgs& ap,
+                                                const RowInfo& info, int row) {
+  int b, s;
+  split_row(p, row, &b, &s);
+  RowTarget r;
+  r.q = kAppend && !info.live ? nullptr : p.qo + b * p.qo_s[0] + s * p.qo_s[1];
+  if constexpr (kAppend) {
+    r.k = info.slot < 0 ? nullptr : ap.k_pages + info.slot;
+    r.v = info.slot < 0 ? nullptr : ap.v_pages + info.slot;
+  } else {
+    r.k = p.ko + b * p.ko_s[0] + s * p.ko_s[1];
+    r.v = nullptr;
+  }
+  return r;
+}
+
 template <bool kAppend>
 __device__ __forceinline__ const __nv_bfloat16* source(const RopeArgs& p, const AppendArgs& ap,
-                                                       int row, int h) {
-  const int b = p.B > 1 ? row / p.S : 0;
-  const long long s = row - b * p.S;
-  if (h < p.Hq) return p.q + b * p.q_s[0] + s * p.q_s[1] + h * p.q_s[2];
-  if (!kAppend || h < p.Hq + p.Hkv)
-    return p.k + b * p.k_s[0] + s * p.k_s[1] + (h - p.Hq) * p.k_s[2];
-  return ap.v + s * ap.v_s[0] + (h - p.Hq - p.Hkv) * ap.v_s[1];
+                                                       const RowSource& r, int h) {
+  if (h < p.Hq) return r.q + h * p.q_s[2];
+  h -= p.Hq;
+  if (!kAppend || h < p.Hkv) return r.k + h * p.k_s[2];
+  return r.v + (h - p.Hkv) * ap.v_s[1];
 }
 
-// Where the head goes; null: it is not written.
 template <bool kAppend>
-__device__ __forceinline__ __nv_bfloat16* destination(const RopeArgs& p, const AppendArgs& ap,
-                                                      const RowInfo* info, int row, int h) {
-  if (kAppend && h >= p.Hq) {
-    if (info->slot < 0) return nullptr;
-    return h < p.Hq + p.Hkv ? ap.k_pages + info->slot + (h - p.Hq) * p.d
-                            : ap.v_pages + info->slot + (h - p.Hq - p.Hkv) * p.d;
-  }
-  if (kAppend && !info->live) return nullptr;
-  const int b = p.B > 1 ? row / p.S : 0;
-  const long long s = row - b * p.S;
-  if (h < p.Hq) return p.qo + b * p.qo_s[0] + s * p.qo_s[1] + h * p.qo_s[2];
-  return p.ko + b * p.ko_s[0] + s * p.ko_s[1] + (h - p.Hq) * p.ko_s[2];
+__device__ __forceinline__ __nv_bfloat16* target(const RopeArgs& p, const RowTarget& r, int h) {
+  if (h < p.Hq) return r.q == nullptr ? nullptr : r.q + h * p.qo_s[2];
+  h -= p.Hq;
+  if (!kAppend) return r.k + h * p.ko_s[2];
+  if (r.k == nullptr) return nullptr;
+  return h < p.Hkv ? r.k + h * p.d : r.v + (h - p.Hkv) * p.d;
 }
 
-// Positions (append: and cache slots) of the CTA's rows, then cos and sin of
-// their pairs: row r's cos at sm[2 r npairs + place(pair)], its sin npairs
-// further on.  The whole CTA calls it; the values may be read on return.
-template <bool kAppend, typename Place>
-__device__ __forceinline__ void form_angles(const RopeArgs& p, const AppendArgs& ap, int row0,
-                                            int nrows, float* sm, RowInfo* rows_s, Place place) {
-  const int tid = threadIdx.x;
-  const int npairs = p.rot >> 1;
+// Position (append: and cache slot) of a row; the whole warp calls it.
+template <bool kAppend>
+__device__ __forceinline__ RowInfo row_info(const RopeArgs& p, const AppendArgs& ap, int row) {
   if constexpr (kAppend) {
-    for (int r = tid >> 5; r < nrows; r += kThreads / 32) {
-      const RowInfo info = append_row(ap, row0 + r);
-      if ((tid & 31) == 0) rows_s[r] = info;
-    }
-    if (blockIdx.x == 0 && ap.cu_q != nullptr) {
-      // offsets that decrease or leave [0, total_q]
-      for (int i = tid; i <= ap.B; i += kThreads) {
-        const int c = __ldg(ap.cu_q + i);
-        const int next = i < ap.B ? __ldg(ap.cu_q + i + 1) : c;
-        if (c < 0 || c > ap.total_q || next < c) atomicOr(ap.status, kStatusBadInput);
-      }
-    }
-    __syncthreads();
+    return append_row(ap, row);
+  } else {
+    RowInfo r;
+    r.slot = -1;
+    r.live = 1;
+    r.pos = p.positions != nullptr ? __ldg(p.positions + row) : row % p.S;
+    return r;
   }
-  for (int e = tid; e < nrows * npairs; e += kThreads) {
-    const int r = e / npairs, pr = e - r * npairs;
-    const int row = row0 + r;
-    int pos;
-    if constexpr (kAppend)
-      pos = rows_s[r].pos;
-    else
-      pos = p.positions != nullptr ? __ldg(p.positions + row) : row % p.S;
-    float c, s;
-    angle(pos, __ldg(p.inv_freq + pr), p.amplitude, p.sign, &c, &s);
-    float* at = sm + 2 * r * npairs + place(pr);
-    at[0] = c;
-    at[npairs] = s;
+}
+
+// Offsets that decrease or leave [0, total_q] are reported; the whole grid
+// shares the list.
+__device__ __forceinline__ void check_offsets(const AppendArgs& ap) {
+  if (ap.cu_q == nullptr) return;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i <= ap.B;
+       i += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const int c = __ldg(ap.cu_q + i);
+    const int next = i < ap.B ? __ldg(ap.cu_q + i + 1) : c;
+    if (c < 0 || c > ap.total_q || next < c) atomicOr(ap.status, kStatusBadInput);
   }
-  __syncthreads();
 }
 
 // ---------------------------------------------------------------- the kernels
@@ -237,17 +255,19 @@ __device__ __forceinline__ void form_angles(const RopeArgs& p, const AppendArgs&
 template <int D, bool kAppend>
 __global__ void __launch_bounds__(kThreads)
     attn_rope_kernel(const __grid_constant__ RopeArgs p, const __grid_constant__ AppendArgs ap) {
-  constexpr int kUnits = D / 16;              // per head
-  constexpr int kStep = kThreads / kUnits;    // (row, head) pairs of one pass of the CTA
-  extern __shared__ __align__(16) float sm[];
-  __shared__ RowInfo rows_s[kAppend ? kMaxRowsPerCta : 1];
-  const int tid = threadIdx.x;
-  const int npairs = p.rot >> 1;
-  const int row0 = blockIdx.x * p.rows_per_cta;
-  const int nrows = min(p.rows_per_cta, p.rows - row0);
+  constexpr int kUnits = D / 16;       // per head
+  constexpr int kStep = 32 / kUnits;   // heads of one pass of the warp
+  __shared__ __align__(16) float sm[kThreads / 32][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if constexpr (kAppend) check_offsets(ap);
+  const int task = blockIdx.x * (kThreads / 32) + warp;
+  if (task >= p.tasks) return;
+  const int row = p.chunks > 1 ? task / p.chunks : task;
   const int H = p.Hq + p.Hkv + (kAppend ? p.Hkv : 0);
-  const int items = nrows * H;
-  const int j = tid & (kUnits - 1);
+  const int h0 = (task - row * p.chunks) * p.chunk_heads;
+  const int h1 = min(h0 + p.chunk_heads, H);
+  const int npairs = p.rot >> 1;
+  const int j = lane & (kUnits - 1);
   const bool turn = j < (p.rot >> 4);
   const bool skip = !turn && p.in_place;  // passed through, and already there
   // offsets of the unit's two vectors inside a head
@@ -256,117 +276,137 @@ __global__ void __launch_bounds__(kThreads)
     va = j * 8;
     vb = npairs + j * 8;
   }
+  const RowSource from = row_source<kAppend>(p, ap, row);
   uint4 xa[kBatch], xb[kBatch];
-  auto load = [&](int first) {
+  const int first = h0 + lane / kUnits;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int item = first + i * kStep;
-      if (item < items && !skip) {
-        const int r = item / H;
-        const __nv_bfloat16* src = source<kAppend>(p, ap, row0 + r, item - r * H);
-        xa[i] = ld16(src + va);
-        xb[i] = ld16(src + vb);
+  for (int i = 0; i < kBatch; ++i) {
+    const int h = first + i * kStep;
+    if (h < h1 && !skip) {
+      const __nv_bfloat16* src = source<kAppend>(p, ap, from, h);
+      xa[i] = ld16(src + va);
+      xb[i] = ld16(src + vb);
+    }
+  }
+
+  const RowInfo info = row_info<kAppend>(p, ap, row);
+  for (int pr = lane; pr < npairs; pr += 32) {
+    float c, s;
+    angle(info.pos, __ldg(p.inv_freq + pr), p.amplitude, p.sign, &c, &s);
+    sm[warp][pair_slot(pr, npairs)] = c;
+    sm[warp][npairs + pair_slot(pr, npairs)] = s;
+  }
+  __syncwarp();
+  float c[8], s[8];
+  if (turn) {
+    const float* cs = &sm[warp][j * 4];
+    *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(cs);
+    *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(cs + (npairs >> 1));
+    *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(cs + npairs);
+    *reinterpret_cast<float4*>(s + 4) =
+        *reinterpret_cast<const float4*>(cs + npairs + (npairs >> 1));
+  }
+  const RowTarget to = row_target<kAppend>(p, ap, info, row);
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    const int h = first + i * kStep;
+    if (h < h1 && !skip) {
+      __nv_bfloat16* dst = target<kAppend>(p, to, h);
+      if (turn && (!kAppend || h < p.Hq + p.Hkv)) {
+        if (p.interleaved) {
+          rotate_words(xa[i], c, s);
+          rotate_words(xb[i], c + 4, s + 4);
+        } else {
+          rotate_half(xa[i], xb[i], c, s);
+        }
+      }
+      if (!kAppend || dst != nullptr) {
+        st16(dst + va, xa[i]);
+        st16(dst + vb, xb[i]);
       }
     }
-  };
-  int it = tid / kUnits;
-  load(it);
-  form_angles<kAppend>(p, ap, row0, nrows, sm, rows_s,
-                       [=](int pr) { return pair_slot(pr, npairs); });
-  while (true) {
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int item = it + i * kStep;
-      if (item < items && !skip) {
-        const int r = item / H, h = item - r * H;
-        __nv_bfloat16* dst = destination<kAppend>(p, ap, rows_s + (kAppend ? r : 0), row0 + r, h);
-        if (turn && (!kAppend || h < p.Hq + p.Hkv)) {
-          float c[8], s[8];
-          const float* cs = sm + 2 * r * npairs + j * 4;
-          *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(cs);
-          *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(cs + (npairs >> 1));
-          *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(cs + npairs);
-          *reinterpret_cast<float4*>(s + 4) =
-              *reinterpret_cast<const float4*>(cs + npairs + (npairs >> 1));
-          if (p.interleaved) {
-            rotate_words(xa[i], c, s);
-            rotate_words(xb[i], c + 4, s + 4);
-          } else {
-            rotate_half(xa[i], xb[i], c, s);
-          }
-        }
-        if (dst != nullptr) {
-          st16(dst + va, xa[i]);
-          st16(dst + vb, xb[i]);
-        }
-      }
-    }
-    it += kBatch * kStep;
-    if (it >= items) break;
-    load(it);
   }
 }
 
 // Any even rot: one pair per thread, 2-byte loads and stores.  Vectors of
-// eight would straddle the middle of the rotated part.
+// eight would straddle the middle of the rotated part.  A warp takes one row.
 template <bool kAppend>
 __global__ void __launch_bounds__(kThreads)
     attn_rope_pairs_kernel(const __grid_constant__ RopeArgs p,
                            const __grid_constant__ AppendArgs ap) {
-  extern __shared__ __align__(16) float sm[];
-  __shared__ RowInfo rows_s[kAppend ? kMaxRowsPerCta : 1];
+  __shared__ float sm[kThreads / 32][256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if constexpr (kAppend) check_offsets(ap);
+  const int row = blockIdx.x * (kThreads / 32) + warp;
+  if (row >= p.rows) return;
   const int npairs = p.rot >> 1;
-  const int row0 = blockIdx.x * p.rows_per_cta;
-  const int nrows = min(p.rows_per_cta, p.rows - row0);
+  const RowInfo info = row_info<kAppend>(p, ap, row);
+  for (int pr = lane; pr < npairs; pr += 32)
+    angle(info.pos, __ldg(p.inv_freq + pr), p.amplitude, p.sign, &sm[warp][pr],
+          &sm[warp][npairs + pr]);
+  __syncwarp();
+  const RowSource from = row_source<kAppend>(p, ap, row);
+  const RowTarget to = row_target<kAppend>(p, ap, info, row);
   const int H = p.Hq + p.Hkv + (kAppend ? p.Hkv : 0);
-  form_angles<kAppend>(p, ap, row0, nrows, sm, rows_s, [](int pr) { return pr; });
   const int half = p.d >> 1;  // pairs of a head, the passed-through ones included
-  for (long long u = threadIdx.x; u < static_cast<long long>(nrows) * H * half; u += kThreads) {
-    const int item = static_cast<int>(u / half), pr = static_cast<int>(u - (long long)item * half);
-    const int r = item / H, h = item - r * H;
-    const bool turn = pr < npairs && (!kAppend || h < p.Hq + p.Hkv);
-    const bool split = pr < npairs && !p.interleaved;
-    const int a = split ? pr : 2 * pr, b = split ? pr + npairs : 2 * pr + 1;
-    const __nv_bfloat16* src = source<kAppend>(p, ap, row0 + r, h);
-    __nv_bfloat16* dst = destination<kAppend>(p, ap, rows_s + (kAppend ? r : 0), row0 + r, h);
-    if (dst == nullptr) continue;
-    __nv_bfloat16 x = src[a], y = src[b];
-    if (turn) {
-      const float c = sm[2 * r * npairs + pr], s = sm[2 * r * npairs + npairs + pr];
-      const float fx = __bfloat162float(x), fy = __bfloat162float(y);
-      x = __float2bfloat16_rn(fx * c - fy * s);
-      y = __float2bfloat16_rn(fx * s + fy * c);
+  for (int h = 0; h < H; ++h) {
+    const __nv_bfloat16* src = source<kAppend>(p, ap, from, h);
+    __nv_bfloat16* dst = target<kAppend>(p, to, h);
+    if (kAppend && dst == nullptr) continue;
+    const bool rotates = !kAppend || h < p.Hq + p.Hkv;
+    for (int pr = lane; pr < half; pr += 32) {
+      const bool split = pr < npairs && !p.interleaved;
+      const int a = split ? pr : 2 * pr, b = split ? pr + npairs : 2 * pr + 1;
+      __nv_bfloat16 x = src[a], y = src[b];
+      if (pr < npairs && rotates) {
+        const float c = sm[warp][pr], s = sm[warp][npairs + pr];
+        const float fx = __bfloat162float(x), fy = __bfloat162float(y);
+        x = __float2bfloat16_rn(fx * c - fy * s);
+        y = __float2bfloat16_rn(fx * s + fy * c);
+      }
+      dst[a] = x;
+      dst[b] = y;
     }
-    dst[a] = x;
-    dst[b] = y;
   }
 }
 
-template <bool kAppend>
-cudaError_t launch(RopeArgs p, const AppendArgs& ap, int num_sms, cudaStream_t stream) {
+template <int D, bool kAppend>
+cudaError_t launch_units(RopeArgs p, const AppendArgs& ap, int num_sms, cudaStream_t stream) {
+  constexpr int kStep = 32 / (D / 16);
   const int H = p.Hq + p.Hkv + (kAppend ? p.Hkv : 0);
-  if (p.rows == 0 || H == 0) return cudaSuccess;
-  // Rows of a CTA: one batch of units for every thread where there are rows
-  // enough for two CTAs on every SM, fewer where there are not (a decode step
-  // has one row per CTA).
-  const int units = H * (p.d / 16);
-  const int full = (kBatch * kThreads + units - 1) / units;
-  const int spread = (p.rows + 2 * num_sms - 1) / (2 * num_sms);
-  const int rows = full < spread ? full : spread;
-  p.rows_per_cta = rows < 1 ? 1 : rows > kMaxRowsPerCta ? kMaxRowsPerCta : rows;
-  const dim3 grid((p.rows + p.rows_per_cta - 1) / p.rows_per_cta);
-  const size_t smem = static_cast<size_t>(p.rows_per_cta) * p.rot * sizeof(float);
-  if (p.rot % 16 != 0)
-    attn_rope_pairs_kernel<kAppend><<<grid, kThreads, smem, stream>>>(p, ap);
-  else if (p.d == 64)
-    attn_rope_kernel<64, kAppend><<<grid, kThreads, smem, stream>>>(p, ap);
-  else if (p.d == 128)
-    attn_rope_kernel<128, kAppend><<<grid, kThreads, smem, stream>>>(p, ap);
-  else if (p.d == 256)
-    attn_rope_kernel<256, kAppend><<<grid, kThreads, smem, stream>>>(p, ap);
-  else
-    return cudaErrorInvalidValue;
+  // A row's heads are dealt to as many warps as give each one batch of loads,
+  // and to more, down to one pass each, while that leaves fewer than
+  // kWarpsPerSm warps for every SM.
+  const int passes = (H + kStep - 1) / kStep;
+  const long long want = static_cast<long long>(num_sms) * kWarpsPerSm;
+  long long chunks = (want + p.rows - 1) / p.rows;
+  const int least = (passes + kBatch - 1) / kBatch;
+  chunks = chunks < least ? least : chunks > passes ? passes : chunks;
+  p.chunk_heads = static_cast<int>((passes + chunks - 1) / chunks) * kStep;
+  p.chunks = (H + p.chunk_heads - 1) / p.chunk_heads;
+  const long long tasks = static_cast<long long>(p.rows) * p.chunks;
+  if (tasks > INT32_MAX - kThreads) return cudaErrorInvalidValue;
+  p.tasks = static_cast<int>(tasks);
+  constexpr int kWarps = kThreads / 32;
+  attn_rope_kernel<D, kAppend>
+      <<<(p.tasks + kWarps - 1) / kWarps, kThreads, 0, stream>>>(p, ap);
   return cudaGetLastError();
+}
+
+template <bool kAppend>
+cudaError_t launch(const RopeArgs& p, const AppendArgs& ap, int num_sms, cudaStream_t stream) {
+  if (p.rows == 0 || p.Hq + p.Hkv == 0) return cudaSuccess;
+  if (p.rot % 16 != 0) {
+    constexpr int kWarps = kThreads / 32;
+    attn_rope_pairs_kernel<kAppend>
+        <<<static_cast<unsigned>((static_cast<long long>(p.rows) + kWarps - 1) / kWarps), kThreads,
+           0, stream>>>(p, ap);
+    return cudaGetLastError();
+  }
+  if (p.d == 64) return launch_units<64, kAppend>(p, ap, num_sms, stream);
+  if (p.d == 128) return launch_units<128, kAppend>(p, ap, num_sms, stream);
+  if (p.d == 256) return launch_units<256, kAppend>(p, ap, num_sms, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace

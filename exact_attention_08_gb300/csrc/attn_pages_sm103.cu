@@ -573,7 +573,7 @@ cudaError_t launch_finish(const PagesArgs& a, long long most_copies, int rows,
   const long long items =
       most_copies * 2 * a.layers * ((a.page_vecs + kPiece - 1) / kPiece);
   long long grid = items > rows ? items : rows;
-  const long long most = 4ll * a.num_sms;
+  const long long most = 8ll * a.num_sms;
   if (grid > most) grid = most;
   if (grid < 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};

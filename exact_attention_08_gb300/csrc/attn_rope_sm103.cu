@@ -11,9 +11,9 @@
 // Angles.  p f in fp32 loses the angle of a far position (at p = 10^6 an
 // fp32 angle is off by 0.06 rad), so f arrives in fp64 and becomes a 64-bit
 // fraction of a turn, f / 2 pi mod 1 in units of 2^-64; an integer product
-// with p then drops whole turns exactly.  The error is p 2^-53 of f / 2 pi:
-// below 10^-9 of a turn up to p = 2^23, 1e-7 at p = 2^31.  The top 32 bits
-// of the fraction, as half turns in [-1, 1), go through sincospif in fp32.
+// with p then drops whole turns exactly.  That costs less than p 2^-63 of a
+// turn for f <= 1: 3e-10 at p = 2^31.  The top 32 bits of the fraction, as
+// half turns in [-1, 1), go through sincospif in fp32.
 // Products and sums are fp32 and are rounded once, to bf16.
 //
 // Layout.  A block takes a row (token), each of its warps up to 12 heads (at
@@ -23,6 +23,14 @@
 // lane's unit is eight pairs, two 16-byte loads and two 16-byte stores; all
 // its loads are issued before the angles are formed, which hides the
 // position's and frequencies' latency.
+//
+// Bound: bytes.  Measured (one GB300, device time of a call in a graph): q, k
+// of 2 x 4096 rows, 32 + 8 heads, d = 128, 167.8 MB moved: 27.9 us, 6.0 TB/s,
+// 90 % of a copy's measured rate (a copy of those bytes takes 26.4 us); 8192
+// rows, 16 + 16 heads, 134.3 MB: 20.3 us (copy 21.5).  On the first, fp64
+// angles took 28.4 us, warps that each formed the angles of their own heads
+// 31.1 us, a block for three rows with a division per unit 33.3 us; packed
+// fp32 instructions 28.8 us (more registers, fewer blocks on an SM).
 #include "attn_internal.h"
 #include "sm103_ptx.cuh"
 
@@ -42,11 +50,21 @@ struct RowInfo {
   int live;        // 0: the row belongs to no sequence (nothing is written)
 };
 
-// f (radians per position) as a fraction of a turn in units of 2^-64.
+// f (radians per position) as a fraction of a turn in units of 2^-64, whole
+// turns dropped.  With |f| = M 2^(E - 1086), M its 53 significant bits moved
+// to the top of 64 and E the biased exponent, f / 2 pi in those units is
+// M K 2^(E - 1088) for K = 2^66 / 2 pi: one high product and a shift.  In
+// integers because this GPU's fp64 rate is low.
 __device__ __forceinline__ uint64_t turn_fraction(double f) {
-  double t = f * 0.15915494309189533577;  // 1 / (2 pi)
-  t -= floor(t);
-  return __double2ull_rz(t * 18446744073709551616.0);
+  const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(f));
+  const int e = static_cast<int>(bits >> 52 & 0x7ff);
+  const uint64_t m = (bits << 11) | (1ull << 63);
+  const uint64_t hi = __umul64hi(m, 0xA2F9836E4E441529ull);
+  const int up = e - 1024;
+  uint64_t r = 0;  // below 2^-64 of a turn (and zero), or all whole turns
+  if (up <= 0 && up > -64) r = hi >> -up;
+  if (up > 0 && up < 64) r = hi << up;
+  return bits >> 63 ? 0 - r : r;
 }
 
 // cos and sin of the angle of position pos, times the amplitude; the

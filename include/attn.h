@@ -468,9 +468,11 @@ ATTN_API int attn_append_paged(const void* q, const void* k, const void* v, void
  *     entries from there on are neither read nor, except to add pages, written.
  *   refs [num_pages_total] DEVICE int32: in how many of those entries page p
  *     stands (plus holds of the caller's own, if any).  refs[p] <= 0: page p is
- *     free.  A fresh cache has refs, seqlens 0.  The calls keep refs in step
- *     with the table; a table and refs that disagree give undefined contents,
- *     never an access outside the buffers.
+ *     free.  A fresh cache has refs and seqlens 0 and pools of finite values
+ *     (zeros): an added page keeps what it held until attn_append_paged fills
+ *     its slots, and the attention calls read a last page whole.  The calls
+ *     keep refs in step with the table; a table and refs that disagree give
+ *     undefined contents, never an access outside the buffers.
  *   k_pages, v_pages: the pools of `layers` layers that share the table,
  *     [layers, num_pages_total, 16, Hkv, d] bf16 (layer l's pool is what the
  *     attention calls take).

@@ -137,13 +137,16 @@ def _check(rc: int, what: str) -> None:
         raise AttnError(rc, what)
 
 
-_torch_module = None
+_torch_module = _current_device = _raw_stream = None
 
 
 def _torch():
-    global _torch_module
+    """torch, imported on first use (with the two calls that every launch makes of it)."""
+    global _torch_module, _current_device, _raw_stream
     if _torch_module is None:
         import torch
+        _current_device = torch._C._cuda_getDevice
+        _raw_stream = torch._C._cuda_getCurrentRawStream
         _torch_module = torch
     return _torch_module
 
@@ -565,20 +568,11 @@ class _Call:
             c.__exit__(*exc)
 
 
-def _elsewhere(index, stream):
-    """Whether a call has to switch to another device or stream first."""
-    return stream is not None or index != _torch()._C._cuda_getDevice()
-
-
-def _raw_stream(index):
-    return _torch()._C._cuda_getCurrentRawStream(index)
-
-
 def _rows_tensor(t, name, dims, index):
     """bf16 on device `index`, `dims` dimensions, the last one contiguous."""
     torch = _torch()
-    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() in dims and \
-            index >= 0 and t.get_device() == index and (t.is_contiguous() or t.stride(-1) == 1):
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == index and \
+            index >= 0 and t.dim() in dims and (t.is_contiguous() or t.stride(-1) == 1):
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -617,10 +611,20 @@ def _frequencies(inv_freq, d, index):
     return rot
 
 
+def _output(out, t, name):
+    """`out` if it is a fit output for t, or a new one with t's layout."""
+    if out is None:
+        return _torch_module.empty_like(t)
+    _rows_tensor(out, name + "_out", (t.dim(),), t.get_device())
+    if out.shape != t.shape:
+        raise ValueError(f"{name}_out must be shaped like {name}")
+    return out
+
+
 def _strides(t, n):
     """{[batch,] row, head} strides as a C array of n, or None if t is contiguous.  Packed
     rows have no batch stride."""
-    if t is None or t.is_contiguous():
+    if t.is_contiguous():
         return None
     st = t.stride()[:-1]
     return (ctypes.c_longlong * n)(*(st if len(st) == n else (0, *st)))
@@ -688,29 +692,23 @@ def _rope(fn, what, names, q, k, inv_freq, positions, interleaved, amplitude, q_
         _int_tensor(positions, "positions", index)
         if positions.numel() != B * S:
             raise ValueError(f"positions must hold {B * S} values")
-    if _elsewhere(index, stream):
+    if stream is not None or index != _current_device():
         with _Call(index, stream):
             return _rope(fn, what, names, q, k, inv_freq, positions, interleaved, amplitude,
                          q_out, k_out, None)
-    for t, o, n in ((q, q_out, names[0]), (k, k_out, names[1])):
-        if t is not None and o is not None:
-            _rows_tensor(o, n + "_out", (len(shape),), index)
-            if o.shape != t.shape:
-                raise ValueError(f"{n}_out must be shaped like {n}")
-    if q is None:
-        q_out = None
-    elif q_out is None:
-        q_out = torch.empty_like(q)
-    if k is None:
-        k_out = None
-    elif k_out is None:
-        k_out = torch.empty_like(k)
-    rc = fn(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(positions), inv_freq.data_ptr(), B, S,
-            Hq, Hkv, d, rot, 1 if interleaved else 0, amplitude, _strides(q, 3), _strides(k, 3),
-            _strides(q_out, 3), _strides(k_out, 3), _raw_stream(index))
+    qp = kp = qo = ko = sq = sk = sqo = sko = None
+    if q is not None:
+        q_out = _output(q_out, q, names[0])
+        qp, qo, sq, sqo = q.data_ptr(), q_out.data_ptr(), _strides(q, 3), _strides(q_out, 3)
+    if k is not None:
+        k_out = _output(k_out, k, names[1])
+        kp, ko, sk, sko = k.data_ptr(), k_out.data_ptr(), _strides(k, 3), _strides(k_out, 3)
+    rc = fn(qp, kp, qo, ko, None if positions is None else positions.data_ptr(),
+            inv_freq.data_ptr(), B, S, Hq, Hkv, d, rot, 1 if interleaved else 0, amplitude, sq, sk,
+            sqo, sko, _raw_stream(index))
     if rc != ATTN_OK:
         raise AttnError(rc, what)
-    return q_out, k_out
+    return q_out if q is not None else None, k_out if k is not None else None
 
 
 def attn_append_paged(q, k, v, k_pages, v_pages, page_table, seqlens_k, cu_seqlens_q=None,
@@ -748,27 +746,23 @@ def attn_append_paged(q, k, v, k_pages, v_pages, page_table, seqlens_k, cu_seqle
         if Tq != T or dq != d:
             raise ValueError("q and k shapes disagree")
     rot = 0 if inv_freq is None else _frequencies(inv_freq, d, index)
-    if _elsewhere(index, stream):
+    if stream is not None or index != _current_device():
         with _Call(index, stream):
             return attn_append_paged(q, k, v, k_pages, v_pages, page_table, seqlens_k,
                                      cu_seqlens_q, inv_freq, interleaved=interleaved,
                                      amplitude=amplitude, q_out=q_out)
-    if q is None:
-        q_out = None
-    elif q_out is None:
-        q_out = torch.empty_like(q)
-    else:
-        _rows_tensor(q_out, "q_out", (3,), index)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must be shaped like q")
+    qp = qo = sq = sqo = None
+    if q is not None:
+        q_out = _output(q_out, q, "q")
+        qp, qo, sq, sqo = q.data_ptr(), q_out.data_ptr(), _strides(q, 2), _strides(q_out, 2)
     rc = lib.attn_append_paged(
-        _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), k_pages.data_ptr(), v_pages.data_ptr(),
+        qp, k.data_ptr(), v.data_ptr(), qo, k_pages.data_ptr(), v_pages.data_ptr(),
         page_table.data_ptr(), _ptr(cu_seqlens_q), seqlens_k.data_ptr(), _ptr(inv_freq), B, Hq,
-        Hkv, T, d, rot, 1 if interleaved else 0, amplitude, page, page_table.shape[1], P,
-        _strides(q, 2), _strides(k, 2), _strides(v, 2), _strides(q_out, 2), _raw_stream(index))
+        Hkv, T, d, rot, 1 if interleaved else 0, amplitude, page, page_table.shape[1], P, sq,
+        _strides(k, 2), _strides(v, 2), sqo, _raw_stream(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_append_paged")
-    return q_out
+    return q_out if q is not None else None
 
 
 @functools.lru_cache(maxsize=256)
@@ -829,7 +823,7 @@ def attn_pages_resize(page_table, seqlens, new_seqlens, refs, k_pages=None, v_pa
         if k_pages is None or v_pages is None:
             raise ValueError("k_pages and v_pages must both be given, or neither")
         layers, page, Hkv, d = _cache_pools(k_pages, v_pages, P, index)
-    if _elsewhere(index, stream):
+    if stream is not None or index != _current_device():
         with _Call(index, stream):
             return attn_pages_resize(page_table, seqlens, new_seqlens, refs, k_pages, v_pages,
                                      workspace=workspace)
@@ -852,7 +846,7 @@ def attn_pages_fork(page_table, seqlens, refs, src, dst, k_pages, v_pages, *, wo
     _int_vector(src, "src", n, index)
     _int_vector(dst, "dst", n, index)
     layers, page, Hkv, d = _cache_pools(k_pages, v_pages, P, index)
-    if _elsewhere(index, stream):
+    if stream is not None or index != _current_device():
         with _Call(index, stream):
             return attn_pages_fork(page_table, seqlens, refs, src, dst, k_pages, v_pages,
                                    workspace=workspace)
@@ -872,7 +866,7 @@ def attn_pages_compact(page_table, seqlens, refs, k_pages, v_pages, *, workspace
     page is now (-1: free) and how many are live."""
     index, B, W, P = _cache_tables(page_table, seqlens, refs)
     layers, page, Hkv, d = _cache_pools(k_pages, v_pages, P, index)
-    if _elsewhere(index, stream):
+    if stream is not None or index != _current_device():
         with _Call(index, stream):
             return attn_pages_compact(page_table, seqlens, refs, k_pages, v_pages,
                                       workspace=workspace)

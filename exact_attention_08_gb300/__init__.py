@@ -730,6 +730,7 @@ def attn_append_paged(q, k, v, k_pages, v_pages, page_table, seqlens_k, cu_seqle
         raise ValueError("k, v, k_pages and v_pages shapes disagree")
     if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
         raise ValueError("k_pages and v_pages must be contiguous")
+    _int_tensor(seqlens_k, "seqlens_k", index)
     B = seqlens_k.numel()
     _int_vector(seqlens_k, "seqlens_k", B, index)
     _int_tensor(page_table, "page_table", index)
@@ -803,7 +804,8 @@ def _workspace(workspace, rows, pages, refs):
     if workspace is None:
         return torch.empty(attn_pages_workspace_size(rows, pages), dtype=torch.uint8,
                            device=refs.device)
-    if workspace.get_device() != refs.get_device() or not workspace.is_contiguous():
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or \
+            workspace.get_device() != refs.get_device():
         raise ValueError(f"workspace must be a contiguous tensor on {refs.device}")
     return workspace
 
@@ -842,6 +844,7 @@ def attn_pages_fork(page_table, seqlens, refs, src, dst, k_pages, v_pages, *, wo
     a last page that is not full copied in every layer.  Rows dst must be empty
     (length 0).  Other arguments as attn_pages_resize's."""
     index, B, W, P = _cache_tables(page_table, seqlens, refs)
+    _int_tensor(src, "src", index)
     n = src.numel()
     _int_vector(src, "src", n, index)
     _int_vector(dst, "dst", n, index)

@@ -13,6 +13,9 @@ using namespace attn;
 
 namespace {
 
+// Rows of one call: their numbers stay clear of 2^31 in every index sum.
+constexpr int kMaxRows = INT32_MAX - 1024;
+
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // One tensor's strides: what the caller gave, or the contiguous ones.  A
@@ -62,7 +65,7 @@ int rope_impl(const void* q, const void* k, void* q_out, void* k_out, const int*
   int rc = check_rotation(d, rotary_dim, interleaved, amplitude, inv_freq);
   if (rc != ATTN_OK) return rc;
   const long long rows = static_cast<long long>(B) * S;
-  if (rows > INT32_MAX) return set_error(ATTN_ERR_INVALID_ARG, "B * S does not fit 31 bits");
+  if (rows > kMaxRows) return set_error(ATTN_ERR_INVALID_ARG, "%lld rows are too many", rows);
   if (Hq > (1 << 20) || Hkv > (1 << 20))
     return set_error(ATTN_ERR_INVALID_ARG, "more than 2^20 heads");
   if (rows == 0 || Hq + Hkv == 0) return ATTN_OK;
@@ -238,6 +241,8 @@ ATTN_API int attn_append_paged(const void* q, const void* k, const void* v, void
     return set_error(ATTN_ERR_INVALID_ARG, "max_pages_per_seq too large");
   if (Hq > (1 << 20) || Hkv > (1 << 20))
     return set_error(ATTN_ERR_INVALID_ARG, "more than 2^20 heads");
+  if (total_q > kMaxRows)
+    return set_error(ATTN_ERR_INVALID_ARG, "%d rows are too many", total_q);
   if (cu_seqlens_q == nullptr && total_q != B)
     return set_error(ATTN_ERR_INVALID_ARG,
                      "without cu_seqlens_q every sequence has one new token (total_q=%d, B=%d)",

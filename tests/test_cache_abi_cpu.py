@@ -28,6 +28,7 @@ ROPE = dict(q=0, k=0, qo=0, ko=0, pos=0, inv=0, B=1, S=4, Hq=2, Hkv=2, d=128, ro
     (dict(amp=math.inf), "INVALID_ARG"), (dict(amp=math.nan), "INVALID_ARG"),
     (dict(inv=None), "INVALID_ARG"), (dict(q=None), "INVALID_ARG"), (dict(ko=None), "INVALID_ARG"),
     (dict(B=-1), "INVALID_ARG"), (dict(B=1 << 20, S=1 << 20), "INVALID_ARG"),
+    (dict(B=1, S=2 ** 31 - 1), "INVALID_ARG"), (dict(Hq=(1 << 20) + 1), "INVALID_ARG"),
     (dict(q=2), "INVALID_ARG"), (dict(inv=4), "INVALID_ARG"), (dict(pos=1), "INVALID_ARG"),
     (dict(qs=(1024, 260, 128)), "INVALID_ARG"), (dict(ks=(1024, -256, 128)), "INVALID_ARG"),
     (dict(kos=(1024, 0, 128)), "INVALID_ARG"),
@@ -58,7 +59,7 @@ APPEND = dict(q=0, k=0, v=0, qo=0, kp=0, vp=0, pt=0, cu=None, ln=0, inv=0, B=2, 
     (dict(rot=129), "INVALID_ARG"), (dict(inv=None), "INVALID_ARG"), (dict(v=None), "INVALID_ARG"),
     (dict(qo=None), "INVALID_ARG"), (dict(pt=None), "INVALID_ARG"), (dict(ln=None), "INVALID_ARG"),
     (dict(vs=(250, 128)), "INVALID_ARG"), (dict(qos=(0, 128)), "INVALID_ARG"),
-    (dict(B=0, T=0), "OK"),
+    (dict(B=0, T=0), "OK"), (dict(B=2 ** 31 - 1, T=2 ** 31 - 1), "INVALID_ARG"),
 ])
 def test_append_arguments(change, status):
     buf, p = _ptr()

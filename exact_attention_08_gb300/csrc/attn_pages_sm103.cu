@@ -20,12 +20,14 @@
 // Ranking.  Each warp of the cluster owns a run of pages and turns its
 // refs into one bit per page by ballots kept in shared memory; popcounts
 // summed over warps and CTAs give every page its rank among the free (or
-// live) ones without reading refs a second time.
+// live) ones without reading refs a second time.  A release that leaves a
+// page unheld clears its bit where it stands, in another CTA if need be.
 //
 // Measured (one GB300, device time in a graph).  The bookkeeping kernel is a
 // chain of dependent reads and three or four cluster barriers, bound by their
-// latency: 6.6 us for a decode step of 64 rows over 65,536 pages, launch
-// included.  The finishing kernel is bound by bytes: a compaction of 16,384
+// latency: 6.0 us for a decode step of 64 rows over 65,792 pages, launch
+// included (6.6 with refs read after the releases instead of before, when
+// their latency hides behind the rows').  The finishing kernel is bound by bytes: a compaction of 16,384
 // pages that moves 3,932 of 64 KB (515 MB read and written) takes 85.8 us in
 // all, 90 % of a copy's measured rate (8 blocks an SM; 4 took 91 us).
 #include "attn_internal.h"
@@ -71,8 +73,15 @@ __device__ __forceinline__ int cta_rank() {
 
 // Barrier of all threads of the cluster: what any of them wrote before it,
 // all of them see after it (global data is read back through L2, __ldcg).
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 
 // Stores v at the same shared variable of CTA `rank` of the cluster.
@@ -170,6 +179,19 @@ __device__ __forceinline__ int live_bits(const PagesArgs& a, const Run& r, uint3
   return live;
 }
 
+// Clears a page's bit in the CTA whose run it is in.
+__device__ __forceinline__ void clear_bit(int num_pages, uint32_t* bits, int page) {
+  const int per = (((num_pages + 31) >> 5) + kCtas - 1) / kCtas;
+  const int word = page >> 5, owner = word / per;
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(at)
+               : "r"(ptx::smem_addr(bits + (word - owner * per))), "r"(owner));
+  asm volatile("red.relaxed.cluster.shared::cluster.and.b32 [%0], %1;" ::"r"(at),
+               "r"(~(1u << (page & 31)))
+               : "memory");
+}
+
 // Turns per-warp counts into each warp's offset inside the CTA and tells
 // every CTA of the cluster the CTA's total.
 __device__ __forceinline__ void share_counts(Shared& sh, int cta, int warp_count) {
@@ -231,7 +253,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
   if (tid == 0) sh.rows = 0;
   __syncthreads();
 
-  // 1. pages past a row's new end are given back
+  // 1. pages past a row's new end are given back, and cleared in the bits of
+  // the live pages, which are taken before, where nobody holds them any more
+  const Run r = page_run(a.num_pages, cta, warp);
   if (mine) {
     old = __ldcg(a.seqlens + b);
     n = __ldg(a.new_seqlens + b);
@@ -245,16 +269,17 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
       sh.row[atomicAdd(&sh.rows, 1)] = tid;
     }
   }
-  __syncthreads();
+  live_bits(a, r, bits, 1);
+  cluster_sync();
   for (int i = warp; i < sh.rows; i += kWarps) {
     const int t = sh.row[i];
     const int* row = a.page_table + static_cast<size_t>(cta * per + t) * a.max_pages;
     for (int j = sh.from[t] + lane; j < sh.to[t]; j += 32) {
       const int page = __ldcg(row + j);
-      if (in_pool(a, page))
-        atomicSub(a.refs + page, 1);
-      else
+      if (!in_pool(a, page))
         atomicOr(a.status, kStatusBadInput);
+      else if (atomicSub(a.refs + page, 1) == 1)
+        clear_bit(a.num_pages, bits, page);
     }
   }
   cluster_sync();
@@ -263,8 +288,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
   // it grows by, and for one more where it grows inside a last page that
   // another row holds too: that page is copied before it is written.
   if (tid == 0) sh.rows = 0;
-  const Run r = page_run(a.num_pages, cta, warp);
-  const int live = live_bits(a, r, bits, 1);
+  int live = 0;
+  for (int w = r.w0 + lane; w < r.w1; w += 32) live += __popc(bits[w]);
+  live = __reduce_add_sync(0xffffffffu, live);
   int need = 0, last = -1;
   bool split = false;
   if (ok && n > old) {
@@ -435,9 +461,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = cta_rank();
   if (tid == 0) sh.holes = 0;
+  cluster_arrive();
   const Run r = page_run(a.num_pages, cta, warp);
   const int live_count = live_bits(a, r, bits, 0);
-  cluster_sync();  // every CTA runs before any writes into another's shared memory
+  cluster_wait();  // every CTA runs before any writes into another's shared memory
   share_counts(sh, cta, live_count);
   cluster_sync();
 

@@ -42,6 +42,17 @@ CASES = [
 ]
 
 
+def random_rope(seed):
+    g = np.random.default_rng(100 + seed)
+    d = int(g.choice([64, 128, 256]))
+    rot = int(g.choice([d, d // 2, 16, 2 * int(g.integers(0, d // 2 + 1))]))
+    return (int(g.integers(1, 4)), int(g.integers(1, 200)), int(g.integers(1, 50)),
+            int(g.integers(1, 20)), d, rot, bool(g.random() < 0.5), float(g.choice([1.0, -0.5, 2])))
+
+
+CASES += [random_rope(seed) for seed in range(10)]
+
+
 @pytest.mark.parametrize("case", CASES, ids=str)
 @pytest.mark.parametrize("fn,sign", [(ea.attn_rope, 1.0), (ea.attn_rope_bwd, -1.0)])
 def test_rope(case, fn, sign):
@@ -189,6 +200,20 @@ APPENDS = [
     (6, 3, 64, 64, False, list(range(1, 71)), [1 + i % 5 for i in range(70)]),
     (1, 1, 64, 64, False, [0] * 1500 + [3], [0] * 1500 + [3]),
 ]
+
+
+def random_append(seed):
+    g = np.random.default_rng(seed)
+    Hkv = int(g.integers(1, 9))
+    d = int(g.choice([64, 128, 256]))
+    B = int(g.integers(1, 40))
+    new = None if g.random() < 0.4 else [int(v) for v in g.integers(0, 30, B)]
+    ln = [int(g.integers(0, 90)) for _ in range(B)]
+    rot = int(g.choice([d, d // 2, 16, 2 * int(g.integers(1, d // 2 + 1))]))
+    return Hkv * int(g.integers(1, 7)), Hkv, d, rot, bool(g.random() < 0.5), ln, new
+
+
+APPENDS += [random_append(seed) for seed in range(16)]
 
 
 @pytest.mark.parametrize("case", APPENDS, ids=lambda c: str(c)[:60])

@@ -614,7 +614,11 @@ def _frequencies(inv_freq, d, index):
 def _output(out, t, name):
     """`out` if it is a fit output for t, or a new one with t's layout."""
     if out is None:
-        return _torch_module.empty_like(t)
+        out = _torch_module.empty_like(t)
+        # a broadcast t leaves the order of the new strides to torch
+        if out.is_contiguous() or out.stride(-1) == 1:
+            return out
+        return _torch_module.empty(t.shape, dtype=t.dtype, device=t.device)
     _rows_tensor(out, name + "_out", (t.dim(),), t.get_device())
     if out.shape != t.shape:
         raise ValueError(f"{name}_out must be shaped like {name}")

@@ -241,8 +241,8 @@ ATTN_API int attn_append_paged(const void* q, const void* k, const void* v, void
     return set_error(ATTN_ERR_INVALID_ARG, "max_pages_per_seq too large");
   if (Hq > (1 << 20) || Hkv > (1 << 20))
     return set_error(ATTN_ERR_INVALID_ARG, "more than 2^20 heads");
-  if (total_q > kMaxRows)
-    return set_error(ATTN_ERR_INVALID_ARG, "%d rows are too many", total_q);
+  if (total_q > kMaxRows || B > kMaxRows)
+    return set_error(ATTN_ERR_INVALID_ARG, "%d rows of %d sequences are too many", total_q, B);
   if (cu_seqlens_q == nullptr && total_q != B)
     return set_error(ATTN_ERR_INVALID_ARG,
                      "without cu_seqlens_q every sequence has one new token (total_q=%d, B=%d)",

@@ -60,6 +60,7 @@ APPEND = dict(q=0, k=0, v=0, qo=0, kp=0, vp=0, pt=0, cu=None, ln=0, inv=0, B=2, 
     (dict(qo=None), "INVALID_ARG"), (dict(pt=None), "INVALID_ARG"), (dict(ln=None), "INVALID_ARG"),
     (dict(vs=(250, 128)), "INVALID_ARG"), (dict(qos=(0, 128)), "INVALID_ARG"),
     (dict(B=0, T=0), "OK"), (dict(B=2 ** 31 - 1, T=2 ** 31 - 1), "INVALID_ARG"),
+    (dict(B=2 ** 31 - 1, T=4, cu=16), "INVALID_ARG"),
 ])
 def test_append_arguments(change, status):
     buf, p = _ptr()

@@ -1,5 +1,7 @@
 """The paged cache's upkeep on the GPU against the host walk of tests/_cache_ref.py:
 tables, lengths and counts entry for entry, pages byte for byte."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -299,6 +301,40 @@ def test_captured_steps_and_own_streams():
             ea.attn_pages_resize(c["pt"], c["ln"], none, c["refs"], c["kp"], c["vp"], stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(caches[0][x], caches[1][x]) for x in caches[0])
+
+
+def test_two_threads_on_one_stream():
+    """Two host threads, each with a cache of its own, launching into one stream: the
+    launches of their calls interleave."""
+    def run(out, seed):
+        try:
+            c = Cache(6, 8, 60, layers=2, Hkv=8, d=128, seed=seed)
+            lens = [i32(v) for v in ([40, 0, 0, 7, 0, 100], [41, 41, 0, 8, 17, 101],
+                                     [3, 0, 20, 0, 17, 0], [0] * 6)]
+            src, dst = i32([0, 3]), i32([1, 4])
+            for _ in range(60):
+                ea.attn_pages_resize(c.pt, c.ln, lens[0], c.refs, c.kp, c.vp)
+                ea.attn_pages_fork(c.pt, c.ln, c.refs, src, dst, c.kp, c.vp)
+                for n in lens[1:]:
+                    ea.attn_pages_resize(c.pt, c.ln, n, c.refs, c.kp, c.vp)
+                    ea.attn_pages_compact(c.pt, c.ln, c.refs, c.kp, c.vp)
+            out[seed] = c
+        except Exception as e:  # a thread's failure is the test's
+            out[seed] = e
+
+    alone, both = {}, {}
+    for seed in (1, 2):
+        run(alone, seed)
+    threads = [threading.Thread(target=run, args=(both, seed)) for seed in (1, 2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert ea.attn_device_status() == ea.ATTN_OK
+    for seed in (1, 2):
+        for name in ("pt", "ln", "refs", "kp", "vp"):
+            assert torch.equal(getattr(alone[seed], name), getattr(both[seed], name))
 
 
 def test_workspace_is_the_callers_if_given():

@@ -119,6 +119,12 @@ def test_layouts_and_places(rot, interleaved):
     assert torch.equal(ea.attn_rope_bwd(one, None, inv, pos, interleaved=interleaved)[0],
                        ea.attn_rope_bwd(one.contiguous(), None, inv, pos,
                                         interleaved=interleaved)[0])
+    for part in (x[:1, :, :1].expand(B, S, Hq, d), x[:, :1, :1].expand(B, S, Hq, d),
+                 x[:1, :, :Hq].expand(B, S, Hq, d), x[:1, :1, :Hq].expand(B, S, Hq, d),
+                 x.transpose(1, 2)[:, :Hq, :1].expand(B, Hq, S, d).transpose(1, 2)):
+        got = ea.attn_rope_bwd(part, None, inv, pos, interleaved=interleaved)[0]
+        assert torch.equal(got, ea.attn_rope_bwd(part.contiguous(), None, inv, pos,
+                                                 interleaved=interleaved)[0])
     y = x.clone()
     qi, ki = y[:, :, :Hq], y[:, :, Hq:Hq + Hkv]
     got = call(qi, ki, q_out=qi, k_out=ki)

@@ -123,6 +123,8 @@ int pages_common(PagesArgs* a, int* page_table, int* seqlens, int* refs, int B, 
   if (page_size != 16) return set_error(ATTN_ERR_UNSUPPORTED, "page size %d (16)", page_size);
   if (d != 64 && d != 128 && d != 256)
     return set_error(ATTN_ERR_UNSUPPORTED, "head dim %d (64, 128 or 256)", d);
+  if (B > kPagesMaxTable)
+    return set_error(ATTN_ERR_INVALID_ARG, "%d table rows, at most %d", B, kPagesMaxTable);
   if (rows > kPagesMaxRows)
     return set_error(ATTN_ERR_INVALID_ARG, "%d rows, at most %d in one call", rows,
                      kPagesMaxRows);

@@ -111,7 +111,8 @@ struct AppendArgs {
   int* status;
 };
 
-constexpr int kPagesMaxRows = 8192;       // rows (or forks) of one bookkeeping call
+constexpr int kPagesMaxRows = 8192;      // rows of a resize, forks of one call
+constexpr int kPagesMaxTable = 1 << 20;  // rows of a table (a compaction, or behind a fork)
 constexpr int kPagesMaxPages = 1 << 23;  // pages of a pool: one bit each in a cluster's shared memory
 
 // The page table of a paged cache, its reference counts and its pools.

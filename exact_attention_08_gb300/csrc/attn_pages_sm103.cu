@@ -25,11 +25,14 @@
 //
 // Measured (one GB300, device time in a graph).  The bookkeeping kernel is a
 // chain of dependent reads and three or four cluster barriers, bound by their
-// latency: 6.0 us for a decode step of 64 rows over 65,792 pages, launch
-// included (6.6 with refs read after the releases instead of before, when
-// their latency hides behind the rows').  The finishing kernel is bound by bytes: a compaction of 16,384
-// pages that moves 3,932 of 64 KB (515 MB read and written) takes 85.8 us in
-// all, 90 % of a copy's measured rate (8 blocks an SM; 4 took 91 us).
+// latency: 6.4 us for a decode step of 64 rows over 65,792 pages, launch
+// included.  Rows of more than 512 pages are walked by whole CTAs, and by
+// several blocks of the finishing kernel: with a warp (a block) a row, one row
+// of 65,536 pages took 527 us to grow, 1,155 to free and 64 to fork, now 32,
+// 84 and 15; short rows pay 0.4 us for it.  The finishing kernel is bound by
+// bytes: a compaction of 16,384 pages that moves 3,932 of 64 KB (515 MB read
+// and written) takes 84.3 us in all, 91 % of a copy's measured rate, with 32
+// blocks for every SM (8: 90.5 us; blocks that all run at once keep in step).
 #include "attn_internal.h"
 #include "sm103_ptx.cuh"
 
@@ -42,6 +45,9 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVecs = 4;  // 16-byte vectors in flight per thread
+constexpr int kLong = 512;    // table entries of a row from which a whole CTA walks them
+constexpr int kAtOnce = 4;    // table entries in flight per thread
+constexpr int kSegment = kCopyThreads * kAtOnce;  // table entries of a finishing block's step
 
 // ---------------------------------------------------------------- workspace
 // Ints: [0] the number of copies; at kHead two lists of num_pages (the free
@@ -125,11 +131,39 @@ struct Shared {
   unsigned long long counted[kCtas]; // free (or live) pages of the CTA's run
   int warp_off[kWarps];
   unsigned long long holes;           // compaction: pages that move
-  int rows;                           // entries of row[]
-  int row[kThreads];                  // the CTA's rows whose page lists a whole warp walks
+  int rows, longs;                    // entries of row[] from its front and from its back
+  int row[kThreads];                  // the CTA's rows whose page lists a warp or the CTA walks
   int from[kThreads], to[kThreads];   // those rows' first and last table column, by thread
   int start[kThreads];                // rank of the first page the row gets
 };
+
+// Puts thread t's row, with table columns [from, to), on the list of rows that
+// warps walk, or, from its back, on that of rows the whole CTA walks.
+__device__ __forceinline__ void list_row(Shared& sh, int t, int from, int to) {
+  sh.from[t] = from;
+  sh.to[t] = to;
+  if (to - from > kLong)
+    sh.row[kThreads - 1 - atomicAdd(&sh.longs, 1)] = t;
+  else
+    sh.row[atomicAdd(&sh.rows, 1)] = t;
+}
+
+// Calls walk(t, column, stride) for every listed row, by its warp or by the
+// CTA, with each thread's first column and its step.
+template <typename Walk>
+__device__ __forceinline__ void walk_rows(const Shared& sh, Walk walk) {
+  const int tid = threadIdx.x;
+  // one loop over both lists, so that the walk is compiled once, in line
+  for (int i = tid >> 5, wide = 0;; i += wide ? 1 : kWarps) {
+    if (!wide && i >= sh.rows) {
+      wide = 1;
+      i = 0;
+    }
+    if (wide && i >= sh.longs) break;
+    const int t = sh.row[wide ? kThreads - 1 - i : i];
+    walk(t, sh.from[t] + (wide ? tid : tid & 31), wide ? kThreads : 32);
+  }
+}
 
 constexpr int kCopyShift = 44;
 constexpr unsigned long long kAskMask = (1ull << kCopyShift) - 1;
@@ -239,7 +273,7 @@ __device__ __forceinline__ bool in_pool(const PagesArgs& a, int page) {
 }
 
 // ---------------------------------------------------------------- resize
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     pages_resize_kernel(const __grid_constant__ PagesArgs a) {
   extern __shared__ uint32_t bits[];
   __shared__ Shared sh;
@@ -250,7 +284,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
   const bool mine = tid < per && b < a.B;
   int old = 0, n = 0;
   bool ok = mine;
-  if (tid == 0) sh.rows = 0;
+  if (tid == 0) sh.rows = sh.longs = 0;
   __syncthreads();
 
   // 1. pages past a row's new end are given back, and cleared in the bits of
@@ -264,30 +298,27 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     if (!ok) {
       atomicOr(a.status, kStatusBadInput);
     } else if (pages_of(n) < pages_of(old)) {
-      sh.from[tid] = pages_of(n);
-      sh.to[tid] = pages_of(old);
-      sh.row[atomicAdd(&sh.rows, 1)] = tid;
+      list_row(sh, tid, pages_of(n), pages_of(old));
     }
   }
   live_bits(a, r, bits, 1);
   cluster_sync();
-  for (int i = warp; i < sh.rows; i += kWarps) {
-    const int t = sh.row[i];
+  walk_rows(sh, [&](int t, int first, int step) {
     const int* row = a.page_table + static_cast<size_t>(cta * per + t) * a.max_pages;
-    for (int j = sh.from[t] + lane; j < sh.to[t]; j += 32) {
+    for (int j = first; j < sh.to[t]; j += step) {
       const int page = __ldcg(row + j);
       if (!in_pool(a, page))
         atomicOr(a.status, kStatusBadInput);
       else if (atomicSub(a.refs + page, 1) == 1)
         clear_bit(a.num_pages, bits, page);
     }
-  }
+  });
   cluster_sync();
 
   // 2. free pages counted, pages asked for summed.  A row asks for the pages
   // it grows by, and for one more where it grows inside a last page that
   // another row holds too: that page is copied before it is written.
-  if (tid == 0) sh.rows = 0;
+  if (tid == 0) sh.rows = sh.longs = 0;
   int live = 0;
   for (int w = r.w0 + lane; w < r.w1; w += 32) live += __popc(bits[w]);
   live = __reduce_add_sync(0xffffffffu, live);
@@ -348,24 +379,23 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
         row[c0] = page;
         a.refs[page] = 1;
       } else if (c1 > c0) {
-        sh.from[tid] = c0;
-        sh.to[tid] = c1;
         sh.start[tid] = at;
-        sh.row[atomicAdd(&sh.rows, 1)] = tid;
+        list_row(sh, tid, c0, c1);
       }
       a.seqlens[b] = n;
     }
   }
   __syncthreads();
-  for (int i = warp; i < sh.rows; i += kWarps) {
-    const int t = sh.row[i];
+  walk_rows(sh, [&](int t, int first, int step) {
     int* row = a.page_table + static_cast<size_t>(cta * per + t) * a.max_pages;
-    for (int j = sh.from[t] + lane; j < sh.to[t]; j += 32) {
-      const int page = __ldcg(list + sh.start[t] + j - sh.from[t]);
+    const int* mine = list + sh.start[t] - sh.from[t];
+#pragma unroll 4
+    for (int j = first; j < sh.to[t]; j += step) {
+      const int page = __ldcg(mine + j);
       row[j] = page;
       a.refs[page] = 1;
     }
-  }
+  });
 }
 
 // ---------------------------------------------------------------- fork
@@ -379,7 +409,7 @@ __device__ __forceinline__ int length_before(const PagesArgs& a, int row) {
   return v < kClaim + kPagesMaxRows ? 0 : v;
 }
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     pages_fork_kernel(const __grid_constant__ PagesArgs a) {
   extern __shared__ uint32_t bits[];
   __shared__ Shared sh;
@@ -454,7 +484,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
 // pages after a page are the total less those up to it), which needs no
 // count at the boundary L; the boundary's own count, the number of movers,
 // then turns the ranks round.
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     pages_compact_kernel(const __grid_constant__ PagesArgs a) {
   extern __shared__ uint32_t bits[];
   __shared__ Shared sh;
@@ -516,38 +546,58 @@ __global__ void __launch_bounds__(kCopyThreads)
     pages_finish_kernel(const __grid_constant__ PagesArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x;
+  // Rows in segments, so that one long row is shared by many blocks.  Their
+  // product fits 31 bits: 2^20 rows at most, and a table that fits memory has
+  // fewer than 2^27 segments of 1024 entries beyond one a row.
+  const int segments = (a.max_pages + kSegment - 1) / kSegment;
   if constexpr (kMode == kFork) {
-    for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
+    for (int it = blockIdx.x; it < a.n * segments; it += gridDim.x) {
+      const int i = segments > 1 ? it / segments : it;
+      const int j0 = (it - i * segments) * kSegment + tid;
       const int* fork = ws_forks(a) + 3 * static_cast<size_t>(i);
       const int whole = fork[2];
-      if (whole == 0) continue;
+      if (j0 - tid >= whole) continue;
       const int* from = a.page_table + static_cast<size_t>(fork[0]) * a.max_pages;
       int* to = a.page_table + static_cast<size_t>(fork[1]) * a.max_pages;
-      for (int j = tid; j < whole; j += kCopyThreads) {
-        const int page = from[j];
-        to[j] = page;
-        if (in_pool(a, page))
-          atomicAdd(a.refs + page, 1);
+      int page[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        page[k] = j0 + k * kCopyThreads < whole ? __ldcg(from + j0 + k * kCopyThreads) : 0;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        if (j0 + k * kCopyThreads >= whole) break;
+        to[j0 + k * kCopyThreads] = page[k];
+        if (in_pool(a, page[k]))
+          atomicAdd(a.refs + page[k], 1);
         else
           atomicOr(a.status, kStatusBadInput);
       }
     }
   }
   if constexpr (kMode == kCompact) {
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    for (int it = blockIdx.x; it < a.B * segments; it += gridDim.x) {
+      const int b = segments > 1 ? it / segments : it;
+      const int j0 = (it - b * segments) * kSegment + tid;
       const int len = a.seqlens[b];
       if (len < 0 || len > a.max_pages * kPage) {
         if (tid == 0) atomicOr(a.status, kStatusBadInput);
         continue;
       }
       int* row = a.page_table + static_cast<size_t>(b) * a.max_pages;
-      for (int j = tid; j < pages_of(len); j += kCopyThreads) {
-        const int page = row[j];
-        const int to = in_pool(a, page) ? __ldcg(a.new_index + page) : -1;
-        if (to < 0)  // not a page, or one that nothing counts as held
+      int page[kAtOnce], to[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        page[k] = j0 + k * kCopyThreads < pages_of(len) ? row[j0 + k * kCopyThreads] : -1;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        to[k] = in_pool(a, page[k]) ? __ldcg(a.new_index + page[k]) : -1;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        if (j0 + k * kCopyThreads >= pages_of(len)) break;
+        if (to[k] < 0)  // not a page, or one that nothing counts as held
           atomicOr(a.status, kStatusBadInput);
-        else if (to != page)
-          row[j] = to;
+        else if (to[k] != page[k])
+          row[j0 + k * kCopyThreads] = to[k];
       }
     }
   }
@@ -603,11 +653,13 @@ cudaError_t launch_book(Kernel kernel, const PagesArgs& a, cudaStream_t stream) 
 template <int kMode>
 cudaError_t launch_finish(const PagesArgs& a, long long most_copies, int rows,
                           cudaStream_t stream) {
+  const long long steps =
+      static_cast<long long>(rows) * ((a.max_pages + kSegment - 1) / kSegment);
   constexpr int kPiece = kCopyThreads * kCopyVecs;
   const long long items =
       most_copies * 2 * a.layers * ((a.page_vecs + kPiece - 1) / kPiece);
-  long long grid = items > rows ? items : rows;
-  const long long most = 8ll * a.num_sms;
+  long long grid = items > steps ? items : steps;
+  const long long most = 32ll * a.num_sms;
   if (grid > most) grid = most;
   if (grid < 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};

@@ -482,8 +482,9 @@ ATTN_API int attn_append_paged(const void* q, const void* k, const void* v, void
  *     num_pages_total) bytes (rows: B for a resize, n for a fork, 0 for a
  *     compaction), overwritten; calls that may overlap need one each.
  * Calls on one cache, attention calls among them, must be ordered (one
- * stream, or events).  At most 8192 rows and 2^23 pages a call
- * (ATTN_ERR_INVALID_ARG).  attn_pages_workspace_size: 0 on invalid sizes.
+ * stream, or events).  At most 8192 rows of a resize, 8192 forks of a call,
+ * 2^20 rows of a table and 2^23 pages (ATTN_ERR_INVALID_ARG).
+ * attn_pages_workspace_size: 0 on invalid sizes.
  */
 ATTN_API size_t attn_pages_workspace_size(int rows, int num_pages_total);
 

@@ -91,7 +91,7 @@ def _pages_args(which):
     (dict(P=0), "INVALID_ARG"), (dict(P=(1 << 23) + 1), "INVALID_ARG"),
     (dict(maxp=0), "INVALID_ARG"), (dict(refs=None), "INVALID_ARG"), (dict(pt=None), "INVALID_ARG"),
     (dict(bytes=16), "INVALID_ARG"), (dict(ws=None), "INVALID_ARG"), (dict(kp=None), "INVALID_ARG"),
-    (dict(B=-1), "INVALID_ARG"),
+    (dict(B=-1), "INVALID_ARG"), (dict(B=(1 << 20) + 1, bytes=1 << 30), "INVALID_ARG"),
 ])
 def test_pages_arguments(which, change, status):
     buf, a = _pages_args(which)

@@ -258,6 +258,41 @@ def test_long_rows_and_offsets_past_32_bits():
     assert torch.equal(kp[:, 69999], kp[:, 70000])
 
 
+def test_more_table_rows_than_one_resize_takes():
+    """A table of 10,000 rows: forked from and compacted; a resize of it is refused."""
+    B, P = 10000, 300
+    c = Cache(B, 2, P)
+    g = np.random.default_rng(4)
+    for b in g.choice(B, 100, replace=False):
+        n = int(g.integers(1, 33))
+        c.m.len[b] = n
+        for j in range(ref.pages_of(n)):
+            p = int(g.choice([p for p in range(P) if c.m.refs[p] == 0]))
+            c.m.table[b][j], c.m.refs[p] = p, 1
+    c.load()
+    full = [b for b in range(B) if c.m.len[b]]
+    c.fork(full[:50], [b for b in range(B) if c.m.len[b] == 0][-50:])
+    c.compact()
+    with pytest.raises(ea.AttnError) as e:
+        ea.attn_pages_resize(c.pt, c.ln, c.ln.clone(), c.refs, c.kp, c.vp)
+    assert e.value.status == ea.ATTN_ERR_INVALID_ARG
+
+
+def test_rows_of_every_length():
+    """Rows around the lengths at which a warp, the whole block or several blocks walk
+    their entries."""
+    lens = [0, 16, 500 * 16, 512 * 16, 513 * 16, 1023 * 16 + 1, 1024 * 16, 1025 * 16 - 7,
+            2100 * 16, 1]
+    B = 2 * len(lens)
+    c = Cache(B, 2200, 2 * sum(map(ref.pages_of, lens)) + 40)
+    c.resize(lens + [0] * len(lens))
+    c.fork(list(range(len(lens))), list(range(len(lens), B)))
+    c.resize([0, 16, 40, 513 * 16, 0, 600 * 16, 0, 0, 1500 * 16, 1] + [n + 3 for n in lens])
+    c.compact()
+    c.resize([0] * B)
+    assert c.m.refs == [0] * len(c.m.refs)
+
+
 def test_captured_steps_and_own_streams():
     """A captured resize and fork replayed on new lengths, and two caches on two streams
     at once: the tables of the plain calls."""

@@ -400,14 +400,11 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- fork
 // Row dst[i] claims its place with INT_MIN + i in its length, so that of two
-// forks into one row the first wins whatever the timing; a length in that
-// range therefore reads as the 0 it was.
+// forks into one row the first wins whatever the timing.  Every length is
+// read, and one out of range refused, before the first claim is made (a
+// cluster barrier lies between, waited for after the counts are read), so no
+// stored length is ever taken for a claim.
 constexpr int kClaim = static_cast<int>(0x80000000u);
-
-__device__ __forceinline__ int length_before(const PagesArgs& a, int row) {
-  const int v = __ldcg(a.seqlens + row);
-  return v < kClaim + kPagesMaxRows ? 0 : v;
-}
 
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     pages_fork_kernel(const __grid_constant__ PagesArgs a) {
@@ -419,7 +416,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
   const int i = cta * per + tid;
   const bool mine = tid < per && i < a.n;
 
-  // 1. what each fork copies; claims on the new rows; live pages
+  // 1. what each fork copies; live pages; claims on the new rows
   int src = 0, dst = 0, len = 0, last = -1;
   bool ok = false;
   if (mine) {
@@ -427,17 +424,20 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     dst = __ldg(a.dst + i);
     ok = src >= 0 && src < a.B && dst >= 0 && dst < a.B && src != dst;
     if (ok) {
-      len = length_before(a, src);
-      ok = len >= 0 && len <= a.max_pages * kPage && length_before(a, dst) == 0;
-      if (ok && len % kPage != 0) {
-        last = __ldcg(a.page_table + static_cast<size_t>(src) * a.max_pages + len / kPage);
-        ok = in_pool(a, last);
-      }
-      if (ok) atomicMin(a.seqlens + dst, kClaim + i);
+      len = __ldcg(a.seqlens + src);
+      ok = __ldcg(a.seqlens + dst) == 0 && len >= 0 && len <= a.max_pages * kPage;
     }
+  }
+  cluster_arrive();
+  if (ok && len % kPage != 0) {
+    last = __ldcg(a.page_table + static_cast<size_t>(src) * a.max_pages + len / kPage);
+    ok = in_pool(a, last);
   }
   const Run r = page_run(a.num_pages, cta, warp);
   const int live = live_bits(a, r, bits, 1);
+  cluster_wait();
+  if (ok) atomicMin(a.seqlens + dst, kClaim + i);
+  share_counts(sh, cta, (r.w1 - r.w0) * 32 - live);
   cluster_sync();
 
   // 2. pages asked for: one where the source ends inside a page
@@ -446,7 +446,6 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
   const int need = won && last >= 0;
   unsigned long long total;
   unsigned long long before = scan_exclusive(need, sh.warp_s, &total);
-  share_counts(sh, cta, (r.w1 - r.w0) * 32 - live);
   if (tid < kCtas) st_cluster(&sh.asked[cta], tid, total);
   cluster_sync();
 

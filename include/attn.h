@@ -521,7 +521,8 @@ ATTN_API int attn_pages_resize(int* page_table, int* seqlens, const int* new_seq
  *   ATTN_ERR_BAD_INPUT, and row dst[i] as it was: an index out of [0, B),
  *     dst[i] == src[i], a row that is not empty, a row forked into a second
  *     time (the first fork stands), a source with a length or last page out of
- *     range.  A source that is itself some dst counts as empty.
+ *     range.  Every length is read before any row is filled: a source that
+ *     another fork of the call fills counts as empty.
  */
 ATTN_API int attn_pages_fork(int* page_table, int* seqlens, int* refs, const int* src,
                              const int* dst, int n, void* k_pages, void* v_pages, int B,

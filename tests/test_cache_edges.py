@@ -1,0 +1,45 @@
+"""Rotary positions and the paged cache's upkeep on the GPU, at the lengths, sizes and
+positions where a call could go wrong unnoticed."""
+import numpy as np
+import pytest
+
+from tests import _cache_ref as ref
+from tests.test_pages_parity import Cache
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ fork: stored lengths
+
+@pytest.mark.parametrize("bad", [-2 ** 31, -2 ** 31 + 1, -2 ** 31 + 5, -2 ** 31 + 8191,
+                                 -2 ** 31 + 8192, -1, 65, 2 ** 31 - 1])
+def test_fork_reports_stored_lengths_out_of_range(bad):
+    """As a source's length, as a new row's, and as both, by the fork whose number is near
+    the length's distance from -2^31 and by others."""
+    c = Cache(10, 4, 40, layers=2)
+    c.resize([40, 0, 0, 5, 0, 0, 0, 0, 0, 0])
+    c.m.len[1] = c.m.len[9] = bad
+    c.load()
+    for src, dst in (([1], [2]), ([0], [1]), ([1], [9]), ([0, 1, 3], [1, 2, 9]),
+                     ([0, 0, 0, 0, 0, 0], [2, 4, 5, 6, 7, 1]), ([1, 0, 0], [4, 1, 4])):
+        before = c.m.len[1], c.m.len[9]
+        c.fork(src, dst)
+        assert "bad" in c.m.status and (c.m.len[1], c.m.len[9]) == before == (bad, bad)
+        for b in range(1, 9):
+            if b not in (1, 3):
+                for p in c.m.table[b][:ref.pages_of(c.m.len[b])]:
+                    c.m.refs[p] -= 1
+                c.m.len[b] = 0
+        c.load()
+
+
+def test_many_forks_into_few_rows():
+    """8,192 forks whose rows repeat: the first of each row stands, whichever block
+    holds it, and a row that some fork fills is empty as a source."""
+    B = 600
+    c = Cache(B, 3, 900)
+    g = np.random.default_rng(12)
+    c.resize([int(g.integers(1, 49)) if b < 200 else 0 for b in range(B)])
+    for _ in range(3):
+        c.fork(g.integers(0, B, 8192).tolist(), g.integers(0, B, 8192).tolist())
+        c.resize([n if b < 200 else 0 for b, n in enumerate(c.m.len)])

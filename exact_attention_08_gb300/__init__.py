@@ -141,12 +141,15 @@ _torch_module = _current_device = _raw_stream = None
 
 
 def _torch():
-    """torch, imported on first use (with the two calls that every launch makes of it)."""
+    """torch, imported on first use, with the two calls of it that every launch around the
+    attention makes: torch's own short forms where it has them, which a torch without
+    CUDA does not, else the documented ones."""
     global _torch_module, _current_device, _raw_stream
     if _torch_module is None:
         import torch
-        _current_device = torch._C._cuda_getDevice
-        _raw_stream = torch._C._cuda_getCurrentRawStream
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
         _torch_module = torch
     return _torch_module
 

@@ -2,8 +2,11 @@
 positions where a call could go wrong unnoticed."""
 import numpy as np
 import pytest
+import torch
 
+import exact_attention_08_gb300 as ea
 from tests import _cache_ref as ref
+from tests.test_cache_edges_cpu import without_cuda_names
 from tests.test_pages_parity import Cache
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +46,22 @@ def test_many_forks_into_few_rows():
     for _ in range(3):
         c.fork(g.integers(0, B, 8192).tolist(), g.integers(0, B, 8192).tolist())
         c.resize([n if b < 200 else 0 for b, n in enumerate(c.m.len)])
+
+
+# ------------------------------------------------------------------ torch without private names
+
+def test_calls_without_torchs_private_names(monkeypatch):
+    g = torch.Generator().manual_seed(2)
+    q = torch.randn(2, 5, 3, 64, generator=g).bfloat16().cuda()
+    inv = ea.attn_rope_inv_freq(64)
+    want = ea.attn_rope(q, None, inv)[0]
+    here = torch.cuda.current_device()
+    without_cuda_names(monkeypatch)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: here)  # it uses one of the names
+    assert torch.equal(ea.attn_rope(q, None, inv)[0], want)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        got = ea.attn_rope(q, None, inv)[0]
+    side.synchronize()
+    assert torch.equal(got, want)

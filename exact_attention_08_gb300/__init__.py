@@ -806,19 +806,11 @@ def _cache_pools(k_pages, v_pages, pages, index):
     return layers, page, Hkv, d
 
 
-@functools.lru_cache(maxsize=256)
-def _vector_like(n, dtype, index):
-    """One element spread over n: empty_like of it costs half the host time of empty with a
-    size, a type and a device."""
-    torch = _torch()
-    return torch.empty(1, dtype=dtype, device=torch.device("cuda", index)).expand(n)
-
-
 def _workspace(workspace, rows, pages, refs):
     torch = _torch()
     if workspace is None:
-        return torch.empty_like(_vector_like(attn_pages_workspace_size(rows, pages), torch.uint8,
-                                             refs.get_device()))
+        return torch.empty(attn_pages_workspace_size(rows, pages), dtype=torch.uint8,
+                           device=refs.device)
     if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or \
             workspace.get_device() != refs.get_device():
         raise ValueError(f"workspace must be a contiguous tensor on {refs.device}")
@@ -891,7 +883,7 @@ def attn_pages_compact(page_table, seqlens, refs, k_pages, v_pages, *, workspace
     torch = _torch()
     ws = _workspace(workspace, 0, P, refs)
     new_index = torch.empty_like(refs)
-    num_live = torch.empty_like(_vector_like(1, torch.int32, index))
+    num_live = torch.empty(1, dtype=torch.int32, device=refs.device)
     rc = lib.attn_pages_compact(
         page_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(), new_index.data_ptr(),
         num_live.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), B, layers, Hkv, d, page, W,

@@ -1,5 +1,7 @@
 """Rotary positions and the paged cache's upkeep on the GPU, at the lengths, sizes and
 positions where a call could go wrong unnoticed."""
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -7,7 +9,7 @@ import torch
 import exact_attention_08_gb300 as ea
 from tests import _cache_ref as ref
 from tests.test_cache_edges_cpu import without_cuda_names
-from tests.test_pages_parity import Cache
+from tests.test_pages_parity import Cache, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -46,6 +48,36 @@ def test_many_forks_into_few_rows():
     for _ in range(3):
         c.fork(g.integers(0, B, 8192).tolist(), g.integers(0, B, 8192).tolist())
         c.resize([n if b < 200 else 0 for b, n in enumerate(c.m.len)])
+
+
+# ------------------------------------------------------------------ memory
+
+def test_a_captured_call_leaves_no_memory_behind():
+    """A page call of a size first met in a capture: its graph's memory goes with it."""
+    def tables(P):
+        return (i32([[0, -1]]), i32([5]), i32([1] + [0] * (P - 1)),
+                torch.zeros(P, 16, 1, 64, dtype=torch.bfloat16, device="cuda"),
+                torch.zeros(P, 16, 1, 64, dtype=torch.bfloat16, device="cuda"))
+
+    ea.attn_pages_compact(*tables(8))
+    args, new = tables(1237), i32([20])
+    torch.cuda.synchronize()
+
+    def reserved():
+        gc.collect()
+        torch.cuda.empty_cache()
+        return torch.cuda.memory_reserved()
+
+    before = reserved()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ea.attn_pages_resize(args[0], args[1], new, args[2], *args[3:])
+        out = ea.attn_pages_compact(*args)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert out[1].item() == 2 and ea.attn_device_status() == ea.ATTN_OK
+    del out, graph
+    assert reserved() == before
 
 
 # ------------------------------------------------------------------ torch without private names

@@ -560,6 +560,9 @@ class _Call:
                 raw = int(getattr(stream, "cuda_stream", stream))
                 stream = torch.cuda.ExternalStream(raw, device=index) if raw else \
                     torch.cuda.default_stream(index)
+            elif stream.device_index != index:
+                raise ValueError(f"stream is one of cuda:{stream.device_index}, the tensors are "
+                                 f"on cuda:{index}")
             self._contexts += (torch.cuda.stream(stream),)
 
     def __enter__(self):

@@ -23,3 +23,27 @@ def test_refusals_and_frequencies_without_torchs_private_names(monkeypatch):
         ea.attn_fwd(q, q, q)
     with pytest.raises(ValueError):
         ea.attn_rope(q, None, inv)
+
+
+class FakeStream:
+    def __init__(self, index):
+        self.device_index, self.cuda_stream = index, 64 + index
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """Two devices' streams stood in for: making the other device's current would launch
+    on it, or, with the tensors' device made current again, drop the stream."""
+    class Context:
+        def __init__(self, *_):
+            pass
+
+        __enter__ = __exit__ = lambda self, *_: None
+
+    monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+    monkeypatch.setattr(torch.cuda, "device", Context)
+    monkeypatch.setattr(torch.cuda, "stream", Context)
+    ea._Call(0, FakeStream(0))
+    ea._Call(1, FakeStream(1))
+    for index in (0, 1):
+        with pytest.raises(ValueError):
+            ea._Call(index, FakeStream(1 - index))

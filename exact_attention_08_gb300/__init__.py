@@ -606,6 +606,15 @@ def _int_vector(t, name, n, index):
         raise ValueError(f"{name} must be [{n}], got {list(t.shape)}")
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _c_int(n):
+    """A size for the library's 32-bit arguments, into which ctypes would put the low bits of
+    a larger one: both ends stand for what the library refuses."""
+    return n if -1 <= n <= _INT_MAX else _INT_MAX if n > 0 else -1
+
+
 def _frequencies(inv_freq, d, index):
     torch = _torch()
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype is not torch.float64 or \
@@ -655,8 +664,9 @@ def attn_rope_inv_freq(rotary_dim: int, base: float = 10000.0, *, scaling: str =
     torch = _torch()
     if scaling not in _ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}")
-    out = torch.empty(max(int(rotary_dim) // 2, 0), dtype=torch.float64)
-    _check(lib.attn_rope_inv_freq(int(rotary_dim), float(base), _ROPE_SCALINGS[scaling],
+    rotary_dim = _c_int(int(rotary_dim))
+    out = torch.empty(max(rotary_dim // 2, 0), dtype=torch.float64)
+    _check(lib.attn_rope_inv_freq(rotary_dim, float(base), _ROPE_SCALINGS[scaling],
                                   float(factor), float(original_length), float(ramp[0]),
                                   float(ramp[1]), out.data_ptr()), "attn_rope_inv_freq")
     return out.to(device)
@@ -768,9 +778,10 @@ def attn_append_paged(q, k, v, k_pages, v_pages, page_table, seqlens_k, cu_seqle
         qp, qo, sq, sqo = q.data_ptr(), q_out.data_ptr(), _strides(q, 2), _strides(q_out, 2)
     rc = lib.attn_append_paged(
         qp, k.data_ptr(), v.data_ptr(), qo, k_pages.data_ptr(), v_pages.data_ptr(),
-        page_table.data_ptr(), _ptr(cu_seqlens_q), seqlens_k.data_ptr(), _ptr(inv_freq), B, Hq,
-        Hkv, T, d, rot, 1 if interleaved else 0, amplitude, page, page_table.shape[1], P, sq,
-        _strides(k, 2), _strides(v, 2), sqo, _raw_stream(index))
+        page_table.data_ptr(), _ptr(cu_seqlens_q), seqlens_k.data_ptr(), _ptr(inv_freq), _c_int(B),
+        Hq, Hkv, _c_int(T), d, rot, 1 if interleaved else 0, amplitude, page,
+        _c_int(page_table.shape[1]), P, sq, _strides(k, 2), _strides(v, 2), sqo,
+        _raw_stream(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_append_paged")
     return q_out if q is not None else None
@@ -778,7 +789,7 @@ def attn_append_paged(q, k, v, k_pages, v_pages, page_table, seqlens_k, cu_seqle
 
 @functools.lru_cache(maxsize=256)
 def attn_pages_workspace_size(rows: int, num_pages: int) -> int:
-    return int(lib.attn_pages_workspace_size(int(rows), int(num_pages)))
+    return int(lib.attn_pages_workspace_size(_c_int(int(rows)), _c_int(int(num_pages))))
 
 
 def _cache_tables(page_table, seqlens, refs):
@@ -793,7 +804,7 @@ def _cache_tables(page_table, seqlens, refs):
         raise ValueError("page_table must be [B, max_pages], refs [P]")
     B, W = page_table.shape
     _int_vector(seqlens, "seqlens", B, index)
-    return index, B, W, refs.numel()
+    return index, _c_int(B), _c_int(W), _c_int(refs.numel())
 
 
 def _cache_pools(k_pages, v_pages, pages, index):
@@ -858,6 +869,7 @@ def attn_pages_fork(page_table, seqlens, refs, src, dst, k_pages, v_pages, *, wo
     n = src.numel()
     _int_vector(src, "src", n, index)
     _int_vector(dst, "dst", n, index)
+    n = _c_int(n)
     layers, page, Hkv, d = _cache_pools(k_pages, v_pages, P, index)
     if stream is not None or index != _current_device():
         with _Call(index, stream):

@@ -80,6 +80,31 @@ def test_a_captured_call_leaves_no_memory_behind():
     assert reserved() == before
 
 
+# ------------------------------------------------------------------ sizes
+
+def test_sizes_past_32_bits_are_refused():
+    """Counts, tables and lengths whose sizes a 32-bit int does not hold."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    big = torch.empty((1 << 32) + 12, dtype=torch.int32, device="cuda")
+    big[:64] = 0
+    pt, ln, new = i32([[-1] * 4] * 2), i32([0, 0]), i32([5, 0])
+    refs = i32([0] * 12)
+    pools = [torch.zeros(12, 16, 1, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    kv = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    many = kv.expand(big.numel(), 1, 64)
+    for call in (lambda: ea.attn_pages_resize(pt, ln, new, big),
+                 lambda: ea.attn_pages_resize(big[None], ln[:1], new[:1], refs),
+                 lambda: ea.attn_pages_fork(pt, ln, refs, big, big, *pools),
+                 lambda: ea.attn_append_paged(None, kv, kv, *pools, big[None], i32([1])),
+                 lambda: ea.attn_append_paged(None, many, many, *pools, big[:, None], big)):
+        with pytest.raises(ea.AttnError) as e:
+            call()
+        assert e.value.status == ea.ATTN_ERR_INVALID_ARG
+    assert ea.attn_device_status() == ea.ATTN_OK
+    assert not any(p.any() for p in pools) and not ln.any() and not refs.any()
+
+
 # ------------------------------------------------------------------ torch without private names
 
 def test_calls_without_torchs_private_names(monkeypatch):

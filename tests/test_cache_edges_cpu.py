@@ -47,3 +47,8 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
     for index in (0, 1):
         with pytest.raises(ValueError):
             ea._Call(index, FakeStream(1 - index))
+
+
+def test_sizes_past_32_bits_have_no_workspace():
+    for rows, pages in ((1 << 32, 12), (4, (1 << 32) + 12), (4, 12 - (1 << 32)), (1 - (1 << 32), 12)):
+        assert ea.attn_pages_workspace_size(rows, pages) == 0

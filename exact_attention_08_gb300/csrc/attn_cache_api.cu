@@ -184,19 +184,23 @@ ATTN_API int attn_rope_inv_freq(int rotary_dim, double base, int scaling, double
   const double kTwoPi = 6.283185307179586476925;
   if (scaling == ATTN_ROPE_BASE)
     base *= std::pow(factor, static_cast<double>(rotary_dim) / (rotary_dim - 2));
+  if (!(base > 0.0) || !std::isfinite(base))
+    return set_error(ATTN_ERR_INVALID_ARG, "the stretched base is out of fp64's range");
+  const auto frequency = [&](int i) {
+    const double f = std::pow(base, -2.0 * i / rotary_dim);
+    if (scaling == ATTN_ROPE_LINEAR) return f / factor;
+    if (scaling != ATTN_ROPE_RAMP) return f;
+    // turns the pair makes over the trained length
+    const double turns = original_length * f / kTwoPi;
+    double keep = (turns - ramp_low) / (ramp_high - ramp_low);
+    keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+    return f * (keep + (1.0 - keep) / factor);
+  };
   for (int i = 0; i < rotary_dim / 2; ++i) {
-    double f = std::pow(base, -2.0 * i / rotary_dim);
-    if (scaling == ATTN_ROPE_LINEAR) {
-      f /= factor;
-    } else if (scaling == ATTN_ROPE_RAMP) {
-      // turns the pair makes over the trained length
-      const double turns = original_length * f / kTwoPi;
-      double keep = (turns - ramp_low) / (ramp_high - ramp_low);
-      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
-      f *= keep + (1.0 - keep) / factor;
-    }
-    inv_freq[i] = f;
+    if (!std::isfinite(frequency(i)))
+      return set_error(ATTN_ERR_INVALID_ARG, "frequency %d is out of fp64's range", i);
   }
+  for (int i = 0; i < rotary_dim / 2; ++i) inv_freq[i] = frequency(i);
   return ATTN_OK;
 }
 

@@ -380,7 +380,9 @@ ATTN_API int attn_decode_paged_noalloc(const void* q, const void* k_pages, const
  * attn_rope_inv_freq fills the HOST array inv_freq [rotary_dim / 2] with
  * f_i = base^(-2 i / rotary_dim), stretched as `scaling` says (factor for all
  * but ATTN_ROPE_NONE; original_length, ramp_low and ramp_high for
- * ATTN_ROPE_RAMP).  Host only, no CUDA call.
+ * ATTN_ROPE_RAMP).  ATTN_ERR_INVALID_ARG, and nothing written, where the
+ * stretched base or a frequency is out of fp64's range.  Host only, no CUDA
+ * call.
  */
 ATTN_API int attn_rope_inv_freq(int rotary_dim, double base, int scaling, double factor,
                                 double original_length, double ramp_low, double ramp_high,

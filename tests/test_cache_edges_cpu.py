@@ -1,5 +1,8 @@
 """Rotary positions and the paged cache's upkeep where a host decision could go wrong,
 without a GPU."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
@@ -52,3 +55,22 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
 def test_sizes_past_32_bits_have_no_workspace():
     for rows, pages in ((1 << 32, 12), (4, (1 << 32) + 12), (4, 12 - (1 << 32)), (1 - (1 << 32), 12)):
         assert ea.attn_pages_workspace_size(rows, pages) == 0
+
+
+@pytest.mark.parametrize("args", [
+    dict(base=1e300, scaling="base", factor=1e10),      # the stretched base is infinite
+    dict(base=1e-300, scaling="base", factor=1e-200),   # or zero
+    dict(base=5e-324, scaling="none"),
+    dict(scaling="linear", factor=5e-324),
+    dict(scaling="ramp", factor=5e-324, original_length=2048.0)])
+def test_frequencies_that_fp64_does_not_hold_are_refused(args):
+    with pytest.raises(ea.AttnError) as e:
+        ea.attn_rope_inv_freq(128, device="cpu", **args)
+    assert e.value.status == ea.ATTN_ERR_INVALID_ARG
+
+
+def test_frequencies_near_the_ends_of_fp64_are_given():
+    for base in (1e-300, 1e300):
+        f = ea.attn_rope_inv_freq(64, base, device="cpu").numpy()
+        assert np.isfinite(f).all() and (f > 0).all()
+        np.testing.assert_allclose(np.log(f), -2 * np.arange(32) / 64 * math.log(base), rtol=1e-13)

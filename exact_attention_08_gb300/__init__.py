@@ -820,11 +820,23 @@ def _cache_pools(k_pages, v_pages, pages, index):
     return layers, page, Hkv, d
 
 
+@functools.lru_cache(maxsize=256)
+def _vector_like(n, dtype, index):
+    """A vector of n that holds no memory, only its shape: empty_like of it costs the host
+    about a microsecond less than empty with a size, a type and a device.  The one element
+    it is spread from goes back at once, so nothing stays allocated here, whatever pool
+    (a capture's, say) it came from."""
+    torch = _torch()
+    t = torch.empty(1, dtype=dtype, device=torch.device("cuda", index)).expand(n)
+    t.untyped_storage().resize_(0)
+    return t
+
+
 def _workspace(workspace, rows, pages, refs):
     torch = _torch()
     if workspace is None:
-        return torch.empty(attn_pages_workspace_size(rows, pages), dtype=torch.uint8,
-                           device=refs.device)
+        return torch.empty_like(_vector_like(attn_pages_workspace_size(rows, pages), torch.uint8,
+                                             refs.get_device()))
     if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or \
             workspace.get_device() != refs.get_device():
         raise ValueError(f"workspace must be a contiguous tensor on {refs.device}")
@@ -898,7 +910,7 @@ def attn_pages_compact(page_table, seqlens, refs, k_pages, v_pages, *, workspace
     torch = _torch()
     ws = _workspace(workspace, 0, P, refs)
     new_index = torch.empty_like(refs)
-    num_live = torch.empty(1, dtype=torch.int32, device=refs.device)
+    num_live = torch.empty_like(_vector_like(1, torch.int32, index))
     rc = lib.attn_pages_compact(
         page_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(), new_index.data_ptr(),
         num_live.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), B, layers, Hkv, d, page, W,

@@ -78,6 +78,9 @@ def test_a_captured_call_leaves_no_memory_behind():
     assert out[1].item() == 2 and ea.attn_device_status() == ea.ATTN_OK
     del out, graph
     assert reserved() == before
+    ea.attn_pages_compact(*args)         # the same size again, outside it
+    torch.cuda.synchronize()
+    assert ea.attn_device_status() == ea.ATTN_OK
 
 
 # ------------------------------------------------------------------ sizes

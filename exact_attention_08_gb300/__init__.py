@@ -756,6 +756,7 @@ def attn_append_paged(q, k, v, k_pages, v_pages, page_table, seqlens_k, cu_seqle
     _int_tensor(page_table, "page_table", index)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B, max_pages]")
+    W = page_table.shape[1]
     if cu_seqlens_q is not None:
         _int_vector(cu_seqlens_q, "cu_seqlens_q", B + 1, index)
     elif T != B:
@@ -772,16 +773,17 @@ def attn_append_paged(q, k, v, k_pages, v_pages, page_table, seqlens_k, cu_seqle
             return attn_append_paged(q, k, v, k_pages, v_pages, page_table, seqlens_k,
                                      cu_seqlens_q, inv_freq, interleaved=interleaved,
                                      amplitude=amplitude, q_out=q_out)
+    if B > _INT_MAX or T > _INT_MAX or W > _INT_MAX:
+        B, T, W = _c_int(B), _c_int(T), _c_int(W)
     qp = qo = sq = sqo = None
     if q is not None:
         q_out = _output(q_out, q, "q")
         qp, qo, sq, sqo = q.data_ptr(), q_out.data_ptr(), _strides(q, 2), _strides(q_out, 2)
     rc = lib.attn_append_paged(
         qp, k.data_ptr(), v.data_ptr(), qo, k_pages.data_ptr(), v_pages.data_ptr(),
-        page_table.data_ptr(), _ptr(cu_seqlens_q), seqlens_k.data_ptr(), _ptr(inv_freq), _c_int(B),
-        Hq, Hkv, _c_int(T), d, rot, 1 if interleaved else 0, amplitude, page,
-        _c_int(page_table.shape[1]), P, sq, _strides(k, 2), _strides(v, 2), sqo,
-        _raw_stream(index))
+        page_table.data_ptr(), _ptr(cu_seqlens_q), seqlens_k.data_ptr(), _ptr(inv_freq), B, Hq,
+        Hkv, T, d, rot, 1 if interleaved else 0, amplitude, page, W, P, sq, _strides(k, 2),
+        _strides(v, 2), sqo, _raw_stream(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_append_paged")
     return q_out if q is not None else None
@@ -804,7 +806,10 @@ def _cache_tables(page_table, seqlens, refs):
         raise ValueError("page_table must be [B, max_pages], refs [P]")
     B, W = page_table.shape
     _int_vector(seqlens, "seqlens", B, index)
-    return index, _c_int(B), _c_int(W), _c_int(refs.numel())
+    P = refs.numel()
+    if B > _INT_MAX or W > _INT_MAX or P > _INT_MAX:
+        B, W, P = _c_int(B), _c_int(W), _c_int(P)
+    return index, B, W, P
 
 
 def _cache_pools(k_pages, v_pages, pages, index):
@@ -881,7 +886,8 @@ def attn_pages_fork(page_table, seqlens, refs, src, dst, k_pages, v_pages, *, wo
     n = src.numel()
     _int_vector(src, "src", n, index)
     _int_vector(dst, "dst", n, index)
-    n = _c_int(n)
+    if n > _INT_MAX:
+        n = _c_int(n)
     layers, page, Hkv, d = _cache_pools(k_pages, v_pages, P, index)
     if stream is not None or index != _current_device():
         with _Call(index, stream):

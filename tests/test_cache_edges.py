@@ -1,6 +1,7 @@
 """Rotary positions and the paged cache's upkeep on the GPU, at the lengths, sizes and
 positions where a call could go wrong unnoticed."""
 import gc
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -125,3 +126,56 @@ def test_calls_without_torchs_private_names(monkeypatch):
         got = ea.attn_rope(q, None, inv)[0]
     side.synchronize()
     assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------ far positions
+
+# pi to 60 digits, for angles in exact arithmetic
+TWO_PI = 2 * Fraction(314159265358979323846264338327950288419716939937510582097494, 10 ** 59)
+
+
+def exact_angle(p, f):
+    """p f less whole turns, to the last bit of fp64."""
+    turns = Fraction(f) * p / TWO_PI
+    return float((turns - round(turns)) * TWO_PI)
+
+
+def nearly_cancelling(c, s):
+    """bf16 (x, y) with x c - y s as near zero as a search over their mantissas finds."""
+    m = 1 + np.arange(128) / 128
+    x, y = m[:, None], m[None, :] * 2.0 ** np.round(np.log2(abs(c / s)))
+    y = y * np.sign(c * s)
+    i, j = np.unravel_index(np.argmin(np.abs(x * c - y * s)), (128, 128))
+    return float(x[i, 0]), float(y[0, j])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot", [128, 20])
+def test_angles_of_far_positions(interleaved, rot):
+    """Pairs that the turn brings near zero in their first element: what is left is the
+    angle's error, no longer under half a step of a large value.  An angle off by the
+    documented 1e-6 radians would move that element by sqrt(x^2 + y^2) 1e-6, more than
+    the NEAR (|x| + |y|) allowed here for |y| near |x|; the kernel's own angle is
+    off by less than 2^-33 of a turn.  The reference's angle is exact, so it
+    adds nothing."""
+    positions = [1, -1, 131071, 10 ** 6, 2 ** 25 - 1, -2 ** 30 + 7, 2 ** 31 - 1, -2 ** 31]
+    inv = ea.attn_rope_inv_freq(rot, 1e4)
+    f = inv.cpu().numpy()
+    x = np.zeros((len(positions), 1, 128))
+    want, size = x.copy(), x.copy()
+    for r, p in enumerate(positions):
+        for i in range(rot // 2):
+            t = exact_angle(p, f[i])
+            c, s = np.cos(t), np.sin(t)
+            if not 0.02 < abs(s / c) < 50:
+                continue
+            a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
+            u, v = nearly_cancelling(c, s)
+            x[r, 0, a], x[r, 0, b] = u, v
+            want[r, 0, a], want[r, 0, b] = u * c - v * s, u * s + v * c
+            size[r, 0, a] = size[r, 0, b] = abs(u) + abs(v)
+    q = torch.tensor(x).bfloat16().cuda()
+    assert np.array_equal(q.double().cpu().numpy(), x)
+    assert (size > 0).mean() > 0.4 * rot / 128
+    y = ea.attn_rope(q, None, inv, i32(positions), interleaved=interleaved)[0]
+    ref.check_rotated(y, want, size)

@@ -660,7 +660,9 @@ def attn_rope_inv_freq(rotary_dim: int, base: float = 10000.0, *, scaling: str =
     stretches it for contexts longer than the trained one: "linear" (every
     frequency / factor), "base" (a larger base: the slowest pair / factor) or
     "ramp" (pairs that turn more than ramp[1] times over original_length are
-    kept, those that turn less than ramp[0] times / factor)."""
+    kept, those that turn less than ramp[0] times / factor, linear in the turns
+    between; a model whose ramp is linear in the pair's index needs its own
+    inv_freq)."""
     torch = _torch()
     if scaling not in _ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}")

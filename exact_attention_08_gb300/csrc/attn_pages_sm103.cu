@@ -29,10 +29,12 @@
 // included.  Rows of more than 512 pages are walked by whole CTAs, and by
 // several blocks of the finishing kernel: with a warp (a block) a row, one row
 // of 65,536 pages took 527 us to grow, 1,155 to free and 64 to fork, now 32,
-// 84 and 15; short rows pay 0.4 us for it.  The finishing kernel is bound by
-// bytes: a compaction of 16,384 pages that moves 3,932 of 64 KB (515 MB read
-// and written) takes 84.3 us in all, 91 % of a copy's measured rate, with 32
-// blocks for every SM (8: 90.5 us; blocks that all run at once keep in step).
+// 84 and 15; calls on short rows pay 0.4 to 0.8 us for it.  The scan of the
+// counts grows with the pool: a decode step of 64 rows takes 7.4 us over
+// 65,792 pages, 20 over 2^20 and 35 over 2^21.  The finishing kernel is bound
+// by bytes: a compaction of 16,384 pages that moves 3,932 of 64 KB (515 MB
+// read and written) takes 84.3 us in all, 91 % of a copy's measured rate, with
+// 32 blocks for every SM (8: 90.5 us).
 #include "attn_internal.h"
 #include "sm103_ptx.cuh"
 
@@ -45,7 +47,10 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVecs = 4;  // 16-byte vectors in flight per thread
-constexpr int kLong = 512;    // table entries of a row from which a whole CTA walks them
+// Table entries of a row past which a whole CTA walks them.  64 rows grown and
+// freed in turn: of 200 pages 10.0 us by warps, 11.3 by CTAs; of 600 pages
+// 17.8 and 11.9.  The two meet between 200 and 400.
+constexpr int kLong = 512;
 constexpr int kAtOnce = 4;    // table entries in flight per thread
 constexpr int kSegment = kCopyThreads * kAtOnce;  // table entries of a finishing block's step
 

@@ -24,10 +24,12 @@
 // its loads are issued before the angles are formed, which hides the
 // position's and frequencies' latency.
 //
-// Bound: bytes.  Measured (one GB300, device time of a call in a graph): q, k
-// of 2 x 4096 rows, 32 + 8 heads, d = 128, 167.8 MB moved: 27.9 us, 6.0 TB/s,
-// 90 % of a copy's measured rate (a copy of those bytes takes 26.4 us); 8192
-// rows, 16 + 16 heads, 134.3 MB: 20.3 us (copy 21.5).  On the first, fp64
+// Bound: bytes.  Measured (one GB300, device time of a call in a graph, inputs
+// and outputs rotating over buffers past L2): q, k of 2 x 4096 rows, 32 + 8
+// heads, d = 128, 167.8 MB moved: 27.7 us, 6.1 TB/s, 91 % of a copy's
+// measured rate (a copy of those bytes takes 26.4 us); 8192 rows, 16 + 16
+// heads, 134.2 MB: 22.7 us (copy 21.6; 19.8 into the same outputs each time,
+// which L2 holds in part).  On the first, into outputs used again, fp64
 // angles took 28.4 us, warps that each formed the angles of their own heads
 // 31.1 us, a block for three rows with a division per unit 33.3 us; packed
 // fp32 instructions 28.8 us (more registers, fewer blocks on an SM).
@@ -347,8 +349,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
   }
 }
 
-// Any even rot: one pair per thread, 2-byte loads and stores.  Vectors of
-// eight would straddle the middle of the rotated part.  A warp takes one row.
+// Any even rot: one pair per thread, 2-byte loads and stores.  In the half
+// layout vectors of eight would straddle the middle of the rotated part; the
+// interleaved one, whose vectors are whole pairs, shares the kernel.  A warp
+// takes one row.  Far from the floor: 2 x 4096 rows of 32 + 8 heads, d = 128,
+// rot = 20 take 101 us in either layout (25 at a copy's rate), 64 rows 23 us.
 template <bool kAppend>
 __global__ void __launch_bounds__(kThreads)
     attn_rope_pairs_kernel(const __grid_constant__ RopeArgs p,

@@ -380,7 +380,9 @@ ATTN_API int attn_decode_paged_noalloc(const void* q, const void* k_pages, const
  * attn_rope_inv_freq fills the HOST array inv_freq [rotary_dim / 2] with
  * f_i = base^(-2 i / rotary_dim), stretched as `scaling` says (factor for all
  * but ATTN_ROPE_NONE; original_length, ramp_low and ramp_high for
- * ATTN_ROPE_RAMP).  ATTN_ERR_INVALID_ARG, and nothing written, where the
+ * ATTN_ROPE_RAMP).  The ramp is linear in the turns, not in the pair's index:
+ * a model whose ramp runs over the index needs frequencies computed by its own
+ * formula.  ATTN_ERR_INVALID_ARG, and nothing written, where the
  * stretched base or a frequency is out of fp64's range.  Host only, no CUDA
  * call.
  */
@@ -477,7 +479,9 @@ ATTN_API int attn_append_paged(const void* q, const void* k, const void* v, void
  *     undefined contents, never an access outside the buffers.
  *   k_pages, v_pages: the pools of `layers` layers that share the table,
  *     [layers, num_pages_total, 16, Hkv, d] bf16 (layer l's pool is what the
- *     attention calls take).
+ *     attention calls take).  A call changes the table once for all layers, so
+ *     a cache with a pool per layer keeps those as the slices of one
+ *     allocation; calls layer by layer are not possible.
  *   Pages are taken lowest index first, by the rows in order, so equal calls
  *     give equal tables.
  *   workspace: DEVICE, 16-byte aligned, attn_pages_workspace_size(rows,

@@ -39,6 +39,8 @@ __all__ = [
     "attn_decode_workspace_size", "attn_decode_paged", "attn_decode_paged_sink", "attn_device_status", "attn_check_wait_timeout", "attn_status_string",
     "attn_rope_inv_freq", "attn_rope", "attn_rope_bwd", "attn_append_paged",
     "attn_pages_workspace_size", "attn_pages_resize", "attn_pages_fork", "attn_pages_compact",
+    "attn_decode_mass_workspace_size", "attn_decode_paged_mass",
+    "attn_evict_workspace_size", "attn_evict_paged",
     "attn_last_error", "library_path", "lib",
 ]
 
@@ -96,6 +98,14 @@ def _load() -> ctypes.CDLL:
     L.attn_pages_resize.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp, sz, vp]
     L.attn_pages_fork.argtypes = [vp, vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, i, i, vp, sz, vp]
     L.attn_pages_compact.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp, sz, vp]
+    L.attn_decode_mass_workspace_size.argtypes = [i, i, i, i, i]
+    L.attn_decode_mass_workspace_size.restype = sz
+    L.attn_decode_paged_mass.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i,
+                                         i, i, i, i, f, vp, vp, sz, vp]
+    L.attn_evict_workspace_size.argtypes = [i, i, i, i, i]
+    L.attn_evict_workspace_size.restype = sz
+    L.attn_evict_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, i,
+                                   vp, sz, vp]
     L.attn_device_status.argtypes = [vp]
     L.attn_check_wait_timeout.argtypes = [i, vp]
     L.attn_status_string.argtypes = [i]
@@ -107,6 +117,7 @@ def _load() -> ctypes.CDLL:
                "attn_decode_paged",
                "attn_decode_paged_sink", "attn_rope_inv_freq", "attn_rope", "attn_rope_bwd",
                "attn_append_paged", "attn_pages_resize", "attn_pages_fork", "attn_pages_compact",
+               "attn_decode_paged_mass", "attn_evict_paged",
                "attn_device_status", "attn_check_wait_timeout"):
         getattr(L, fn).restype = ctypes.c_int
     return L
@@ -926,6 +937,198 @@ def attn_pages_compact(page_table, seqlens, refs, k_pages, v_pages, *, workspace
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_pages_compact")
     return new_index, num_live
+
+
+# ---------------------------------------------------------------- shared and thinned caches
+
+def _contiguous(t, name, dtype, index):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype or t.get_device() != index or index < 0 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{index}")
+
+
+def _paged_rows(page_table, seqlens, index):
+    """(B, max_pages)"""
+    _int_tensor(page_table, "page_table", index)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, W = page_table.shape
+    _int_vector(seqlens, "seqlens", B, index)
+    return B, W
+
+
+def _pool(q, k_pages, v_pages, index):
+    """(P, page size, Hkv) of pools that fit q [.., Hq, d]."""
+    torch = _torch()
+    _contiguous(k_pages, "k_pages", torch.bfloat16, index)
+    if v_pages is not None:
+        _contiguous(v_pages, "v_pages", torch.bfloat16, index)
+    shape = k_pages.shape
+    if len(shape) != 4 or (v_pages is not None and v_pages.shape != shape) or \
+            shape[3] != q.shape[-1]:
+        raise ValueError("k_pages/v_pages shapes disagree with q")
+    return shape[0], shape[1], shape[2]
+
+
+def _bytes(n, index, workspace):
+    """A workspace of n bytes, or the caller's."""
+    torch = _torch()
+    if workspace is None:
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=torch.device("cuda", index))
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or \
+            workspace.get_device() != index:
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    return workspace
+
+
+def _decode_outputs(q, o, lse, want_lse, index):
+    torch = _torch()
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _contiguous(o, "o", torch.bfloat16, index)
+        if o.shape != q.shape:
+            raise ValueError("o must be shaped like q")
+    if lse is None:
+        if want_lse:
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    else:
+        _contiguous(lse, "lse", torch.float32, index)
+        if lse.shape != q.shape[:2]:
+            raise ValueError("lse must be [B, Hq]")
+    return o, lse
+
+
+def _sink(sink_logit, Hq, index):
+    if sink_logit is None:
+        return None
+    _contiguous(sink_logit, "sink_logit", _torch().float32, index)
+    if sink_logit.numel() != Hq:
+        raise ValueError(f"sink_logit must hold Hq={Hq} values")
+    return sink_logit.data_ptr()
+
+
+def _mass_tensors(mass, mass_out, positions, last_positions, B, Hkv, index):
+    """(mass_out, slots)"""
+    torch = _torch()
+    _contiguous(mass, "mass", torch.float32, index)
+    shape = mass.shape
+    if len(shape) != 3 or shape[0] != B or shape[1] != Hkv:
+        raise ValueError(f"mass must be [{B}, {Hkv}, slots], got {list(shape)}")
+    if mass_out is None:
+        mass_out = mass
+    else:
+        _contiguous(mass_out, "mass_out", torch.float32, index)
+        if mass_out.shape != shape:
+            raise ValueError("mass_out must be shaped like mass")
+    if positions is not None:
+        _int_tensor(positions, "positions", index)
+        if positions.shape != shape:
+            raise ValueError("positions must be shaped like mass")
+    if last_positions is not None:
+        _int_vector(last_positions, "last_positions", B, index)
+    return mass_out, shape[2]
+
+
+@functools.lru_cache(maxsize=256)
+def attn_decode_mass_workspace_size(B: int, Hq: int, d: int, max_pages: int,
+                                    num_splits: int) -> int:
+    return int(lib.attn_decode_mass_workspace_size(*map(_c_int, (B, Hq, d, max_pages,
+                                                                 num_splits))))
+
+
+def attn_decode_paged_mass(q, k_pages, v_pages, page_table, seqlens, mass, positions=None,
+                           last_positions=None, o=None, lse=None, *, mass_out=None,
+                           sink_logit=None, num_splits=8, scale=None, workspace=None, stream=None,
+                           want_lse=True):
+    """attn_decode_paged (with sink_logit: attn_decode_paged_sink), and the softmax weight of
+    every key, summed over the query heads that read it, added to mass [B,Hkv,slots] fp32
+    (into mass_out if given, else in place).  The newest token's mass starts here, and its
+    slot of positions [B,Hkv,slots] int32 becomes last_positions [B] (None: its slot's
+    number) -> (o, lse)."""
+    torch = _torch()
+    index = q.get_device() if isinstance(q, torch.Tensor) else -1
+    _contiguous(q, "q", torch.bfloat16, index)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, d]")
+    B, Hq, d = q.shape
+    P, page, Hkv = _pool(q, k_pages, v_pages, index)
+    Bt, W = _paged_rows(page_table, seqlens, index)
+    if Bt != B:
+        raise ValueError("page_table must be [B, max_pages] and seqlens [B]")
+    mass_out, slots = _mass_tensors(mass, mass_out, positions, last_positions, B, Hkv, index)
+    sink = _sink(sink_logit, Hq, index)
+    if stream is not None or index != _current_device():
+        with _Call(index, stream):
+            return attn_decode_paged_mass(q, k_pages, v_pages, page_table, seqlens, mass,
+                                          positions, last_positions, o, lse, mass_out=mass_out,
+                                          sink_logit=sink_logit, num_splits=num_splits,
+                                          scale=scale, workspace=workspace, want_lse=want_lse)
+    o, lse = _decode_outputs(q, o, lse, want_lse, index)
+    B, W, P, slots, num_splits = map(_c_int, (B, W, P, slots, int(num_splits)))
+    ws = _bytes(attn_decode_mass_workspace_size(B, Hq, d, W, num_splits), index, workspace)
+    rc = lib.attn_decode_paged_mass(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+        seqlens.data_ptr(), mass.data_ptr(), mass_out.data_ptr(), _ptr(positions),
+        _ptr(last_positions), o.data_ptr(), _ptr(lse), B, Hq, Hkv, d, page, W, P, slots,
+        num_splits, d ** -0.5 if scale is None else float(scale), sink, ws.data_ptr(), ws.nbytes,
+        _raw_stream(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_decode_paged_mass")
+    return o, lse
+
+
+@functools.lru_cache(maxsize=256)
+def attn_evict_workspace_size(layers: int, B: int, Hkv: int, slots: int, max_pages: int) -> int:
+    return int(lib.attn_evict_workspace_size(*map(_c_int, (layers, B, Hkv, slots, max_pages))))
+
+
+def attn_evict_paged(mass, positions, page_table, seqlens, keep, k_pages, v_pages, refs=None,
+                     new_seqlens=None, *, n_sink=0, recent=0, workspace=None, stream=None):
+    """Cuts every row to keep [B] tokens, in place: those of the largest mass [layers,B,Hkv,
+    slots] stay, whatever their mass the ones at positions below n_sink and the `recent`
+    newest ones; tokens behind the budget move to evicted slots before it, in every layer of
+    k_pages, v_pages [layers,P,16,Hkv,d], mass and positions (without layers: [B,Hkv,slots],
+    [P,16,Hkv,d]).  refs [P]: as for attn_pages_resize, None if no rows share pages ->
+    new_seqlens [B] int32, to be passed to attn_pages_resize."""
+    torch = _torch()
+    index = mass.get_device() if isinstance(mass, torch.Tensor) else -1
+    _contiguous(mass, "mass", torch.float32, index)
+    _int_tensor(positions, "positions", index)
+    B, W = _paged_rows(page_table, seqlens, index)
+    _int_vector(keep, "keep", B, index)
+    shape = mass.shape
+    if positions.shape != shape or len(shape) not in (3, 4) or shape[-3] != B:
+        raise ValueError("mass and positions must both be [layers, B, Hkv, slots] or "
+                         "[B, Hkv, slots]")
+    _rows_tensor(k_pages, "k_pages", (len(shape) + 1,), index)
+    P = k_pages.shape[-4]
+    layers, page, Hkv, d = _cache_pools(k_pages, v_pages, P, index)
+    if shape[-2] != Hkv or (len(shape) == 4 and shape[0] != layers):
+        raise ValueError("mass and k_pages disagree in layers or heads")
+    if refs is not None:
+        _int_vector(refs, "refs", P, index)
+    if new_seqlens is not None:
+        _int_vector(new_seqlens, "new_seqlens", B, index)
+    if stream is not None or index != _current_device():
+        with _Call(index, stream):
+            return attn_evict_paged(mass, positions, page_table, seqlens, keep, k_pages, v_pages,
+                                    refs, new_seqlens, n_sink=n_sink, recent=recent,
+                                    workspace=workspace)
+    if new_seqlens is None:
+        new_seqlens = torch.empty_like(seqlens)
+    B, W, P, slots = map(_c_int, (B, W, P, shape[-1]))
+    ws = _bytes(attn_evict_workspace_size(layers, B, Hkv, slots, W), index, workspace)
+    rc = lib.attn_evict_paged(
+        mass.data_ptr(), positions.data_ptr(), page_table.data_ptr(), seqlens.data_ptr(),
+        keep.data_ptr(), _ptr(refs), new_seqlens.data_ptr(), k_pages.data_ptr(),
+        v_pages.data_ptr(), B, layers, Hkv, d, slots, page, W, P, _c_int(int(n_sink)),
+        _c_int(int(recent)), ws.data_ptr(), ws.nbytes, _raw_stream(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_evict_paged")
+    return new_seqlens
 
 
 def attn_device_status(stream=None) -> int:

@@ -127,6 +127,11 @@ int make_map(CUtensorMap* m, const void* ptr, uint64_t d, uint64_t n1, uint64_t 
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+int page_pool_map(CUtensorMap* m, const void* pool, int d, int Hkv, int num_pages,
+                  const char* what) {
+  return make_map(m, pool, d, Hkv, 16, num_pages, 16, what);
+}
+
 int device_info(int* num_sms, int** status) {
   DeviceState* s = nullptr;
   const int rc = device_state(&s);

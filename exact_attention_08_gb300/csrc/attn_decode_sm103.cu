@@ -36,7 +36,8 @@
 #include "sm103_ptx.cuh"
 
 #include <cuda_bf16.h>
-#include <mutex>
+
+#include <algorithm>
 
 namespace attn {
 namespace {
@@ -130,6 +131,12 @@ __global__ void __launch_bounds__(kOrderThreads)
   for (int b = t; b < B; b += kOrderThreads) order[atomicAdd(&cnt[bucket(b)], 1)] = b;
 }
 
+// What a split kernel does besides the decode:
+//   kDecMass    stores the raw scores q.k of its pages, for the keys' masses;
+//   kDecShared  takes only a request's pages from start[b] on, the ones before
+//               them being done once for a whole group elsewhere.
+enum DecMode { kDecPlain = 0, kDecMass = 1, kDecShared = 2 };
+
 struct DecParams {
   const __nv_bfloat16* q;
   const int* page_table;
@@ -137,6 +144,8 @@ struct DecParams {
   float* ws_o;
   float* ws_lse;
   const int* order;  // [B] requests longest first (the grid's z order)
+  float* scores;     // kDecMass: [B, Hq, max_pages * 16] raw scores
+  const int* start;  // kDecShared: [B] first page of a request's own
   int B, Hq, Hkv, G, n_hchunks, max_pages, num_pages, num_splits;
   float scale, scale2;
   uint64_t wait_limit_ns;
@@ -172,7 +181,29 @@ __device__ __forceinline__ uint32_t swz(int token, int e) {
   return token * 128 + ((((e >> 3) ^ token) & 7) << 4) + (e & 7) * 2;
 }
 
-template <int D>
+// kDecShared: the merge that follows waits for this grid alone, so one CTA of it
+// leaves only after the prefix kernel before it.
+__device__ __forceinline__ void leave_after_prefix() {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == gridDim.z - 1)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Raw scores of a page from the product's fragment: heads r and r + 8, tokens
+// t, t + 1, t + 8, t + 9.
+__device__ __forceinline__ void store_scores(const DecParams& p, int b, int h0, int nh, int r,
+                                             int t, const float (*sc)[4]) {
+  const size_t slots = static_cast<size_t>(p.max_pages) * kPage;
+#pragma unroll
+  for (int hr = 0; hr < 2; ++hr) {
+    if (r + 8 * hr >= nh) continue;
+    float* to = p.scores + (static_cast<size_t>(b) * p.Hq + h0 + r + 8 * hr) * slots + t;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+      *reinterpret_cast<float2*>(to + nt * 8) = make_float2(sc[nt][2 * hr], sc[nt][2 * hr + 1]);
+  }
+}
+
+template <int D, int kMode>
 __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
     attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
                              const __grid_constant__ CUtensorMap tmV, const DecParams p) {
@@ -189,8 +220,9 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
   const int hkv = blockIdx.y / p.n_hchunks;
   const int hchunk = blockIdx.y % p.n_hchunks;
   // Launched as a programmatic dependent of the order kernel: the launch
-  // overlaps it, and this waits for its result.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // overlaps it, and this waits for its result.  (kDecShared: of the prefix
+  // kernel, which lets this one start only once it has itself seen the order.)
+  if constexpr (kMode != kDecShared) asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = p.order[blockIdx.z];
   const int g0 = hchunk * kHeadsPerCta;                  // first group member served
   const int nh = min(kHeadsPerCta, p.G - g0);            // query heads served
@@ -202,8 +234,9 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
     L = max(0, min(L, p.max_pages * kPage));
   }
   const int np = (L + kPage - 1) / kPage;
-  const int pps = (np + p.num_splits - 1) / p.num_splits;
-  const int pg0 = min(split * pps, np);
+  const int first = kMode == kDecShared ? min(p.start[b], np) : 0;
+  const int pps = (np - first + p.num_splits - 1) / p.num_splits;
+  const int pg0 = min(first + split * pps, np);
   const int pg1 = min(pg0 + pps, np);
   const int npg = pg1 - pg0;
 
@@ -313,6 +346,9 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
         for (int e = 0; e < 4; ++e)
           if (tok_base + nt * 8 + cpair + (e & 1) >= L) sc[nt][e] = -INFINITY;
 
+      if constexpr (kMode == kDecMass) {
+        store_scores(p, b, h0, nh, r_lo, tok_base + cpair, sc);
+      }
       // ---- online softmax over the page (rows r_lo: e = 0,1; r_lo + 8: e = 2,3)
       float mx_lo = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
       float mx_hi = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
@@ -422,6 +458,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
     while (globaltimer_ns() - t0 < 2000000ull) {
     }
   }
+  if constexpr (kMode == kDecShared) leave_after_prefix();
 }
 
 // Head dimension 256.  One accumulator tile of 16 query heads x 256 columns
@@ -446,6 +483,7 @@ struct Dec256 {
   static constexpr int kSmemBytes = kOffBar + 2 * kStages256 * 8 + 1024;
 };
 
+template <int kMode>
 __global__ void __launch_bounds__(kDecThreads, 2)
     attn_decode_split256_kernel(const __grid_constant__ CUtensorMap tmK,
                                 const __grid_constant__ CUtensorMap tmV, const DecParams p) {
@@ -464,8 +502,9 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   const int hkv = blockIdx.y / p.n_hchunks;
   const int hchunk = blockIdx.y % p.n_hchunks;
   // Launched as a programmatic dependent of the order kernel: the launch
-  // overlaps it, and this waits for its result.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // overlaps it, and this waits for its result.  (kDecShared: of the prefix
+  // kernel, which lets this one start only once it has itself seen the order.)
+  if constexpr (kMode != kDecShared) asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = p.order[blockIdx.z];
   const int g0 = hchunk * kHeadsPerCta;
   const int nh = min(kHeadsPerCta, p.G - g0);
@@ -477,8 +516,9 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     L = max(0, min(L, p.max_pages * kPage));
   }
   const int np = (L + kPage - 1) / kPage;
-  const int pps = (np + p.num_splits - 1) / p.num_splits;
-  const int pg0 = min(split * pps, np);
+  const int first = kMode == kDecShared ? min(p.start[b], np) : 0;
+  const int pps = (np - first + p.num_splits - 1) / p.num_splits;
+  const int pg0 = min(first + split * pps, np);
   const int pg1 = min(pg0 + pps, np);
   const int npg = pg1 - pg0;
 
@@ -581,6 +621,9 @@ __global__ void __launch_bounds__(kDecThreads, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (tok_base + nt * 8 + cpair + (e & 1) >= L) sc[nt][e] = -INFINITY;
+      if constexpr (kMode == kDecMass) {
+        if (half == 0) store_scores(p, b, h0, nh, r_lo, tok_base + cpair, sc);
+      }
       float mx_lo = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
       float mx_hi = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
       mx_lo = fmaxf(mx_lo, __shfl_xor_sync(0xffffffffu, mx_lo, 1));
@@ -662,6 +705,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     while (globaltimer_ns() - t0 < 2000000ull) {
     }
   }
+  if constexpr (kMode == kDecShared) leave_after_prefix();
 }
 
 // Merge of the split partials, ascending split order (deterministic).
@@ -716,16 +760,111 @@ cudaError_t launch_combine(const DecodeLaunch& a, cudaStream_t stream) {
                             static_cast<__nv_bfloat16*>(a.o), a.lse, a.num_splits, a.sink, a.Hq);
 }
 
-// The request order, then the split kernel as its programmatic dependent.
-template <typename Kernel>
-cudaError_t launch_ordered(const DecodeLaunch& a, Kernel kernel, dim3 grid, size_t smem,
-                           const DecParams& p, cudaStream_t stream) {
-  attn_decode_order_kernel<<<1, kOrderThreads, 0, stream>>>(a.seqlens, a.B, a.max_pages, a.order);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+// Accumulated attention weight of a decode step, and the merge, in one launch:
+// both need every split's log-sum-exp.  Of the blocks along x the first merge_blocks
+// merge (the arithmetic of attn_decode_combine_kernel, kMassThreads / D query heads
+// each), the others take kMassTokens tokens each: they merge the log-sum-exps
+// of the group's heads (a warp a head), then w = sum over the heads of
+// 2^(s scale2 - LSE log2 e), heads in order, and mass_out = mass + w.  The newest
+// token's mass is w alone, and its position is noted.  Bound by bytes: the raw scores
+// (4 G a token, written by the split kernel just before and in L2 in part) and the mass.
+constexpr int kMassThreads = 256;
+constexpr int kMassTokens = 4 * kMassThreads;
+constexpr int kMassHeads = 64;  // log-sum-exps held at a time
+
+template <int D>
+__global__ void __launch_bounds__(kMassThreads)
+    attn_decode_mass_kernel(const DecodeLaunch a, int merge_blocks) {
+  __shared__ float s_lse2[kMassHeads];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int hkv = blockIdx.y, b = blockIdx.z;
+  const int G = a.Hq / a.Hkv, S = a.num_splits, tid = threadIdx.x;
+  const size_t row0 = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(hkv) * G;
+  if (static_cast<int>(blockIdx.x) < merge_blocks) {
+    const int g = blockIdx.x * (kMassThreads / D) + tid / D;
+    if (g >= G) return;
+    const int t = tid % D;
+    const size_t row = row0 + g;
+    const float* ls = a.ws_lse + row * S;
+    const float sg = a.sink ? a.sink[hkv * G + g] : -INFINITY;
+    float M = sg;
+    for (int s = 0; s < S; ++s) M = fmaxf(M, ls[s]);
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o);
+    if (M == -INFINITY) {
+      o[row * D + t] = __float2bfloat16(0.f);
+      if (a.lse && t == 0) a.lse[row] = -INFINITY;
+      return;
+    }
+    float wsum = (sg == -INFINITY) ? 0.f : expf(sg - M), acc = 0.f;
+    for (int s = 0; s < S; ++s) {
+      const float w = expf(ls[s] - M);
+      wsum += w;
+      acc += w * a.ws_o[(row * S + s) * D + t];
+    }
+    o[row * D + t] = __float2bfloat16(acc / wsum);
+    if (a.lse && t == 0) a.lse[row] = M + logf(wsum);
+    return;
+  }
+  const int L = a.seqlens[b];
+  if (L < 0 || L > min(a.max_pages * kPage, a.mass_slots)) {
+    if (tid == 0) atomicOr(a.status, kStatusBadInput);
+    return;
+  }
+  const int t0 = (blockIdx.x - merge_blocks) * kMassTokens;
+  if (t0 >= L) return;
+  const size_t slots = static_cast<size_t>(a.max_pages) * kPage;
+  const float scale2 = a.scale * kLog2eDec;
+  const int warp = tid >> 5, lane = tid & 31;
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
+  const int t = t0 + tid * 4;  // the raw scores of a token beyond L are -inf or not read
+  for (int c = 0; c < G; c += kMassHeads) {
+    const int n = min(G - c, kMassHeads);
+    __syncthreads();
+    for (int g = warp; g < n; g += kMassThreads / 32) {
+      const float* ls = a.ws_lse + (row0 + c + g) * S;
+      const float sg = a.sink ? a.sink[hkv * G + c + g] : -INFINITY;
+      const float l0 = lane < S ? ls[lane] : -INFINITY;
+      const float l1 = lane + 32 < S ? ls[lane + 32] : -INFINITY;
+      float M = fmaxf(fmaxf(l0, l1), sg);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      float sum = expf(l0 - M) + expf(l1 - M);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      sum += expf(sg - M);
+      if (lane == 0) s_lse2[g] = (M + logf(sum)) * kLog2eDec;
+    }
+    __syncthreads();
+    if (t < L) {
+      const float* sc = a.ws_scores + (row0 + c) * slots + t;
+      for (int g = 0; g < n; ++g) {
+        const float4 x = *reinterpret_cast<const float4*>(sc + g * slots);
+        const float l2 = s_lse2[g];
+        w[0] += ex2_approx(fmaf(x.x, scale2, -l2));
+        w[1] += ex2_approx(fmaf(x.y, scale2, -l2));
+        w[2] += ex2_approx(fmaf(x.z, scale2, -l2));
+        w[3] += ex2_approx(fmaf(x.w, scale2, -l2));
+      }
+    }
+  }
+  if (t >= L) return;
+  const size_t at = (static_cast<size_t>(b) * a.Hkv + hkv) * a.mass_slots + t;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (t + j >= L) break;
+    const bool newest = t + j == L - 1;
+    a.mass_out[at + j] = newest ? w[j] : a.mass[at + j] + w[j];
+    if (newest && a.positions != nullptr)
+      a.positions[at + j] = a.last_positions ? a.last_positions[b] : L - 1;
+  }
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kDecThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -733,82 +872,78 @@ cudaError_t launch_ordered(const DecodeLaunch& a, Kernel kernel, dim3 grid, size
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a.tmK, a.tmV, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+DecParams split_params(const DecodeLaunch& a) {
+  DecParams p;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.page_table = a.page_table;
+  p.seqlens = a.seqlens;
+  p.ws_o = a.ws_o;
+  p.ws_lse = a.ws_lse;
+  p.order = a.order;
+  p.scores = a.ws_scores;
+  p.start = a.start;
+  p.B = a.B;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.G = a.Hq / a.Hkv;
+  p.n_hchunks = (p.G + kHeadsPerCta - 1) / kHeadsPerCta;
+  p.max_pages = a.max_pages;
+  p.num_pages = a.num_pages;
+  p.num_splits = a.num_splits;
+  p.scale = a.scale;
+  p.scale2 = a.scale * kLog2eDec;
+  p.wait_limit_ns = kWaitLimitNs;
+  p.status = a.status;
+  return p;
+}
+
+// The split kernel as a programmatic dependent of the launch before it.
+template <int D, int kMode>
+cudaError_t launch_split(const DecodeLaunch& a, cudaStream_t stream) {
+  const DecParams p = split_params(a);
+  const dim3 grid(a.num_splits, a.Hkv * p.n_hchunks, a.B);
+  static SharedMemoryLimit limit;
+  if constexpr (D == 256) {
+    constexpr int kBytes = Dec256::kSmemBytes;
+    const cudaError_t e = limit.raise(attn_decode_split256_kernel<kMode>, kBytes);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(attn_decode_split256_kernel<kMode>, grid, kDecThreads, kBytes, stream,
+                            a.tmK, a.tmV, p);
+  } else {
+    constexpr int kBytes = DecCfg<D>::kSmemBytes;
+    const cudaError_t e = limit.raise(attn_decode_split_kernel<D, kMode>, kBytes);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(attn_decode_split_kernel<D, kMode>, grid, kDecThreads, kBytes, stream,
+                            a.tmK, a.tmV, p);
+  }
+}
+
+// The request order, the splits, the merge (and the masses).
 template <int D>
 cudaError_t launch_dec(const DecodeLaunch& a, cudaStream_t stream) {
-  using C = DecCfg<D>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(attn_decode_split_kernel<D>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-  });
-  if (attr_err != cudaSuccess) return attr_err;
-  DecParams p;
-  p.q = static_cast<const __nv_bfloat16*>(a.q);
-  p.page_table = a.page_table;
-  p.seqlens = a.seqlens;
-  p.ws_o = a.ws_o;
-  p.ws_lse = a.ws_lse;
-  p.B = a.B;
-  p.Hq = a.Hq;
-  p.Hkv = a.Hkv;
-  p.G = a.Hq / a.Hkv;
-  p.n_hchunks = (p.G + kHeadsPerCta - 1) / kHeadsPerCta;
-  p.max_pages = a.max_pages;
-  p.num_pages = a.num_pages;
-  p.num_splits = a.num_splits;
-  p.scale = a.scale;
-  p.scale2 = a.scale * kLog2eDec;
-  p.wait_limit_ns = kWaitLimitNs;
-  p.status = a.status;
-  dim3 grid(a.num_splits, a.Hkv * p.n_hchunks, a.B);
-  p.order = a.order;
-  cudaError_t e =
-      launch_ordered(a, attn_decode_split_kernel<D>, grid, C::kSmemBytes, p, stream);
-  if (e == cudaSuccess) e = cudaGetLastError();
+  attn_decode_order_kernel<<<1, kOrderThreads, 0, stream>>>(a.seqlens, a.B, a.max_pages, a.order);
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = launch_combine<D>(a, stream);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-
-cudaError_t launch_dec256(const DecodeLaunch& a, cudaStream_t stream) {
-  using C = Dec256;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(attn_decode_split256_kernel,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-  });
-  if (attr_err != cudaSuccess) return attr_err;
-  DecParams p;
-  p.q = static_cast<const __nv_bfloat16*>(a.q);
-  p.page_table = a.page_table;
-  p.seqlens = a.seqlens;
-  p.ws_o = a.ws_o;
-  p.ws_lse = a.ws_lse;
-  p.B = a.B;
-  p.Hq = a.Hq;
-  p.Hkv = a.Hkv;
-  p.G = a.Hq / a.Hkv;
-  p.n_hchunks = (p.G + kHeadsPerCta - 1) / kHeadsPerCta;
-  p.max_pages = a.max_pages;
-  p.num_pages = a.num_pages;
-  p.num_splits = a.num_splits;
-  p.scale = a.scale;
-  p.scale2 = a.scale * kLog2eDec;
-  p.wait_limit_ns = kWaitLimitNs;
-  p.status = a.status;
-  dim3 grid(a.num_splits, a.Hkv * p.n_hchunks, a.B);
-  p.order = a.order;
-  cudaError_t e = launch_ordered(a, attn_decode_split256_kernel, grid, C::kSmemBytes, p, stream);
-  if (e == cudaSuccess) e = cudaGetLastError();
+  if (a.mass_out == nullptr) {
+    e = launch_split<D, kDecPlain>(a, stream);
+    if (e != cudaSuccess) return e;
+    e = launch_combine<D>(a, stream);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
+  e = launch_split<D, kDecMass>(a, stream);
   if (e != cudaSuccess) return e;
-  e = launch_combine<256>(a, stream);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const int G = a.Hq / a.Hkv, per = kMassThreads / D;
+  const int merge_blocks = (G + per - 1) / per;
+  const long long slots = std::min<long long>(static_cast<long long>(a.max_pages) * kPage,
+                                              a.mass_slots);
+  const dim3 grid(static_cast<unsigned>(merge_blocks + (slots + kMassTokens - 1) / kMassTokens),
+                  a.Hkv, a.B);
+  return launch_dependent(attn_decode_mass_kernel<D>, grid, kMassThreads, 0, stream, a,
+                          merge_blocks);
 }
 
 }  // namespace
@@ -816,7 +951,14 @@ cudaError_t launch_dec256(const DecodeLaunch& a, cudaStream_t stream) {
 cudaError_t launch_attn_decode(const DecodeLaunch& a, cudaStream_t stream) {
   if (a.d == 128) return launch_dec<128>(a, stream);
   if (a.d == 64) return launch_dec<64>(a, stream);
-  if (a.d == 256) return launch_dec256(a, stream);
+  if (a.d == 256) return launch_dec<256>(a, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_attn_decode_own(const DecodeLaunch& a, cudaStream_t stream) {
+  if (a.d == 128) return launch_split<128, kDecShared>(a, stream);
+  if (a.d == 64) return launch_split<64, kDecShared>(a, stream);
+  if (a.d == 256) return launch_split<256, kDecShared>(a, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -2,6 +2,7 @@
 // units.  Not installed; not part of the public ABI.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -53,6 +54,14 @@ struct DecodeLaunch {
   float* ws_o;    // [B, Hq, S, d] fp32 split outputs (normalised)
   float* ws_lse;  // [B, Hq, S] fp32 split log-sum-exps (natural log)
   int* order;     // [B] workspace: the requests longest first
+  // masses of the keys (all null without)
+  float* ws_scores;  // [B, Hq, max_pages * 16] raw scores
+  const float* mass;  // [B, Hkv, mass_slots]
+  float* mass_out;
+  int* positions;             // [B, Hkv, mass_slots], may be null
+  const int* last_positions;  // [B], may be null
+  int mass_slots;
+  const int* start;  // first page of a request's own (shared prefixes), or null
   int B, Hq, Hkv, d, page, max_pages, num_pages, num_splits;
   float scale;
   int* status;
@@ -138,6 +147,48 @@ struct PagesArgs {
 
 size_t pages_workspace_bytes(int rows, int num_pages);
 
+constexpr int kEvictMaxUnits = 1 << 24;  // layers x rows x key heads of one call
+
+// Rows cut to their budget by accumulated attention weight.
+struct EvictArgs {
+  float* mass;     // [layers, B, Hkv, slots]
+  int* positions;  // [layers, B, Hkv, slots]
+  const int* page_table;  // [B, max_pages]
+  const int* seqlens;     // [B]
+  const int* keep;        // [B]
+  const int* refs;        // [num_pages], or null
+  int* new_seqlens;       // [B] out
+  uint4* k_pages;         // [layers, num_pages, 16, Hkv, d]
+  uint4* v_pages;
+  int units;  // layers * B * Hkv
+  int B, Hkv, slots, max_pages, num_pages;
+  int vecs;        // 16-byte vectors of a head: d / 8
+  int most_moves;  // half the slots a row can use
+  int n_sink, recent;
+  int copy_blocks;  // blocks that move a unit's keys and values (set by the launcher)
+  int* ws;          // moves of every unit (pairs), then their counts
+  int* status;
+};
+
+// Dynamic shared memory past 48 KB is allowed kernel by kernel, on each device once.
+class SharedMemoryLimit {
+ public:
+  template <typename Kernel>
+  cudaError_t raise(Kernel* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+};
+
 // Host-side helpers shared by the C-ABI translation units.
 int set_error(int code, const char* fmt, ...);
 int cuda_error(cudaError_t e, const char* what);
@@ -145,6 +196,10 @@ void clear_error();
 // The current device's SM count and status word (checks that it is sm_103).
 int device_info(int* num_sms, int** status);
 bool aligned16(const void* p);
+// Tensor map of a page pool [num_pages, 16, Hkv, d], boxes of one page of one head's 64
+// columns.
+int page_pool_map(CUtensorMap* m, const void* pool, int d, int Hkv, int num_pages,
+                  const char* what);
 
 // Bytes of workspace the backward needs (two fp32 row vectors per query row,
 // padded to whole 128-row tiles).
@@ -158,12 +213,15 @@ cudaError_t launch_attn_fwd(const FwdLaunch& a, cudaStream_t stream);
 cudaError_t launch_attn_fwd256(const FwdLaunch& a, cudaStream_t stream);
 cudaError_t launch_attn_fill_empty(const FwdLaunch& a, cudaStream_t stream);
 cudaError_t launch_attn_decode(const DecodeLaunch& a, cudaStream_t stream);
+// The splits of the requests' own pages, after the kernel of their shared ones.
+cudaError_t launch_attn_decode_own(const DecodeLaunch& a, cudaStream_t stream);
 cudaError_t launch_attn_rope(const RopeArgs& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_attn_append(const RopeArgs& p, const AppendArgs& ap, int num_sms,
                                cudaStream_t stream);
 cudaError_t launch_pages_resize(const PagesArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_fork(const PagesArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_compact(const PagesArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_evict(EvictArgs a, int num_sms, cudaStream_t stream);
 cudaError_t launch_wait_timeout_check(int* status, uint64_t limit_ns, cudaStream_t stream);
 
 }  // namespace attn

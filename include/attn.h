@@ -553,6 +553,83 @@ ATTN_API int attn_pages_compact(int* page_table, const int* seqlens, int* refs, 
                                 void* stream);
 
 /*
+ * Attention weight that the keys of a cache accumulate, and eviction by it.
+ * There is no counterpart on the source pages: these calls are additions of
+ * this library for caches that outgrow their memory.
+ *   mass [B, Hkv, mass_slots] DEVICE fp32: entry (b, h, t) belongs to slot t
+ *     of row b for key head h, and holds the sum, over the queries so far and
+ *     over the query heads that read key head h, of the key's softmax weight.
+ *     Entries of slots past a row's length are neither read nor written.
+ *   positions [B, Hkv, mass_slots] DEVICE int32: the position of the token in
+ *     that slot.  Before any eviction slot t holds position t in every head;
+ *     attn_evict_paged moves tokens head by head.
+ *   Both lie by row and slot, not by page: attn_pages_compact leaves them as
+ *   they are, a fork copies the parent's rows of them (the caller's part).
+ *
+ * attn_decode_paged_mass: attn_decode_paged (and _sink: sink_logit may be
+ * NULL), the same o and lse bit for bit, and for every row b of length L
+ *   w(b, h, t) = sum over the heads i of the group of
+ *                exp(scale q_i . k_t - LSE_i),              t < L
+ *   mass_out(b, h, t) = mass(b, h, t) + w for t < L - 1;  w for t = L - 1,
+ * whose token is new: its position becomes last_positions[b] (NULL: L - 1).
+ * mass_out may be mass; positions may be NULL.  A row longer than mass_slots,
+ * or with a length out of range, has its mass left as it was
+ * (ATTN_ERR_BAD_INPUT).  Sums run over the heads in order, in fp32.
+ *   workspace: attn_decode_mass_workspace_size(...) bytes (the decode's, and
+ *   the raw scores, fp32 [B, Hq, max_pages_per_seq * 16]), 16-byte aligned.
+ *   B and Hq at most 65,535.
+ */
+ATTN_API size_t attn_decode_mass_workspace_size(int B, int Hq, int d, int max_pages_per_seq,
+                                                int num_splits);
+ATTN_API int attn_decode_paged_mass(const void* q, const void* k_pages, const void* v_pages,
+                                    const int* page_table, const int* seqlens, const float* mass,
+                                    float* mass_out, int* positions, const int* last_positions,
+                                    void* o, float* lse, int B, int Hq, int Hkv, int d,
+                                    int page_size, int max_pages_per_seq, int num_pages_total,
+                                    int mass_slots, int num_splits, float scale,
+                                    const float* sink_logit, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
+ * Cuts rows to a budget: of each layer, row b and key head h the keep[b] tokens
+ * that rank highest stay, in slots 0 .. keep[b] - 1.
+ *   mass, positions [layers, B, Hkv, slots], k_pages, v_pages [layers,
+ *     num_pages_total, 16, Hkv, d] bf16 (all moved along), page_table and
+ *     seqlens as for the attention calls, keep [B] DEVICE int32.
+ *   Rank: first the tokens whose position is below n_sink or among the `recent`
+ *     newest (position > newest of the row and head - recent), then by mass,
+ *     largest first (NaN last); equal ones by slot, lowest first.  A keep[b]
+ *     below the number of protected tokens therefore keeps those of the lowest
+ *     slots.
+ *   Tokens that stay and are before slot keep[b] do not move; the k-th one
+ *     behind it goes to the k-th evicted slot before it.  The order of a row's
+ *     keys is lost, which attention without a window does not see: a window
+ *     over a thinned row is no longer one over positions.
+ *   new_seqlens [B] DEVICE int32 (out, not seqlens or keep): keep[b] where the
+ *     row was cut, else its length.  seqlens and the table are unchanged: pass
+ *     new_seqlens to attn_pages_resize, which gives the pages back.  Entries
+ *     of mass and positions from keep[b] on have no meaning afterwards.
+ *   refs [num_pages_total] DEVICE int32, the table's counts as for
+ *     attn_pages_resize, or NULL if no two rows share a page: a row that would
+ *     write to a page which another row holds too is left as it was.
+ *   A row of at most keep[b] tokens is left as it was.  Left as it was and
+ *     reported (ATTN_ERR_BAD_INPUT): a negative keep, a length below 0 or above
+ *     min(slots, max_pages_per_seq * 16), a page out of range, a shared page.
+ *   New tokens of a thinned row: their slots no longer are their positions, so
+ *     rotate q and k with attn_rope and append them with rotary_dim 0.
+ *   workspace: attn_evict_workspace_size(...) bytes, 16-byte aligned.  layers *
+ *   B * Hkv at most 2^24, B and Hkv at most 65,535.
+ */
+ATTN_API size_t attn_evict_workspace_size(int layers, int B, int Hkv, int slots,
+                                          int max_pages_per_seq);
+ATTN_API int attn_evict_paged(float* mass, int* positions, const int* page_table,
+                              const int* seqlens, const int* keep, const int* refs,
+                              int* new_seqlens, void* k_pages, void* v_pages, int B, int layers,
+                              int Hkv, int d, int slots, int page_size, int max_pages_per_seq,
+                              int num_pages_total, int n_sink, int recent, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
  * Synchronises `stream`, then returns and clears the device-side status word
  * of the current device (ATTN_OK, ATTN_ERR_TIMEOUT, ATTN_ERR_BAD_INPUT,
  * ATTN_ERR_NO_PAGES, or

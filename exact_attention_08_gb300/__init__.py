@@ -40,7 +40,7 @@ __all__ = [
     "attn_rope_inv_freq", "attn_rope", "attn_rope_bwd", "attn_append_paged",
     "attn_pages_workspace_size", "attn_pages_resize", "attn_pages_fork", "attn_pages_compact",
     "attn_decode_mass_workspace_size", "attn_decode_paged_mass",
-    "attn_evict_workspace_size", "attn_evict_paged",
+    "attn_mass_workspace_size", "attn_mass_paged", "attn_evict_workspace_size", "attn_evict_paged",
     "attn_last_error", "library_path", "lib",
 ]
 
@@ -102,6 +102,10 @@ def _load() -> ctypes.CDLL:
     L.attn_decode_mass_workspace_size.restype = sz
     L.attn_decode_paged_mass.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i,
                                          i, i, i, i, f, vp, vp, sz, vp]
+    L.attn_mass_workspace_size.argtypes = [i, i, i]
+    L.attn_mass_workspace_size.restype = sz
+    L.attn_mass_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i,
+                                  i, i, f, i, i, i, vp, sz, vp]
     L.attn_evict_workspace_size.argtypes = [i, i, i, i, i]
     L.attn_evict_workspace_size.restype = sz
     L.attn_evict_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, i,
@@ -117,7 +121,7 @@ def _load() -> ctypes.CDLL:
                "attn_decode_paged",
                "attn_decode_paged_sink", "attn_rope_inv_freq", "attn_rope", "attn_rope_bwd",
                "attn_append_paged", "attn_pages_resize", "attn_pages_fork", "attn_pages_compact",
-               "attn_decode_paged_mass", "attn_evict_paged",
+               "attn_decode_paged_mass", "attn_mass_paged", "attn_evict_paged",
                "attn_device_status", "attn_check_wait_timeout"):
         getattr(L, fn).restype = ctypes.c_int
     return L
@@ -1078,6 +1082,58 @@ def attn_decode_paged_mass(q, k_pages, v_pages, page_table, seqlens, mass, posit
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_paged_mass")
     return o, lse
+
+
+@functools.lru_cache(maxsize=256)
+def attn_mass_workspace_size(B: int, Hkv: int, max_pages: int) -> int:
+    return int(lib.attn_mass_workspace_size(*map(_c_int, (B, Hkv, max_pages))))
+
+
+def attn_mass_paged(q, lse, k_pages, page_table, cu_seqlens_q, seqlens_k, mass, positions=None,
+                    last_positions=None, new_tokens=None, *, max_seqlen_q=None, causal=True,
+                    window=0, n_sink=0, scale=None, mass_out=None, workspace=None, stream=None):
+    """After attn_fwd_paged of packed queries q [Tq,Hq,d] with its lse [Hq,Tq]: the softmax
+    weight that every key got from them, summed over the queries and the query heads that
+    read it, added to mass [B,Hkv,slots] fp32 (into mass_out if given, else in place).  The
+    last new_tokens [B] keys of a sequence (None: as many as its queries) start here: their
+    slots of positions [B,Hkv,slots] int32 count up to last_positions [B] (None: to the last
+    slot's number) -> mass_out."""
+    torch = _torch()
+    index = q.get_device() if isinstance(q, torch.Tensor) else -1
+    _contiguous(q, "q", torch.bfloat16, index)
+    if q.dim() != 3:
+        raise ValueError("q must be [Tq, Hq, d]")
+    Tq, Hq, d = q.shape
+    _contiguous(lse, "lse", torch.float32, index)
+    if lse.shape != (Hq, Tq):
+        raise ValueError(f"lse must be [{Hq}, {Tq}]")
+    P, page, Hkv = _pool(q, k_pages, None, index)
+    B, W = _paged_rows(page_table, seqlens_k, index)
+    _int_vector(cu_seqlens_q, "cu_seqlens_q", B + 1, index)
+    out, slots = _mass_tensors(mass, mass_out, positions, last_positions, B, Hkv, index)
+    if new_tokens is not None:
+        _int_vector(new_tokens, "new_tokens", B, index)
+    if max_seqlen_q is None:
+        raise ValueError("max_seqlen_q is required")
+    if stream is not None or index != _current_device():
+        with _Call(index, stream):
+            return attn_mass_paged(q, lse, k_pages, page_table, cu_seqlens_q, seqlens_k, mass,
+                                   positions, last_positions, new_tokens,
+                                   max_seqlen_q=max_seqlen_q, causal=causal, window=window,
+                                   n_sink=n_sink, scale=scale, mass_out=mass_out,
+                                   workspace=workspace)
+    B, W, P, slots, Tq = map(_c_int, (B, W, P, slots, Tq))
+    ws = _bytes(attn_mass_workspace_size(B, Hkv, W), index, workspace)
+    rc = lib.attn_mass_paged(
+        q.data_ptr(), lse.data_ptr(), k_pages.data_ptr(), page_table.data_ptr(),
+        cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), mass.data_ptr(), out.data_ptr(),
+        _ptr(positions), _ptr(last_positions), _ptr(new_tokens), B, Hq, Hkv,
+        _c_int(int(max_seqlen_q)), Tq, d, page, W, P, slots,
+        d ** -0.5 if scale is None else float(scale), int(bool(causal)), _c_int(int(window)),
+        _c_int(int(n_sink)), ws.data_ptr(), ws.nbytes, _raw_stream(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_mass_paged")
+    return out
 
 
 @functools.lru_cache(maxsize=256)

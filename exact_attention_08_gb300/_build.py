@@ -19,7 +19,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libattn_gb300.so")
 SOURCES = ["attn_api.cu", "attn_fwd_sm103.cu", "attn_fwd256_sm103.cu", "attn_decode_sm103.cu",
            "attn_bwd_sm103.cu", "attn_bwd256_sm103.cu", "attn_cache_api.cu", "attn_rope_sm103.cu",
-           "attn_pages_sm103.cu", "attn_thin_api.cu", "attn_evict_sm103.cu"]
+           "attn_pages_sm103.cu", "attn_thin_api.cu", "attn_evict_sm103.cu", "attn_mass_sm103.cu"]
 HEADERS = ["sm103_ptx.cuh", "attn_internal.h", "attn_bwd_common.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",

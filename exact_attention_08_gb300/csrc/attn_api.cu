@@ -101,10 +101,11 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // 4-D bf16 tensor (d, n1, n2, n3), innermost first, contiguous; box
-// 64 x 1 x box2 x 1 with the 128-byte swizzle.
+// 64 x box1 x box2 x 1 with the 128-byte swizzle.
 // s1, s2, s3: strides of dimensions 1..3 in elements (0: contiguous).
 int make_map(CUtensorMap* m, const void* ptr, uint64_t d, uint64_t n1, uint64_t n2, uint64_t n3,
-             uint32_t box2, const char* what, uint64_t s1 = 0, uint64_t s2 = 0, uint64_t s3 = 0) {
+             uint32_t box2, const char* what, uint64_t s1 = 0, uint64_t s2 = 0, uint64_t s3 = 0,
+             uint32_t box1 = 1) {
   auto fn = encode_fn();
   if (!fn) return set_error(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   cuuint64_t dims[4] = {d, n1, n2, n3};
@@ -112,7 +113,7 @@ int make_map(CUtensorMap* m, const void* ptr, uint64_t d, uint64_t n1, uint64_t 
   if (s2 == 0) s2 = n1 * d;
   if (s3 == 0) s3 = n2 * n1 * d;
   cuuint64_t strides[3] = {s1 * 2, s2 * 2, s3 * 2};
-  cuuint32_t box[4] = {64, 1, box2, 1};
+  cuuint32_t box[4] = {64, box1, box2, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides,
                   box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -130,6 +131,11 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 int page_pool_map(CUtensorMap* m, const void* pool, int d, int Hkv, int num_pages,
                   const char* what) {
   return make_map(m, pool, d, Hkv, 16, num_pages, 16, what);
+}
+
+int packed_rows_map(CUtensorMap* m, const void* x, int d, int H, int rows, int box_heads,
+                    int box_rows, const char* what) {
+  return make_map(m, x, d, H, rows, 1, box_rows, what, 0, 0, 0, box_heads);
 }
 
 int device_info(int* num_sms, int** status) {

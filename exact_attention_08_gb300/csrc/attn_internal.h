@@ -147,6 +147,32 @@ struct PagesArgs {
 
 size_t pages_workspace_bytes(int rows, int num_pages);
 
+// The attention weight that keys get from a block of queries.
+struct MassArgs {
+  CUtensorMap tmK, tmQ;  // page pool; q, boxes of TQ tokens x GP heads x 64 columns
+  const float* lse;      // [Hq, total_q]
+  const int* page_table;
+  const int* cu_q;
+  const int* seqlens_k;
+  const float* mass;  // [B, Hkv, slots]
+  float* mass_out;
+  int* positions;             // [B, Hkv, slots], may be null
+  const int* last_positions;  // [B], may be null
+  const int* new_tokens;      // [B], may be null
+  int B, Hq, Hkv, G, d;
+  int GP, TQ, HC;  // heads and tokens of a query tile; tiles that the group's heads take
+  int max_Sq, total_q, max_pages, num_pages, slots, max_kt;
+  float scale2;  // scale log2 e
+  int causal, window, n_sink;
+  long long* ws_plan;  // [B, max_kt + 1] units before a key tile; [B + 1] before a sequence
+  float* ws_part;      // partial sums [B * Hkv * max_kt + CTAs, key tile]
+  int* status;
+};
+
+// Columns of a query tile and keys of a key tile of launch_attn_mass.
+int mass_query_tile(int d);
+int mass_key_tile();
+
 constexpr int kEvictMaxUnits = 1 << 24;  // layers x rows x key heads of one call
 
 // Rows cut to their budget by accumulated attention weight.
@@ -200,6 +226,9 @@ bool aligned16(const void* p);
 // columns.
 int page_pool_map(CUtensorMap* m, const void* pool, int d, int Hkv, int num_pages,
                   const char* what);
+// Tensor map of packed rows [rows, H, d], boxes of box_rows x box_heads x 64 columns.
+int packed_rows_map(CUtensorMap* m, const void* x, int d, int H, int rows, int box_heads,
+                    int box_rows, const char* what);
 
 // Bytes of workspace the backward needs (two fp32 row vectors per query row,
 // padded to whole 128-row tiles).
@@ -221,6 +250,7 @@ cudaError_t launch_attn_append(const RopeArgs& p, const AppendArgs& ap, int num_
 cudaError_t launch_pages_resize(const PagesArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_fork(const PagesArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_compact(const PagesArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_mass(const MassArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_attn_evict(EvictArgs a, int num_sms, cudaStream_t stream);
 cudaError_t launch_wait_timeout_check(int* status, uint64_t limit_ns, cudaStream_t stream);
 

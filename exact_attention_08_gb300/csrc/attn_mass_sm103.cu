@@ -1,0 +1,667 @@
+// The attention weight that the keys of a paged cache get from a block of
+// queries: mass(b, h, t) += sum over the query heads g of key head h and over
+// the block's queries i that see key t of exp(scale q_ig . k_t - LSE_ig), the
+// log-sum-exps being those of the block's attention.
+//
+// Product.  Keys are the rows: S^T = K Q^T, M = 128 keys, N = kQN queries, so a
+// thread owns a key and its sum never leaves a register.  A query tile holds
+// whole tokens with all their heads of the group (column = token * GP + head),
+// loaded as one box of the q tensor.  With the LSE known there is no running
+// maximum and no second product: one product and one exponential for each
+// (query, key), and the tensor cores' 512 cycles for 128 x 128 x 128 against 512
+// of the exponential units.
+//
+// Tile.  256 keys (two row tiles) against each query tile: one row tile alone
+// would read 64 bytes of Q a cycle and SM from L2, more than it delivers.  Four
+// warps for each row tile; two S buffers each, so that the product of the next
+// query tile runs under the exponentials of this one.
+//
+//   tensor memory  S[row tile][2], kQN columns each
+//   shared memory  K ring (256 keys a slot), Q ring, LSEs, barriers
+//   warps          0-3 row tile 0, 4-7 row tile 1, 8 TMA producer, 9 MMA issuer,
+//                  10 LSEs of the query tiles (two tiles ahead, in column order)
+//
+// Split.  The work is cut into units, a query tile against a key tile, in the order
+// (sequence, key head, key tile, query tile), and each of the persistent CTAs (one an
+// SM) takes an equal run of units: causal triangles, windows and ragged lengths
+// balance by themselves, and few keys with many queries still fill the GPU.  A plan
+// kernel counts the units of every key tile.  A key tile that several CTAs share has
+// one partial sum from each; partial sums go to workspace slot (key tile + CTA), both
+// of which only grow along the order, and the last kernel adds them in CTA order
+// and updates the mass: the same bits on every call.
+//
+// A query tile that stays the same from one key tile to the next (few queries that
+// judge a long cache) is not loaded again: then the K stream alone is the traffic.
+#include "attn_internal.h"
+#include "sm103_ptx.cuh"
+
+#include <algorithm>
+#include <cmath>
+
+namespace attn {
+namespace {
+
+using namespace ptx;
+
+constexpr int kPage = 16;
+constexpr int kRows = 128;            // keys of a row tile
+constexpr int kKeys = 2 * kRows;      // keys of a key tile
+constexpr int kPagesPerTile = kKeys / kPage;
+constexpr int kThr = 352;
+constexpr int kWarpProducer = 8;
+constexpr int kWarpIssuer = 9;
+constexpr int kWarpLse = 10;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kAtoms = D / 64;
+  static constexpr int kQN = D == 256 ? 64 : 128;  // queries (token, head) of a query tile
+  static constexpr int kKSlots = D == 256 ? 1 : 2;
+  static constexpr int kQSlots = D == 64 ? 4 : 3;
+  static constexpr int kKAtom = kRows * 128;       // one row tile x 64 columns
+  static constexpr int kKRow = kAtoms * kKAtom;    // one row tile
+  static constexpr int kKBytes = 2 * kKRow;        // a K slot
+  static constexpr int kQAtom = kQN * 128;
+  static constexpr int kQBytes = kAtoms * kQAtom;  // a Q slot
+  static constexpr int kOffQ = kKSlots * kKBytes;
+  static constexpr int kOffLse = kOffQ + kQSlots * kQBytes;
+  static constexpr int kOffBar = kOffLse + 2 * kQN * 4;
+  static constexpr int kNumBars = 2 * kKSlots + 2 * kQSlots + 4 + 4 + 2 + 2 + 1;
+  static constexpr int kSmem = kOffBar + (kNumBars + 1) * 8 + 1024;
+  static_assert(kSmem <= 227 * 1024 - 512, "shared memory (512 bytes of it static)");
+};
+
+// One sequence: its queries and keys.
+struct Seq {
+  int Lq, L, off, q_base;
+};
+
+__device__ __forceinline__ bool load_seq(const MassArgs& a, int b, Seq& s) {
+  const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], L = a.seqlens_k[b];
+  s.q_base = q0;
+  s.Lq = q1 - q0;
+  s.L = L;
+  s.off = s.L - s.Lq;
+  return q0 >= 0 && q1 >= q0 && q1 <= a.total_q && q1 - q0 <= a.max_Sq && L >= 0 &&
+         L <= min(a.max_pages * kPage, a.slots);
+}
+
+__device__ __forceinline__ int key_tiles(const Seq& s) { return (s.L + kKeys - 1) / kKeys; }
+
+// Query tiles (of TQ tokens) with a query that sees a key of key tile kt: the first, and how
+// many.
+__device__ __forceinline__ int query_tiles(const MassArgs& a, const Seq& s, int kt, int* first) {
+  const int ka = kt * kKeys, kb = min(ka + kKeys, s.L) - 1;
+  int lo = 0, hi = s.Lq - 1;
+  if (a.causal) lo = max(lo, ka - s.off);
+  if (a.window > 0 && ka >= a.n_sink)
+    hi = static_cast<int>(min(static_cast<long long>(hi),
+                              static_cast<long long>(kb) + a.window - 1 - s.off));
+  *first = lo / a.TQ;
+  return hi < lo ? 0 : hi / a.TQ - lo / a.TQ + 1;
+}
+
+__device__ __forceinline__ long long* ws_cum(const MassArgs& a, int b) {
+  return a.ws_plan + static_cast<size_t>(b) * (a.max_kt + 1);
+}
+__device__ __forceinline__ long long* ws_base(const MassArgs& a) {  // [B + 1]
+  return a.ws_plan + static_cast<size_t>(a.B) * (a.max_kt + 1);
+}
+
+// ---------------------------------------------------------------- plan
+// cum[b][kt]: units of sequence b's key tiles before kt, one key head; cum[b][max_kt]: all.
+constexpr int kPlanThreads = 256;
+__global__ void __launch_bounds__(kPlanThreads) attn_mass_plan_kernel(const MassArgs a) {
+  __shared__ long long s_part[kPlanThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Seq s;
+  const bool ok = load_seq(a, b, s);
+  if (!ok && tid == 0) atomicOr(a.status, kStatusBadInput);
+  const int n = ok ? key_tiles(s) : 0;
+  long long* cum = ws_cum(a, b);
+  long long base = 0;
+  for (int k0 = 0; k0 < n; k0 += kPlanThreads) {
+    const int kt = k0 + tid;
+    int first;
+    const long long v =
+        kt < n ? static_cast<long long>(query_tiles(a, s, kt, &first)) * a.HC : 0;
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_part[warp] = x;
+    __syncthreads();
+    long long before = base, all = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < warp) before += s_part[w];
+      all += s_part[w];
+    }
+    if (kt < n) cum[kt] = before + x - v;
+    base += all;
+  }
+  if (tid == 0) cum[a.max_kt] = base;
+}
+
+// ---------------------------------------------------------------- the walk
+// A CTA's run of units: the key tiles in order, each with its query tiles.
+struct Walk {
+  int b, h, kt, first, n, u;  // key tile; its first query tile, units, and the next unit
+  long long left;             // units left in the run
+  int tiles;                  // key tiles of the sequence
+  Seq s;
+};
+
+__device__ __forceinline__ bool walk_item(const MassArgs& a, Walk& w) {
+  if (w.left <= 0) return false;
+  w.n = query_tiles(a, w.s, w.kt, &w.first) * a.HC;
+  return true;
+}
+
+// The next key tile with units.
+__device__ __forceinline__ bool walk_next(const MassArgs& a, Walk& w) {
+  w.u = 0;
+  while (w.left > 0) {
+    if (++w.kt >= w.tiles) {
+      w.kt = 0;
+      if (++w.h >= a.Hkv) {
+        w.h = 0;
+        do {
+          if (++w.b >= a.B) return false;
+          w.tiles = load_seq(a, w.b, w.s) ? key_tiles(w.s) : 0;
+        } while (w.tiles == 0);
+      }
+    }
+    if (walk_item(a, w) && w.n > 0) return true;
+  }
+  return false;
+}
+
+// Units of the current key tile that belong to this run.
+__device__ __forceinline__ int walk_units(const Walk& w) {
+  return static_cast<int>(min(static_cast<long long>(w.n - w.u), w.left));
+}
+
+// Sums of a thread's weights over 32 columns.  kMasked: only columns [lo, hi) count.
+template <bool kMasked>
+__device__ __forceinline__ void add_columns(const uint32_t* r, const float* nl, int c0,
+                                            float scale2, int lo, int hi, float* acc) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(nl + c0 + j);
+    const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float p = ex2_approx(fmaf(__uint_as_float(r[j + e]), scale2, lv[e]));
+      if (kMasked) p = (c0 + j + e >= lo && c0 + j + e < hi) ? p : 0.f;
+      acc[e] += p;
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThr, 1)
+    attn_mass_kernel(const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmQ, const MassArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ long long s_part[kThr / 32];
+  __shared__ long long s_run[2];
+  __shared__ int s_start[3];
+  __shared__ int abort_s;
+  uint8_t* smem = smem_align1024(smem_raw);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* k_empty = k_full + C::kKSlots;
+  uint64_t* q_full = k_empty + C::kKSlots;
+  uint64_t* q_empty = q_full + C::kQSlots;
+  uint64_t* s_full = q_empty + C::kQSlots;  // [row tile][buffer]
+  uint64_t* s_empty = s_full + 4;
+  uint64_t* l_full = s_empty + 4;
+  uint64_t* l_empty = l_full + 2;
+  uint64_t* drain = l_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = &abort_s;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+
+  // The mass update starts while this kernel drains; the plan comes first.
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (tid == 0) {
+    for (int i = 0; i < C::kKSlots; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < C::kQSlots; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&l_full[i], 1);
+      mbar_init(&l_empty[i], 8);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    abort_s = 0;
+    s_start[0] = -1;
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  // Rows of a Q slot that no box fills (a group that does not divide the tile) stay zero.
+  if (a.GP * a.TQ < C::kQN) {
+    for (int i = tid; i < C::kQSlots * C::kQBytes / 16; i += kThr)
+      reinterpret_cast<uint4*>(smem + C::kOffQ)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---- this CTA's run: units [u0, u1) of the T in all
+  {
+    const int per = (a.B + kThr - 1) / kThr;
+    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) sum += ws_cum(a, b)[a.max_kt] * a.Hkv;
+    long long x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_part[warp] = x;
+    __syncthreads();
+    long long before = x - sum, T = 0;
+    for (int w = 0; w < kThr / 32; ++w) {
+      if (w < warp) before += s_part[w];
+      T += s_part[w];
+    }
+    // with fewer units than CTAs the last CTAs have none, the others one each
+    const long long n = min(T, static_cast<long long>(gridDim.x)), c = blockIdx.x;
+    const long long u0 = c < n ? T * c / n : 0, u1 = c < n ? T * (c + 1) / n : 0;
+    for (int b = b0; b < b1; ++b) {
+      const long long per_head = ws_cum(a, b)[a.max_kt], here = per_head * a.Hkv;
+      if (blockIdx.x == 0) ws_base(a)[b] = before;
+      if (u0 < u1 && u0 >= before && u0 < before + here) {
+        const long long in = u0 - before;
+        const long long v = in % per_head;  // unit within the head
+        const long long* cum = ws_cum(a, b);
+        Seq s;
+        load_seq(a, b, s);
+        int lo = 0, hi = key_tiles(s) - 1;  // the last key tile with cum <= v
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) / 2;
+          if (cum[mid] <= v)
+            lo = mid;
+          else
+            hi = mid - 1;
+        }
+        s_start[0] = b;
+        s_start[1] = static_cast<int>(in / per_head);
+        s_start[2] = lo;
+        s_run[0] = v - cum[lo];
+      }
+      before += here;
+    }
+    if (tid == 0) {
+      s_run[1] = u1 - u0;
+      if (blockIdx.x == 0) ws_base(a)[a.B] = T;
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  if (s_start[0] >= 0) {
+    Walk w;
+    w.b = s_start[0];
+    w.h = s_start[1];
+    w.kt = s_start[2];
+    w.left = s_run[1];
+    load_seq(a, w.b, w.s);
+    w.tiles = key_tiles(w.s);
+    walk_item(a, w);
+    w.u = static_cast<int>(s_run[0]);
+
+    if (warp == kWarpProducer) {
+      // ============================================================ TMA producer
+      int kn = 0, qn = 0;  // K and Q slots filled
+      int pb = -1, ph = -1, pu = -1;
+      bool ok = true;
+      do {
+        const int ka = w.kt * kKeys;
+        const int two = w.s.L - ka > kRows ? 2 : 1;
+        const int np = (w.s.L + kPage - 1) / kPage;
+        int page = 0;
+        if (lane < kPagesPerTile) {
+          page = a.page_table[static_cast<size_t>(w.b) * a.max_pages +
+                              min(w.kt * kPagesPerTile + lane, np - 1)];
+          if (page < 0 || page >= a.num_pages) {
+            atomicOr(a.status, kStatusBadInput);
+            page = 0;
+          }
+        }
+        __syncwarp();
+        const int ks = kn % C::kKSlots;
+        if (kn >= C::kKSlots &&
+            !mbar_wait_warp(&k_empty[ks], (kn / C::kKSlots - 1) & 1, abort_flag, kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx_w(&k_full[ks], two * C::kKRow);
+        if (lane < two * (kRows / kPage)) {
+#pragma unroll
+          for (int at = 0; at < C::kAtoms; ++at)
+            tma_load_4d(smem + ks * C::kKBytes + (lane / 8) * C::kKRow + at * C::kKAtom +
+                            (lane % 8) * kPage * 128,
+                        &tmK, &k_full[ks], at * 64, w.h, 0, page);
+        }
+        __syncwarp();
+        ++kn;
+        const int units = walk_units(w);
+        for (int i = 0; ok && i < units; ++i) {
+          const int u = w.first * a.HC + w.u + i;  // the tile's number in the sequence
+          if (w.b == pb && w.h == ph && u == pu) continue;
+          pb = w.b, ph = w.h, pu = u;
+          const int qs = qn % C::kQSlots;
+          if (qn >= C::kQSlots &&
+              !mbar_wait_warp(&q_empty[qs], (qn / C::kQSlots - 1) & 1, abort_flag,
+                              kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx_w(&q_full[qs], C::kAtoms * a.GP * a.TQ * 128);
+#pragma unroll
+          for (int at = 0; at < C::kAtoms; ++at)
+            tma_load_4d_w(smem + C::kOffQ + qs * C::kQBytes + at * C::kQAtom, &tmQ, &q_full[qs],
+                          at * 64, w.h * a.G + (u % a.HC) * a.GP,
+                          w.s.q_base + (u / a.HC) * a.TQ, 0);
+          ++qn;
+        }
+        w.left -= units;
+      } while (ok && walk_next(a, w));
+      if (!ok && lane == 0) {
+        atomicOr(a.status, kStatusTimeout);
+        *abort_flag = 1;
+      }
+      // every copy issued lands before the CTA leaves
+      for (int i = 0; i < C::kKSlots; ++i) {
+        const int n = kn > i ? (kn - 1 - i) / C::kKSlots : -1;  // last use of the slot
+        if (n >= 0) mbar_wait(&k_full[i], n & 1, nullptr, kWaitLimitNs);
+      }
+      for (int i = 0; i < C::kQSlots; ++i) {
+        const int n = qn > i ? (qn - 1 - i) / C::kQSlots : -1;
+        if (n >= 0) mbar_wait(&q_full[i], n & 1, nullptr, kWaitLimitNs);
+      }
+    } else if (warp == kWarpIssuer) {
+      // ============================================================ MMA issuer
+      constexpr uint32_t idesc = idesc_bf16_f32(kRows, C::kQN, false);
+      int kn = 0, qn = 0;
+      int cnt[2] = {0, 0};  // products of each row tile
+      int pb = -1, ph = -1, pu = -1;
+      bool ok = true;
+      do {
+        const int ks = kn % C::kKSlots;
+        if (!mbar_wait_warp(&k_full[ks], (kn / C::kKSlots) & 1, abort_flag, kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        const int units = walk_units(w);
+        for (int i = 0; ok && i < units; ++i) {
+          const int u = w.first * a.HC + w.u + i;
+          if (!(w.b == pb && w.h == ph && u == pu)) {
+            // the tile before this one is done with once its products are
+            if (pu >= 0) mma_commit_w(&q_empty[(qn - 1) % C::kQSlots]);
+            pb = w.b, ph = w.h, pu = u;
+            if (!mbar_wait_warp(&q_full[qn % C::kQSlots], (qn / C::kQSlots) & 1, abort_flag,
+                                kWaitLimitNs)) {
+              ok = false;
+              break;
+            }
+            ++qn;
+          }
+          tc_fence_after_sync();
+          const int qs = (qn - 1) % C::kQSlots;
+          const uint64_t dq = sdesc_sw128(smem_addr(smem + C::kOffQ + qs * C::kQBytes), 16, 1024);
+          // Keys past the last one: whatever the slot holds, in rows that nothing reads.
+          for (int t = 0; t < 2; ++t) {
+            const int buf = cnt[t] & 1;
+            if (cnt[t] >= 2 &&
+                !mbar_wait_warp(&s_empty[t * 2 + buf], (cnt[t] / 2 - 1) & 1, abort_flag,
+                                kWaitLimitNs)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            const uint64_t dk = sdesc_sw128(
+                smem_addr(smem + ks * C::kKBytes + t * C::kKRow), 16, 1024);
+            const uint32_t tS = tmem + (t * 2 + buf) * C::kQN;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t ko = static_cast<uint64_t>(((kk / 4) * C::kKAtom + (kk % 4) * 32) >> 4);
+              const uint64_t qo = static_cast<uint64_t>(((kk / 4) * C::kQAtom + (kk % 4) * 32) >> 4);
+              mma_bf16_ss_w(tS, dk + ko, dq + qo, idesc, kk > 0 ? 1u : 0u);
+            }
+            mma_commit_w(&s_full[t * 2 + buf]);
+            ++cnt[t];
+          }
+        }
+        mma_commit_w(&k_empty[ks]);
+        ++kn;
+        w.left -= units;
+      } while (ok && walk_next(a, w));
+      if (!ok && lane == 0) {
+        atomicOr(a.status, kStatusTimeout);
+        *abort_flag = 1;
+      }
+      // every product issued has completed before tensor memory is released
+      mma_commit_w(drain);
+      mbar_wait(drain, 0, nullptr, kWaitLimitNs);
+    } else if (warp == kWarpLse) {
+      // ============================================================ LSEs
+      // -LSE log2 e of every column of a query tile, -inf where there is no query.
+      constexpr int kPer = C::kQN / 32;
+      int n = 0;
+      bool ok = true;
+      do {
+        const int units = walk_units(w);
+        for (int i = 0; i < units; ++i, ++n) {
+          const int u = w.first * a.HC + w.u + i;
+          float v[kPer];
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            const int c = j * 32 + lane, tok = (u / a.HC) * a.TQ + c / a.GP;
+            v[j] = -INFINITY;
+            if (c < a.GP * a.TQ && tok < w.s.Lq)
+              v[j] = -kLog2e * a.lse[static_cast<size_t>(w.h * a.G + (u % a.HC) * a.GP + c % a.GP) *
+                                         a.total_q + w.s.q_base + tok];
+          }
+          if (n >= 2 && !mbar_wait_warp(&l_empty[n & 1], (n / 2 - 1) & 1, abort_flag, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          float* nl = reinterpret_cast<float*>(smem + C::kOffLse) + (n & 1) * C::kQN;
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) nl[j * 32 + lane] = v[j];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&l_full[n & 1]);
+        }
+        w.left -= units;
+      } while (ok && walk_next(a, w));
+      if (!ok && lane == 0) {
+        atomicOr(a.status, kStatusTimeout);
+        *abort_flag = 1;
+      }
+    } else {
+      // ============================================================ sums: warps 0-3, 4-7
+      const int t = warp / 4;
+      const int r = tid % kRows;  // the row of this thread
+      const uint32_t taddr = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
+      int cnt = 0;
+      bool ok = true;
+      do {
+        const int ka = w.kt * kKeys + t * kRows;
+        const int units = walk_units(w);
+        float sum = 0.f;
+        for (int i = 0; i < units; ++i) {
+          const int buf = cnt & 1;
+          const uint32_t parity = (cnt / 2) & 1;
+          if (!mbar_wait_warp(&l_full[buf], parity, abort_flag, kWaitLimitNs) ||
+              !mbar_wait_warp(&s_full[t * 2 + buf], parity, abort_flag, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const float* nl = reinterpret_cast<const float*>(smem + C::kOffLse) + buf * C::kQN;
+          const int i0 = ((w.first * a.HC + w.u + i) / a.HC) * a.TQ;  // the tile's first token
+          const uint32_t tS = taddr + (t * 2 + buf) * C::kQN;
+          // Does every row see every query of the tile?
+          const bool interior =
+              i0 + a.TQ <= w.s.Lq && (!a.causal || ka + kRows - 1 <= i0 + w.s.off) &&
+              (a.window <= 0 || ka + kRows <= a.n_sink ||
+               static_cast<long long>(ka) + a.window > i0 + a.TQ - 1 + w.s.off);
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          if (interior) {
+#pragma unroll
+            for (int c = 0; c < C::kQN; c += 32) {
+              uint32_t x[32];
+              tmem_ld_x32(tS + c, x);
+              tmem_ld_wait_x32(x);
+              add_columns<false>(x, nl, c, a.scale2, 0, 0, acc);
+            }
+          } else {
+            // columns [lo, hi): the tokens of the tile that see key ka + r
+            const int key = ka + r;
+            long long lo = 0, hi = min(a.TQ, w.s.Lq - i0);
+            if (a.causal) lo = max(0, key - w.s.off - i0);
+            if (a.window > 0 && key >= a.n_sink)
+              hi = min(hi, static_cast<long long>(key) + a.window - w.s.off - i0);
+            const int clo = static_cast<int>(min(lo, static_cast<long long>(a.TQ))) * a.GP;
+            const int chi = static_cast<int>(max(hi, 0LL)) * a.GP;
+#pragma unroll 1
+            for (int c = 0; c < C::kQN; c += 32) {
+              uint32_t x[32];
+              tmem_ld_x32(tS + c, x);
+              tmem_ld_wait_x32(x);
+              add_columns<true>(x, nl, c, a.scale2, clo, chi, acc);
+            }
+          }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&s_empty[t * 2 + buf]);
+            mbar_arrive(&l_empty[buf]);
+          }
+          ++cnt;
+          sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        }
+        if (!ok) break;
+        const size_t slot =
+            (static_cast<size_t>(w.b) * a.Hkv + w.h) * a.max_kt + w.kt + blockIdx.x;
+        a.ws_part[slot * kKeys + t * kRows + r] = sum;
+        w.left -= units;
+      } while (walk_next(a, w));
+      if (!ok && lane == 0) {
+        atomicOr(a.status, kStatusTimeout);
+        *abort_flag = 1;
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- the mass
+constexpr int kAddThreads = 256;
+constexpr int kAddTokens = 4 * kAddThreads;
+__global__ void __launch_bounds__(kAddThreads) attn_mass_add_kernel(const MassArgs a, int ctas) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int h = blockIdx.y, b = blockIdx.z;
+  Seq s;
+  if (!load_seq(a, b, s)) return;
+  const int t0 = blockIdx.x * kAddTokens;
+  if (t0 >= s.L) return;
+  const long long* cum = ws_cum(a, b);
+  const long long per_head = cum[a.max_kt], T = ws_base(a)[a.B];
+  const long long head0 = ws_base(a)[b] + per_head * h;
+  int fresh = a.new_tokens ? a.new_tokens[b] : s.Lq;
+  fresh = max(0, min(fresh, s.L));
+  const int last = a.last_positions ? a.last_positions[b] : s.L - 1;
+  const size_t row = (static_cast<size_t>(b) * a.Hkv + h) * a.slots;
+#pragma unroll
+  for (int j = 0; j < kAddTokens / kAddThreads; ++j) {
+    const int t = t0 + j * kAddThreads + threadIdx.x;
+    if (t >= s.L) break;
+    const int kt = t / kKeys;
+    const long long n = (kt + 1 < key_tiles(s) ? cum[kt + 1] : per_head) - cum[kt];
+    float w = 0.f;
+    if (n > 0) {
+      // of C CTAs with units, unit u belongs to CTA ((u + 1) C - 1) / T
+      const long long u = head0 + cum[kt], C = min(T, static_cast<long long>(ctas));
+      const int c0 = static_cast<int>(((u + 1) * C - 1) / T);
+      const int c1 = static_cast<int>(((u + n) * C - 1) / T);
+      const size_t slot = (static_cast<size_t>(b) * a.Hkv + h) * a.max_kt + kt;
+      for (int c = c0; c <= c1; ++c) w += a.ws_part[(slot + c) * kKeys + t % kKeys];
+    }
+    const bool is_new = t >= s.L - fresh;
+    a.mass_out[row + t] = is_new ? w : a.mass[row + t] + w;
+    if (is_new && a.positions != nullptr) a.positions[row + t] = last - (s.L - 1 - t);
+  }
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_mass(const MassArgs& a, int num_sms, cudaStream_t stream) {
+  static SharedMemoryLimit limit;
+  cudaError_t e = limit.raise(attn_mass_kernel<D>, Cfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  attn_mass_plan_kernel<<<a.B, kPlanThreads, 0, stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_dependent(attn_mass_kernel<D>, dim3(num_sms), kThr, Cfg<D>::kSmem, stream, a.tmK,
+                       a.tmQ, a);
+  if (e != cudaSuccess) return e;
+  const long long reach = std::min<long long>(static_cast<long long>(a.max_pages) * kPage, a.slots);
+  const dim3 grid(static_cast<unsigned>((reach + kAddTokens - 1) / kAddTokens), a.Hkv, a.B);
+  return launch_dependent(attn_mass_add_kernel, grid, kAddThreads, 0, stream, a, num_sms);
+}
+
+}  // namespace
+
+int mass_query_tile(int d) { return d == 256 ? Cfg<256>::kQN : Cfg<128>::kQN; }
+int mass_key_tile() { return kKeys; }
+
+cudaError_t launch_attn_mass(const MassArgs& a, int num_sms, cudaStream_t stream) {
+  if (a.d == 64) return launch_mass<64>(a, num_sms, stream);
+  if (a.d == 128) return launch_mass<128>(a, num_sms, stream);
+  if (a.d == 256) return launch_mass<256>(a, num_sms, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace attn

@@ -89,6 +89,13 @@ int decode_maps(DecodeLaunch* a, const void* k_pages, const void* v_pages, int* 
   return page_pool_map(&a->tmV, v_pages, a->d, a->Hkv, a->num_pages, "v_pages");
 }
 
+constexpr int kMaxSms = 256;  // SMs that workspaces provide for
+
+// Key tiles of a row's page table.
+size_t mass_tiles(int max_pages) {
+  return (static_cast<size_t>(max_pages) * 16 + mass_key_tile() - 1) / mass_key_tile();
+}
+
 size_t pad16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
 }  // namespace
@@ -139,6 +146,96 @@ ATTN_API int attn_decode_paged_mass(const void* q, const void* k_pages, const vo
   if ((rc = decode_maps(&a, k_pages, v_pages, &num_sms)) != ATTN_OK) return rc;
   const cudaError_t e = launch_attn_decode(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : cuda_error(e, "attn_decode_paged_mass launch");
+}
+
+ATTN_API size_t attn_mass_workspace_size(int B, int Hkv, int max_pages_per_seq) {
+  if (B < 0 || Hkv <= 0 || max_pages_per_seq <= 0) return 0;
+  const size_t kt = mass_tiles(max_pages_per_seq);
+  return pad16((static_cast<size_t>(B) * (kt + 2) + 1) * sizeof(long long)) +
+         (static_cast<size_t>(B) * Hkv * kt + kMaxSms) * mass_key_tile() * sizeof(float);
+}
+
+ATTN_API int attn_mass_paged(const void* q, const float* lse, const void* k_pages,
+                             const int* page_table, const int* cu_seqlens_q, const int* seqlens_k,
+                             const float* mass, float* mass_out, int* positions,
+                             const int* last_positions, const int* new_tokens, int B, int Hq,
+                             int Hkv, int max_Sq, int total_q, int d, int page_size,
+                             int max_pages_per_seq, int num_pages_total, int mass_slots,
+                             float scale, int causal, int window, int n_sink, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  clear_error();
+  int rc = check_heads(B, Hq, Hkv, d, page_size, max_pages_per_seq, num_pages_total);
+  if (rc != ATTN_OK) return rc;
+  if (mass_slots <= 0 || max_Sq < 0 || total_q < 0 || max_Sq > (1 << 30) || total_q > (1 << 30))
+    return set_error(ATTN_ERR_INVALID_ARG, "bad sizes (mass_slots=%d max_Sq=%d total_q=%d)",
+                     mass_slots, max_Sq, total_q);
+  if (causal != 0 && causal != 1) return set_error(ATTN_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (window > 0 && !causal)
+    return set_error(ATTN_ERR_INVALID_ARG, "a sliding window requires causal");
+  if (n_sink < 0 || (n_sink > 0 && window <= 0))
+    return set_error(ATTN_ERR_INVALID_ARG, "n_sink=%d needs a window", n_sink);
+  if ((rc = check_scale(scale)) != ATTN_OK) return rc;
+  if (B == 0) return ATTN_OK;
+  if ((total_q > 0 && (!q || !lse)) || !k_pages || !page_table || !cu_seqlens_q || !seqlens_k ||
+      !mass || !mass_out)
+    return set_error(ATTN_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned4(lse) || !aligned4(page_table) ||
+      !aligned4(cu_seqlens_q) || !aligned4(seqlens_k) || !aligned4(mass) || !aligned4(mass_out) ||
+      !aligned4(positions) || !aligned4(last_positions) || !aligned4(new_tokens))
+    return set_error(ATTN_ERR_INVALID_ARG, "misaligned pointer");
+  const size_t need = attn_mass_workspace_size(B, Hkv, max_pages_per_seq);
+  if ((rc = check_workspace(workspace, workspace_bytes, need)) != ATTN_OK) return rc;
+  MassArgs a;
+  std::memset(&a, 0, sizeof(a));
+  int num_sms = 0;
+  if ((rc = device_info(&num_sms, &a.status)) != ATTN_OK) return rc;
+  if (num_sms > kMaxSms) return set_error(ATTN_ERR_UNSUPPORTED, "%d SMs", num_sms);
+  a.G = Hq / Hkv;
+  // The heads of a query tile: the group, or its largest part that fits.
+  const int tile = mass_query_tile(d);
+  a.GP = a.G;
+  if (a.G > tile) {
+    a.GP = tile;
+    while (a.G % a.GP != 0) --a.GP;
+  }
+  a.TQ = tile / a.GP;
+  a.HC = a.G / a.GP;
+  if ((rc = page_pool_map(&a.tmK, k_pages, d, Hkv, num_pages_total, "k_pages")) != ATTN_OK)
+    return rc;
+  // with no query at all the map is of nothing that is read
+  if ((rc = packed_rows_map(&a.tmQ, total_q > 0 ? q : k_pages, d, total_q > 0 ? Hq : Hkv,
+                            total_q > 0 ? total_q : 16, total_q > 0 ? a.GP : 1, a.TQ, "q")) !=
+      ATTN_OK)
+    return rc;
+  a.lse = lse;
+  a.page_table = page_table;
+  a.cu_q = cu_seqlens_q;
+  a.seqlens_k = seqlens_k;
+  a.mass = mass;
+  a.mass_out = mass_out;
+  a.positions = positions;
+  a.last_positions = last_positions;
+  a.new_tokens = new_tokens;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.max_Sq = max_Sq;
+  a.total_q = total_q;
+  a.max_pages = max_pages_per_seq;
+  a.num_pages = num_pages_total;
+  a.slots = mass_slots;
+  a.max_kt = static_cast<int>(mass_tiles(max_pages_per_seq));
+  a.scale2 = scale * 1.4426950408889634f;
+  a.causal = causal;
+  a.window = window > 0 ? window : 0;
+  a.n_sink = n_sink;
+  a.ws_plan = static_cast<long long*>(workspace);
+  a.ws_part = reinterpret_cast<float*>(
+      static_cast<char*>(workspace) +
+      pad16((static_cast<size_t>(B) * (a.max_kt + 2) + 1) * sizeof(long long)));
+  const cudaError_t e = launch_attn_mass(a, num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_error(e, "attn_mass_paged launch");
 }
 
 ATTN_API size_t attn_evict_workspace_size(int layers, int B, int Hkv, int slots,

@@ -591,6 +591,39 @@ ATTN_API int attn_decode_paged_mass(const void* q, const void* k_pages, const vo
                                     size_t workspace_bytes, void* stream);
 
 /*
+ * The same sums for a block of queries against a paged cache, after their
+ * attention (attn_fwd_paged):
+ *   w(b, h, t) = sum over the heads g of the group and the queries i of
+ *                sequence b that see key t of exp(scale q_ig . k_t - LSE_ig)
+ *   mass_out(b, h, t) = mass(b, h, t) + w, for the sequence's new tokens w.
+ * q [total_q, Hq, d] bf16, lse [Hq, total_q] fp32 (attn_fwd_paged's, a logit
+ * sink included if there was one), page_table, cu_seqlens_q, seqlens_k, max_Sq,
+ * causal, window and n_sink as attn_fwd_paged's.  The block may be the last
+ * queries of a prompt only: they are aligned to the end of the keys.
+ *   new_tokens: DEVICE int32 [B], how many of the sequence's last keys are new
+ *     (their old mass is not read); NULL: as many as it has queries.  Taken
+ *     into [0, seqlens_k[b]].
+ *   positions (may be NULL): a new token t gets last_positions[b] -
+ *     (seqlens_k[b] - 1 - t) (last_positions NULL: t).
+ *   mass_out may be mass.  A sequence with offsets or a length out of range, or
+ *   longer than mass_slots, has its mass left as it was (ATTN_ERR_BAD_INPUT).
+ *   Page indices out of range read page 0 (ATTN_ERR_BAD_INPUT).
+ *   Each partial sum is formed by one CTA and they are added in a fixed order:
+ *   repeated calls give identical bits.
+ *   workspace: attn_mass_workspace_size(...) bytes, 16-byte aligned.  B and Hq
+ *   at most 65,535, max_Sq and total_q at most 2^30.
+ */
+ATTN_API size_t attn_mass_workspace_size(int B, int Hkv, int max_pages_per_seq);
+ATTN_API int attn_mass_paged(const void* q, const float* lse, const void* k_pages,
+                             const int* page_table, const int* cu_seqlens_q, const int* seqlens_k,
+                             const float* mass, float* mass_out, int* positions,
+                             const int* last_positions, const int* new_tokens, int B, int Hq,
+                             int Hkv, int max_Sq, int total_q, int d, int page_size,
+                             int max_pages_per_seq, int num_pages_total, int mass_slots,
+                             float scale, int causal, int window, int n_sink, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
  * Cuts rows to a budget: of each layer, row b and key head h the keep[b] tokens
  * that rank highest stay, in slots 0 .. keep[b] - 1.
  *   mass, positions [layers, B, Hkv, slots], k_pages, v_pages [layers,

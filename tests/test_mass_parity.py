@@ -163,3 +163,190 @@ def test_decode_captured_on_another_stream():
     torch.cuda.synchronize()
     assert torch.equal(mass, first)
     assert ea.attn_device_status() == ea.ATTN_OK
+
+
+# ------------------------------------------------------------------ blocks of queries
+
+def block_reference(r, q, cu, causal, window, n_sink, scale, sink=None):
+    """lse [Hq, T] and per row the weights [Hkv, n] in fp64."""
+    lse, w = np.full((r.Hq, q.shape[0]), -np.inf), []
+    G = r.Hq // r.Hkv
+    for b, n in enumerate(r.lens):
+        k, v = r.keys(b)
+        got = np.zeros((r.Hkv, len(k)))
+        for i in range(cu[b + 1] - cu[b]):
+            seen = ref.seen_keys(i, cu[b + 1] - cu[b], len(k), causal, window, n_sink)
+            _, z, p = ref.attend(np64(q[cu[b] + i]), k, v, scale, sink, seen)
+            lse[:, cu[b] + i] = z
+            got += p.reshape(r.Hkv, G, -1).sum(1)
+        w.append(got)
+    return lse, w
+
+
+def check_block(r, w, out, new, mass=None):
+    mass = r.mass if mass is None else mass
+    for b, n in enumerate(r.lens):
+        base = mass[b, :, :n].double().numpy().copy()
+        base[:, n - new[b]:] = 0
+        ref.check_mass(out[b, :, :n].double().cpu().numpy(), base, w[b], b)
+        assert torch.equal(out[b, :, n:].cpu(), mass[b, :, n:])
+
+
+MASKS = [(True, 0, 0), (False, 0, 0), (True, 7, 0), (True, 100, 5), (True, 1, 300)]
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(1, 1, 64), (8, 2, 128), (6, 2, 64), (4, 1, 256), (5, 1, 256),
+                                      (10, 2, 128)])
+@pytest.mark.parametrize("causal,window,n_sink", MASKS)
+def test_blocks(Hq, Hkv, d, causal, window, n_sink):
+    lens = [1, 16, 129, 300, 257, 40, 0, 530]
+    nq = [1, 16, 5, 130, 257, 0, 0, 33]
+    r = Rows(lens, Hq, Hkv, d, seed=Hq + d + window)
+    cu = np.concatenate([[0], np.cumsum(nq)]).tolist()
+    q = r.q(cu[-1] + 3)                       # rows behind the last sequence
+    q[cu[-1]:] = NAN
+    lse, w = block_reference(r, q[:cu[-1]], cu, causal, window, n_sink, d ** -0.5)
+    lse = np.concatenate([lse, np.full((Hq, 3), NAN)], 1)
+    mass, pos = r.mass.cuda(), r.pos.cuda()
+    mass_new = r.mass.clone()
+    for b, n in enumerate(lens):
+        mass_new[b, :, n - nq[b]:n] = NAN     # of new tokens: not read
+    mass = mass_new.cuda()
+    out = ea.attn_mass_paged(q.cuda(), torch.tensor(lse).float().cuda(), r.k.cuda(),
+                             i32(r.table), i32(cu), i32(lens), mass, pos, max_seqlen_q=257,
+                             causal=causal, window=window, n_sink=n_sink)
+    torch.cuda.synchronize()
+    assert ea.attn_device_status() == ea.ATTN_OK and out is mass
+    check_block(r, w, out, nq)
+    for b, n in enumerate(lens):
+        want = r.pos[b].clone()
+        want[:, n - nq[b]:n] = torch.arange(n - nq[b], n, dtype=torch.int32)
+        assert torch.equal(pos[b].cpu(), want)
+
+
+def test_lse_of_the_attention_and_more_queries_than_keys():
+    """The LSE as attn_fwd_paged returns it: within 1e-3 by its own tests, 1e-4 here, so the
+    weights of a query sum to one within that.  Some queries see no key."""
+    lens, nq, d = [100, 20, 3], [100, 50, 9], 128
+    r = Rows(lens, 4, 2, d, seed=21)
+    cu = np.concatenate([[0], np.cumsum(nq)]).tolist()
+    q = r.q(cu[-1]).cuda()
+    sink = torch.tensor([0.5, -float("inf"), 3.0, 1.0])
+    for s in (None, sink):
+        o, lse = ea.attn_fwd_paged(q, r.k.cuda(), r.v.cuda(), i32(r.table), i32(cu), i32(lens),
+                                   max_seqlen_q=100, sink_logit=None if s is None else s.cuda())
+        out = ea.attn_mass_paged(q, lse, r.k.cuda(), i32(r.table), i32(cu), i32(lens),
+                                 torch.zeros_like(r.mass).cuda(), max_seqlen_q=100)
+        torch.cuda.synchronize()
+        _, w = block_reference(r, q.cpu(), cu, True, 0, 0, d ** -0.5,
+                               None if s is None else s.double().numpy())
+        for b, n in enumerate(lens):
+            got = out[b, :, :n].double().cpu().numpy()
+            assert np.abs(got - w[b]).max() <= 1e-4 * w[b].max() + 1e-6
+            if s is None:
+                assert abs(got.sum() - 4 * min(nq[b], n)) <= 1e-4 * 4 * n
+    assert ea.attn_device_status() == ea.ATTN_OK
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(130, 1, 64), (134, 1, 64), (70, 1, 256), (67, 1, 256)])
+def test_groups_larger_than_a_query_tile(Hq, Hkv, d):
+    lens, nq = [33, 300], [3, 2]
+    r = Rows(lens, Hq, Hkv, d, seed=Hq)
+    cu = [0, 3, 5]
+    q = r.q(5)
+    lse, w = block_reference(r, q, cu, True, 0, 0, d ** -0.5)
+    out = ea.attn_mass_paged(q.cuda(), torch.tensor(lse).float().cuda(), r.k.cuda(),
+                             i32(r.table), i32(cu), i32(lens), r.mass.cuda(), max_seqlen_q=3)
+    torch.cuda.synchronize()
+    check_block(r, w, out, nq)
+    assert ea.attn_device_status() == ea.ATTN_OK
+
+
+@pytest.mark.parametrize("lens,nq,Hkv", [([9000], [32], 2), ([4000, 5, 2500], [2, 5, 600], 1),
+                                         ([300] * 40, [1] * 40, 3)])
+def test_many_key_tiles(lens, nq, Hkv):
+    """Key tiles shared by CTAs, query tiles kept from one key tile to the next; new tokens
+    and positions given."""
+    d = 64
+    r = Rows(lens, 2 * Hkv, Hkv, d, seed=len(lens))
+    cu = np.concatenate([[0], np.cumsum(nq)]).tolist()
+    q = r.q(cu[-1])
+    lse, w = block_reference(r, q, cu, True, 0, 0, d ** -0.5)
+    fresh = [min(n, 7 * b + 1) for b, n in enumerate(lens)]
+    fresh[0] = lens[0]
+    given = list(fresh)
+    given[0] = 10 ** 9                        # taken into the row's length
+    pos, last = r.pos.cuda(), [3 * n for n in lens]
+    args = (q.cuda(), torch.tensor(lse).float().cuda(), r.k.cuda(), i32(r.table), i32(cu),
+            i32(lens))
+    out = torch.empty_like(r.mass).cuda()
+    out.copy_(r.mass)
+    got = ea.attn_mass_paged(*args, r.mass.cuda(), pos, i32(last), i32(given),
+                             max_seqlen_q=max(nq), mass_out=out)
+    torch.cuda.synchronize()
+    assert got is out
+    check_block(r, w, out, fresh)
+    for b, n in enumerate(lens):
+        want = r.pos[b].clone()
+        want[:, n - fresh[b]:n] = last[b] - torch.arange(fresh[b] - 1, -1, -1, dtype=torch.int32)
+        assert torch.equal(pos[b].cpu(), want)
+    again = torch.empty_like(out)
+    ea.attn_mass_paged(*args, r.mass.cuda(), None, None, i32(given), max_seqlen_q=max(nq),
+                       mass_out=again)
+    torch.cuda.synchronize()
+    for b, n in enumerate(lens):
+        assert torch.equal(again[b, :, :n], out[b, :, :n])
+    assert ea.attn_device_status() == ea.ATTN_OK
+
+
+def test_block_inputs_out_of_range():
+    r = Rows([40, 40, 40], 2, 1, 64, slots=45, seed=9)
+    q, lse = r.q(12).cuda(), torch.zeros(2, 12).cuda()
+    for cu, lens in (([0, 4, 2, 12], [40, 40, 40]), ([-1, 4, 8, 12], [40, 40, 40]),
+                     ([0, 4, 8, 13], [40, 40, 40]), ([0, 4, 8, 12], [40, 46, 40]),
+                     ([0, 4, 8, 12], [40, -3, 40]), ([0, 2, 10, 12], [40, 40, 40])):
+        mass = r.mass.cuda()
+        ea.attn_mass_paged(q, lse, r.k.cuda(), i32([t[:3] + [0] for t in r.table]), i32(cu),
+                           i32(lens), mass, max_seqlen_q=7)
+        torch.cuda.synchronize()
+        assert ea.attn_device_status() == ea.ATTN_ERR_BAD_INPUT
+        left = [b for b in range(3) if torch.equal(mass[b].cpu(), r.mass[b])]
+        assert 0 < len(left) < 3, (cu, lens)
+    table = [list(t) for t in r.table]
+    table[1][1] = r.P
+    ea.attn_mass_paged(q, lse, r.k.cuda(), i32(table), i32([0, 4, 8, 12]), i32([40] * 3),
+                       r.mass.cuda(), max_seqlen_q=7)
+    assert ea.attn_device_status() == ea.ATTN_ERR_BAD_INPUT
+
+
+def test_block_captured_on_another_stream_and_empty():
+    lens, nq, d = [700, 100], [65, 3], 128
+    r = Rows(lens, 8, 2, d, seed=17)
+    cu = [0, 65, 68]
+    q = r.q(68)
+    lse, w = block_reference(r, q, cu, True, 0, 0, d ** -0.5)
+    args = (q.cuda(), torch.tensor(lse).float().cuda(), r.k.cuda(), i32(r.table), i32(cu),
+            i32(lens))
+    mass, out = r.mass.cuda(), r.mass.cuda()
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    ea.attn_mass_paged(*args, mass, max_seqlen_q=65, mass_out=out, stream=other)
+    other.synchronize()
+    check_block(r, w, out, nq)
+    first = out.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ea.attn_mass_paged(*args, mass, max_seqlen_q=65, mass_out=out)
+    out.copy_(r.mass.cuda())
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first)
+    # no queries at all: the mass is passed on
+    none = ea.attn_mass_paged(q[:0].cuda(), torch.zeros(8, 0).cuda(), r.k.cuda(), i32(r.table),
+                              i32([0, 0, 0]), i32(lens), mass, max_seqlen_q=0,
+                              mass_out=torch.zeros_like(mass))
+    torch.cuda.synchronize()
+    for b, n in enumerate(lens):
+        assert torch.equal(none[b, :, :n], mass[b, :, :n])
+    assert ea.attn_device_status() == ea.ATTN_OK

@@ -39,6 +39,7 @@ __all__ = [
     "attn_decode_workspace_size", "attn_decode_paged", "attn_decode_paged_sink", "attn_device_status", "attn_check_wait_timeout", "attn_status_string",
     "attn_rope_inv_freq", "attn_rope", "attn_rope_bwd", "attn_append_paged",
     "attn_pages_workspace_size", "attn_pages_resize", "attn_pages_fork", "attn_pages_compact",
+    "attn_decode_shared_workspace_size", "attn_decode_paged_shared",
     "attn_decode_mass_workspace_size", "attn_decode_paged_mass",
     "attn_mass_workspace_size", "attn_mass_paged", "attn_evict_workspace_size", "attn_evict_paged",
     "attn_last_error", "library_path", "lib",
@@ -98,6 +99,10 @@ def _load() -> ctypes.CDLL:
     L.attn_pages_resize.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp, sz, vp]
     L.attn_pages_fork.argtypes = [vp, vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, i, i, vp, sz, vp]
     L.attn_pages_compact.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp, sz, vp]
+    L.attn_decode_shared_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
+    L.attn_decode_shared_workspace_size.restype = sz
+    L.attn_decode_paged_shared.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i,
+                                           i, i, i, i, f, vp, vp, sz, vp]
     L.attn_decode_mass_workspace_size.argtypes = [i, i, i, i, i]
     L.attn_decode_mass_workspace_size.restype = sz
     L.attn_decode_paged_mass.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i,
@@ -121,7 +126,7 @@ def _load() -> ctypes.CDLL:
                "attn_decode_paged",
                "attn_decode_paged_sink", "attn_rope_inv_freq", "attn_rope", "attn_rope_bwd",
                "attn_append_paged", "attn_pages_resize", "attn_pages_fork", "attn_pages_compact",
-               "attn_decode_paged_mass", "attn_mass_paged", "attn_evict_paged",
+               "attn_decode_paged_shared", "attn_decode_paged_mass", "attn_mass_paged", "attn_evict_paged",
                "attn_device_status", "attn_check_wait_timeout"):
         getattr(L, fn).restype = ctypes.c_int
     return L
@@ -1034,6 +1039,67 @@ def _mass_tensors(mass, mass_out, positions, last_positions, B, Hkv, index):
     if last_positions is not None:
         _int_vector(last_positions, "last_positions", B, index)
     return mass_out, shape[2]
+
+
+@functools.lru_cache(maxsize=256)
+def attn_decode_shared_workspace_size(B: int, Hq: int, Hkv: int, d: int, n_groups: int,
+                                      n_rows: int, max_pages: int, num_splits: int) -> int:
+    return int(lib.attn_decode_shared_workspace_size(
+        *map(_c_int, (B, Hq, Hkv, d, n_groups, n_rows, max_pages, num_splits))))
+
+
+def attn_decode_paged_shared(q, k_pages, v_pages, page_table, seqlens, cu_groups, prefix_lens,
+                             group_rows=None, o=None, lse=None, *, sink_logit=None,
+                             num_splits=None, scale=None, workspace=None, stream=None,
+                             want_lse=True):
+    """attn_decode_paged (with sink_logit: attn_decode_paged_sink) for rows that share leading
+    pages, whose keys are read once a group.  Group g is rows group_rows[cu_groups[g]:
+    cu_groups[g+1]] (int32; None: the rows in order), which share the whole pages of their
+    first prefix_lens[g] tokens (int32).  Rows in no group are decoded by themselves.
+    num_splits: splits of each row's own keys (None: enough to fill the GPU) -> (o, lse)."""
+    torch = _torch()
+    index = q.get_device() if isinstance(q, torch.Tensor) else -1
+    _contiguous(q, "q", torch.bfloat16, index)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, d]")
+    B, Hq, d = q.shape
+    P, page, Hkv = _pool(q, k_pages, v_pages, index)
+    Bt, W = _paged_rows(page_table, seqlens, index)
+    if Bt != B:
+        raise ValueError("page_table must be [B, max_pages] and seqlens [B]")
+    _int_tensor(prefix_lens, "prefix_lens", index)
+    n_groups = prefix_lens.numel()
+    _int_vector(prefix_lens, "prefix_lens", n_groups, index)
+    _int_vector(cu_groups, "cu_groups", n_groups + 1, index)
+    n_rows = B
+    if group_rows is not None:
+        _int_tensor(group_rows, "group_rows", index)
+        n_rows = group_rows.numel()
+        _int_vector(group_rows, "group_rows", n_rows, index)
+    sink = _sink(sink_logit, Hq, index)
+    if stream is not None or index != _current_device():
+        with _Call(index, stream):
+            return attn_decode_paged_shared(q, k_pages, v_pages, page_table, seqlens, cu_groups,
+                                            prefix_lens, group_rows, o, lse,
+                                            sink_logit=sink_logit, num_splits=num_splits,
+                                            scale=scale, workspace=workspace, want_lse=want_lse)
+    o, lse = _decode_outputs(q, o, lse, want_lse, index)
+    B, W, P, n_groups, n_rows = map(_c_int, (B, W, P, n_groups, n_rows))
+    if num_splits is None:
+        # four CTAs an SM; rows' own keys are few next to the prefix
+        num_splits = max(1, min(8, -(-608 // max(1, B * Hkv))))
+    num_splits = _c_int(int(num_splits))
+    ws = _bytes(attn_decode_shared_workspace_size(B, Hq, Hkv, d, n_groups, n_rows, W, num_splits),
+                index, workspace)
+    rc = lib.attn_decode_paged_shared(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+        seqlens.data_ptr(), cu_groups.data_ptr(), prefix_lens.data_ptr(), _ptr(group_rows),
+        o.data_ptr(), _ptr(lse), B, Hq, Hkv, d, page, W, P, n_groups, n_rows, num_splits,
+        d ** -0.5 if scale is None else float(scale), sink, ws.data_ptr(), ws.nbytes,
+        _raw_stream(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_decode_paged_shared")
+    return o, lse
 
 
 @functools.lru_cache(maxsize=256)

@@ -2,8 +2,9 @@
 
 The translation units (host ABI, the forward kernels at d <= 128 and at
 d = 256, the decode kernels, the backward kernels at d <= 128 and at d = 256,
-and the host ABI and kernels of rotary positions and the paged cache) compile in parallel, then link into one shared library next to this file.  The CUDA
-runtime is linked statically; the driver's tensor-map encoder is resolved at
+the host ABI and kernels of rotary positions and the paged cache, and those of
+shared and thinned caches) compile in parallel, then link into one shared library
+next to this file.  The CUDA runtime is linked statically; the driver's tensor-map encoder is resolved at
 run time, so the library needs no link-time libcuda.
 """
 from __future__ import annotations
@@ -19,7 +20,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libattn_gb300.so")
 SOURCES = ["attn_api.cu", "attn_fwd_sm103.cu", "attn_fwd256_sm103.cu", "attn_decode_sm103.cu",
            "attn_bwd_sm103.cu", "attn_bwd256_sm103.cu", "attn_cache_api.cu", "attn_rope_sm103.cu",
-           "attn_pages_sm103.cu", "attn_thin_api.cu", "attn_evict_sm103.cu", "attn_mass_sm103.cu"]
+           "attn_pages_sm103.cu", "attn_thin_api.cu", "attn_evict_sm103.cu", "attn_mass_sm103.cu",
+           "attn_shared_sm103.cu"]
 HEADERS = ["sm103_ptx.cuh", "attn_internal.h", "attn_bwd_common.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",

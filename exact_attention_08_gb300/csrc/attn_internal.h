@@ -173,6 +173,34 @@ struct MassArgs {
 int mass_query_tile(int d);
 int mass_key_tile();
 
+// The decode of rows that share a prefix: the groups, and the workspace.
+struct SharedArgs {
+  const __nv_bfloat16* q;  // [B, Hq, d]
+  const int* page_table;
+  const int* seqlens;
+  const int* cu_groups;    // [n_groups + 1] offsets into the list of rows
+  const int* prefix_lens;  // [n_groups]
+  const int* rows;         // [n_rows], or null: row i is entry i
+  int B, Hq, Hkv, G, n_groups, n_rows, max_pages, num_pages;
+  float scale, scale2;       // scale2: scale log2 e
+  int tile_rows, tile_pages;  // set by the launcher
+  // the plan
+  long long* base;  // [n_groups + 1] units before a group
+  int* pages;       // [n_groups] pages that its rows share
+  int* source;      // [n_groups] the row whose table names them
+  int* entry;       // [B] where the row stands in the list
+  int* group;       // [B] its group, -1: none
+  int* start;       // [B] first page of its own
+  int* order;       // [B] rows by own pages
+  // partial results of the prefix
+  float* part_o;    // [shared_part_rows, d]
+  float* part_lse;  // [shared_part_rows]
+  int* status;
+};
+
+constexpr int kSharedMaxCtas = 160;  // CTAs of the prefix kernel at most
+size_t shared_part_rows(int Hq, int Hkv, int d, int n_groups, int n_rows, int max_pages);
+
 constexpr int kEvictMaxUnits = 1 << 24;  // layers x rows x key heads of one call
 
 // Rows cut to their budget by accumulated attention weight.
@@ -250,6 +278,9 @@ cudaError_t launch_attn_append(const RopeArgs& p, const AppendArgs& ap, int num_
 cudaError_t launch_pages_resize(const PagesArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_fork(const PagesArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_compact(const PagesArgs& a, cudaStream_t stream);
+// dec: the decode of the rows' own pages (start and order are the plan's).
+cudaError_t launch_attn_shared(const SharedArgs& a, const DecodeLaunch& dec, int num_sms,
+                               cudaStream_t stream);
 cudaError_t launch_attn_mass(const MassArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_attn_evict(EvictArgs a, int num_sms, cudaStream_t stream);
 cudaError_t launch_wait_timeout_check(int* status, uint64_t limit_ns, cudaStream_t stream);

@@ -1,0 +1,768 @@
+// One-token decode of rows that share the leading pages of their caches (samples of
+// one prompt, chats under one system prompt): the shared keys are read and
+// multiplied once for all rows of a group, the rows' own keys by the split decode,
+// and the partial results are merged by log-sum-exp.
+//
+// Prefix kernel.  For one key head the group's queries, (row, head of the head
+// group) pairs, are the rows of a product with the prefix's keys: up to 256 of them
+// (two 128-row tiles) are an item.  The work is cut into units, a key tile of an item,
+// in the order (group, key head, query tile pair, key tile), and each of the
+// persistent CTAs (one an SM) takes an equal run of units, so one long prompt and
+// many short ones alike fill the GPU.  An item that several CTAs share has a partial
+// result from each.
+//
+// With S = Q K^T and O += P V on the tensor cores and the online softmax between them, a
+// key tile keeps an SM busy for less time than HBM needs to bring its keys and values
+// while an item has at most 256 rows; more rows find them in L2.
+//
+// Two streams (d = 64, 128): S buffer, O and four softmax warps each.  An item of more
+// than 128 rows has a tile in each stream, and every key tile is a job of both; a
+// smaller one has the same tile in both, and they take the key tiles in turn (two
+// partial results).  At d = 256 O alone fills half of tensor memory: one stream, two S
+// buffers, key tiles of 64.
+//
+//   tensor memory  S[2], O[streams] (d columns each)
+//   shared memory  Q (two tiles; one at d = 256), a ring of K and V tiles
+//   warps          0-3, 4-7 softmax of a stream, 8 TMA producer, 9 MMA issuer
+#include "attn_internal.h"
+#include "sm103_ptx.cuh"
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+namespace attn {
+namespace {
+
+using namespace ptx;
+
+constexpr int kPage = 16;
+constexpr int kRows = 128;          // rows of a query tile
+constexpr int kItemRows = 2 * kRows;
+constexpr int kThr = 320;
+constexpr int kWarpProducer = 8;
+constexpr int kWarpIssuer = 9;
+// O is rescaled only when the running maximum has grown by more than 2^8.
+constexpr float kRescaleLog2 = 8.0f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kStreams = D == 256 ? 1 : 2;
+  static constexpr int kTileRows = kStreams * kRows;   // rows of an item at most
+  static constexpr int kKeys = D == 256 ? 64 : 128;    // keys of a key tile
+  static constexpr int kPages = kKeys / kPage;
+  static constexpr int kAtoms = D / 64;
+  static constexpr int kQAtom = kRows * 128;
+  static constexpr int kQTile = kAtoms * kQAtom;
+  static constexpr int kAtom = kKeys * 128;
+  static constexpr int kSlot = kAtoms * kAtom;         // a K or V tile
+  static constexpr int kSlots = D == 64 ? 8 : 5;
+  static constexpr int kOffRing = kStreams * kQTile;
+  static constexpr int kOffBar = kOffRing + kSlots * kSlot;
+  // full, empty of the ring; s_full, p_ready, o_done [2]; q_full, q_empty; drain
+  static constexpr int kNumBars = 2 * kSlots + 6 + 2 + 1;
+  static constexpr int kSmem = kOffBar + (kNumBars + 1) * 8 + 1024;
+  static_assert(kSmem <= 227 * 1024 - 512, "shared memory (512 bytes of it static)");
+  static constexpr uint32_t kColO = 256;
+};
+
+// ---------------------------------------------------------------- plan
+// Workspace of a call (ints): see SharedArgs.  One block: rows to groups, the pages that
+// every group shares, units before each group, first own page of every row, and the
+// rows in the order of their own pages, longest first.
+constexpr int kPlanThreads = 1024;
+constexpr int kBuckets = 4096;
+
+__device__ __forceinline__ int row_length(const SharedArgs& a, int b) {
+  const int L = a.seqlens[b];
+  return max(0, min(L, a.max_pages * kPage));
+}
+
+// Item rows and units of a group of n rows that share `pages` pages.
+__device__ __forceinline__ long long group_units(const SharedArgs& a, int n, int pages) {
+  const long long tiles = (static_cast<long long>(n) * a.G + a.tile_rows - 1) / a.tile_rows;
+  return tiles * a.Hkv * ((pages + a.tile_pages - 1) / a.tile_pages);
+}
+
+__device__ __forceinline__ long long block_scan(long long v, long long* part, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  long long base = 0, all = 0;
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) base += part[w];
+    all += part[w];
+  }
+  *total = all;
+  return base + x - v;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const SharedArgs a) {
+  __shared__ int s_cnt[kBuckets];
+  __shared__ long long s_part[kPlanThreads / 32];
+  __shared__ int s_bad;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_bad = 0;
+  for (int b = tid; b < a.B; b += kPlanThreads) {
+    a.entry[b] = INT_MAX;
+    a.start[b] = 0;
+    a.group[b] = -1;
+  }
+  for (int i = tid; i < kBuckets; i += kPlanThreads) s_cnt[i] = 0;
+  __syncthreads();
+  // offsets that decrease or leave the list: no group is used
+  for (int g = tid; g <= a.n_groups; g += kPlanThreads) {
+    const int c = a.cu_groups[g];
+    if (c < 0 || c > a.n_rows || (g > 0 && c < a.cu_groups[g - 1])) s_bad = 1;
+  }
+  __syncthreads();
+  const bool groups_ok = s_bad == 0;
+  if (!groups_ok && tid == 0) atomicOr(a.status, kStatusBadInput);
+  const int n_groups = groups_ok ? a.n_groups : 0;
+  // a row listed more than once belongs where it stands first
+  if (n_groups > 0) {
+    for (int e = a.cu_groups[0] + tid; e < a.cu_groups[n_groups]; e += kPlanThreads) {
+      const int b = a.rows ? a.rows[e] : e;
+      if (b < 0 || b >= a.B)
+        atomicOr(a.status, kStatusBadInput);
+      else if (atomicMin(&a.entry[b], e) != INT_MAX)
+        atomicOr(a.status, kStatusBadInput);
+    }
+  }
+  __syncthreads();
+  // a warp for each group: its longest row, the pages it shares
+  for (int g = warp; g < n_groups; g += kPlanThreads / 32) {
+    const int e0 = a.cu_groups[g], e1 = a.cu_groups[g + 1];
+    int best = -1, at = INT_MAX, live = 0;
+    for (int e = e0 + lane; e < e1; e += 32) {
+      const int b = a.rows ? a.rows[e] : e;
+      if (b < 0 || b >= a.B || a.entry[b] != e) continue;
+      ++live;
+      const int L = row_length(a, b);
+      if (L > best) best = L, at = b;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const int L = __shfl_xor_sync(0xffffffffu, best, o);
+      const int b = __shfl_xor_sync(0xffffffffu, at, o);
+      if (L > best || (L == best && b < at)) best = L, at = b;
+      live += __shfl_xor_sync(0xffffffffu, live, o);
+    }
+    const int prefix = a.prefix_lens[g];
+    if (lane == 0 && (prefix < 0 || prefix > a.max_pages * kPage))
+      atomicOr(a.status, kStatusBadInput);
+    // a group of one shares nothing: its row is done by the split decode alone
+    int pages = live < 2 || prefix < 0 ? 0 : min(prefix, best) / kPage;
+    if (lane == 0) {
+      a.pages[g] = pages;
+      a.source[g] = at;
+    }
+    for (int e = e0 + lane; e < e1; e += 32) {
+      const int b = a.rows ? a.rows[e] : e;
+      if (b < 0 || b >= a.B || a.entry[b] != e) continue;
+      a.start[b] = min(pages, (row_length(a, b) + kPage - 1) / kPage);
+      a.group[b] = g;
+    }
+  }
+  __syncthreads();
+  // units before each group
+  {
+    long long base = 0;
+    for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
+      const int g = g0 + tid;
+      const long long v = g < n_groups ? group_units(a, a.cu_groups[g + 1] - a.cu_groups[g],
+                                                     a.pages[g])
+                                       : 0;
+      long long all;
+      const long long before = block_scan(v, s_part, &all);
+      if (g < n_groups) a.base[g] = base + before;
+      base += all;
+    }
+    if (tid == 0) a.base[a.n_groups] = base;
+    // a list that is not used: every group ends where it begins
+    if (n_groups == 0)
+      for (int g = tid; g < a.n_groups; g += kPlanThreads) a.base[g] = 0;
+  }
+  // rows by own pages, longest first (a counting sort; rows of one bucket in any order,
+  // which only says which CTA runs first)
+  const int nb = min(a.max_pages + 1, kBuckets);
+  auto bucket = [&](int b) {
+    const int own = (row_length(a, b) + kPage - 1) / kPage - a.start[b];
+    const long long k = static_cast<long long>(a.max_pages - own) * nb / (a.max_pages + 1);
+    return static_cast<int>(k < nb - 1 ? k : nb - 1);
+  };
+  for (int b = tid; b < a.B; b += kPlanThreads) atomicAdd(&s_cnt[bucket(b)], 1);
+  __syncthreads();
+  constexpr int kPer = kBuckets / kPlanThreads;
+  int local[kPer], run = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    local[j] = run;
+    run += s_cnt[tid * kPer + j];
+  }
+  long long all;
+  const int before = static_cast<int>(block_scan(run, s_part, &all));
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) s_cnt[tid * kPer + j] = before + local[j];
+  __syncthreads();
+  for (int b = tid; b < a.B; b += kPlanThreads) a.order[atomicAdd(&s_cnt[bucket(b)], 1)] = b;
+}
+
+// ---------------------------------------------------------------- items
+// One item of the prefix work and this CTA's part of it.
+struct Item {
+  int g, h, mt;           // group, key head, query tile pair
+  int kt, n;              // first key tile of this CTA's part, key tiles in it
+  int rows;               // (row, head) pairs of the item
+  int row0;               // its first pair among the group's
+  int first;              // the group's first list entry
+  int keys;               // keys of the prefix
+  long long part;         // first row of its partial results
+};
+
+struct Walk {
+  long long at, end;      // units
+  int g;
+};
+
+__device__ __forceinline__ bool walk_next(const SharedArgs& a, Walk& w, Item& it) {
+  if (w.at >= w.end) return false;
+  while (a.base[w.g + 1] <= w.at) ++w.g;
+  const int pages = a.pages[w.g];
+  const int e0 = a.cu_groups[w.g], n = a.cu_groups[w.g + 1] - e0;
+  const int tiles = (pages + a.tile_pages - 1) / a.tile_pages;
+  const int pairs = n * a.G;
+  const int mts = (pairs + a.tile_rows - 1) / a.tile_rows;
+  const long long in = w.at - a.base[w.g];
+  const int item = static_cast<int>(in / tiles);
+  it.g = w.g;
+  it.h = item / mts;
+  it.mt = item % mts;
+  it.kt = static_cast<int>(in % tiles);
+  it.n = static_cast<int>(min(static_cast<long long>(tiles - it.kt), w.end - w.at));
+  it.row0 = it.mt * a.tile_rows;
+  it.rows = min(a.tile_rows, pairs - it.row0);
+  it.first = e0;
+  it.keys = pages * kPage;
+  it.part = 2 * (static_cast<long long>(e0) * a.Hq + static_cast<long long>(it.h) * pairs + it.row0) +
+            static_cast<long long>(kItemRows) * blockIdx.x;
+  w.at += it.n;
+  return true;
+}
+
+// Units [at, end) of CTA c among the first min(units, CTAs).
+__device__ __forceinline__ void run_of(const SharedArgs& a, int c, int ctas, long long* at,
+                                       long long* end) {
+  const long long T = a.base[a.n_groups], n = min(T, static_cast<long long>(ctas));
+  *at = c < n ? T * c / n : 0;
+  *end = c < n ? T * (c + 1) / n : 0;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThr, 1)
+    attn_shared_prefix_kernel(const __grid_constant__ CUtensorMap tmK,
+                              const __grid_constant__ CUtensorMap tmV, const SharedArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int abort_s;
+  uint8_t* smem = smem_align1024(smem_raw);
+  uint8_t* ring = smem + C::kOffRing;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* empty = full + C::kSlots;
+  uint64_t* s_full = empty + C::kSlots;  // [S buffer]
+  uint64_t* p_ready = s_full + 2;        // [S buffer]
+  uint64_t* o_done = p_ready + 2;        // [S buffer] O += P V of that buffer's P
+  uint64_t* q_full = o_done + 2;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* drain = q_empty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = &abort_s;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_ready[i], 4);
+      mbar_init(&o_done[i], 1);
+    }
+    mbar_init(q_full, 8);
+    mbar_init(q_empty, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    abort_s = 0;
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  // The plan.  Only then may the decode of the rows' own pages start (it does not wait for
+  // the plan itself, but for every CTA here to have seen it).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  Walk w;
+  run_of(a, blockIdx.x, gridDim.x, &w.at, &w.end);
+  {
+    int lo = 0, hi = a.n_groups;  // the last group with base <= at
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (a.base[mid] <= w.at)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    w.g = lo;
+  }
+  // An item's jobs, in order: S buffer and, with two streams, stream j % 2.  With a tile in
+  // both streams job j is key tile j / 2, else key tile j.
+  auto split = [&](const Item& it) { return C::kStreams == 2 && it.rows > kRows; };
+  Item it;
+
+  if (warp == kWarpProducer) {
+    // ============================================================ TMA producer
+    int n_load = 0;
+    bool ok = true;
+    while (ok && walk_next(a, w, it)) {
+      const int* row = a.page_table + static_cast<size_t>(a.source[it.g]) * a.max_pages;
+      const int pages = it.keys / kPage;
+      auto lookup = [&](int i) -> int {  // page of lane l of the part's key tile i
+        if (i >= it.n || lane >= C::kPages) return 0;
+        return row[min((it.kt + i) * C::kPages + lane, pages - 1)];
+      };
+      auto checked = [&](int page) -> int {
+        if (page < 0 || page >= a.num_pages) {
+          atomicOr(a.status, kStatusBadInput);
+          page = 0;
+        }
+        return page;
+      };
+      auto load = [&](const CUtensorMap* map, int page) {
+        const int s = n_load % C::kSlots;
+        if (n_load >= C::kSlots && !mbar_wait_warp(&empty[s], (n_load / C::kSlots - 1) & 1,
+                                                   abort_flag, kWaitLimitNs)) {
+          ok = false;
+          return;
+        }
+        mbar_arrive_expect_tx_w(&full[s], C::kSlot);
+        if (lane < C::kPages) {
+#pragma unroll
+          for (int at = 0; at < C::kAtoms; ++at)
+            tma_load_4d(ring + s * C::kSlot + at * C::kAtom + lane * kPage * 128, map, &full[s],
+                        at * 64, it.h, 0, page);
+        }
+        __syncwarp();
+        ++n_load;
+      };
+      // K(0), K(1), V(0), K(2), V(1), ...
+      int now = checked(lookup(0)), next = lookup(1);
+      load(&tmK, now);
+      for (int i = 0; ok && i < it.n; ++i) {
+        const int later = lookup(i + 2);
+        if (i + 1 < it.n) {
+          next = checked(next);
+          load(&tmK, next);
+          if (!ok) break;
+        }
+        load(&tmV, now);
+        now = next;
+        next = later;
+      }
+    }
+    if (!ok && lane == 0) {
+      atomicOr(a.status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+    // every copy issued lands before the CTA leaves
+    for (int i = 0; i < C::kSlots; ++i) {
+      const int n = n_load > i ? (n_load - 1 - i) / C::kSlots : -1;
+      if (n >= 0) mbar_wait(&full[i], n & 1, nullptr, kWaitLimitNs);
+    }
+  } else if (warp == kWarpIssuer) {
+    // ============================================================ MMA issuer
+    constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, C::kKeys, false);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, D, true);
+    int n_load = 0;        // tiles of the ring before this item
+    int jobs[2] = {0, 0};  // jobs of each S buffer so far
+    int items = 0;
+    bool ok = true;
+    // K of the part's key tile i is load 0 (i = 0) or 2 i - 1; V is 2 i + 2, or 2 i + 1 last.
+    while (ok && walk_next(a, w, it)) {
+      const bool two = split(it);
+      const int J = two ? 2 * it.n : it.n;
+      auto k_load = [&](int i) { return n_load + (i == 0 ? 0 : 2 * i - 1); };
+      auto v_load = [&](int i) { return n_load + (i + 1 < it.n ? 2 * i + 2 : 2 * i + 1); };
+      if (!mbar_wait_warp(q_full, items & 1, abort_flag, kWaitLimitNs)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      // S of job j = Q K^T
+      auto issue_s = [&](int j) -> bool {
+        const int i = two ? j / 2 : j, l = k_load(i), s = l % C::kSlots, buf = j & 1;
+        if (!(two && (j & 1)) &&
+            !mbar_wait_warp(&full[s], (l / C::kSlots) & 1, abort_flag, kWaitLimitNs))
+          return false;
+        tc_fence_after_sync();
+        const uint64_t dq =
+            sdesc_sw128(smem_addr(smem + (two ? (j & 1) * C::kQTile : 0)), 16, 1024);
+        const uint64_t dk = sdesc_sw128(smem_addr(ring + s * C::kSlot), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t qo = static_cast<uint64_t>(((kk / 4) * C::kQAtom + (kk % 4) * 32) >> 4);
+          const uint64_t ko = static_cast<uint64_t>(((kk / 4) * C::kAtom + (kk % 4) * 32) >> 4);
+          mma_bf16_ss_w(tmem + buf * C::kKeys, dq + qo, dk + ko, idesc_s, kk > 0 ? 1u : 0u);
+        }
+        mma_commit_w(&s_full[buf]);
+        if (!two || (j & 1)) mma_commit_w(&empty[s]);
+        if (j == J - 1) mma_commit_w(q_empty);
+        return true;
+      };
+      ok = issue_s(0);
+      for (int j = 0; ok && j < J; ++j) {
+        if (j + 1 < J && !issue_s(j + 1)) {
+          ok = false;
+          break;
+        }
+        // O += P V: P in the first half of its S buffer's columns, as bf16 pairs
+        const int i = two ? j / 2 : j, l = v_load(i), s = l % C::kSlots, buf = j & 1;
+        const int stream = C::kStreams == 2 ? buf : 0;
+        if (!mbar_wait_warp(&p_ready[buf], jobs[buf] & 1, abort_flag, kWaitLimitNs) ||
+            !mbar_wait_warp(&full[s], (l / C::kSlots) & 1, abort_flag, kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        ++jobs[buf];
+        tc_fence_after_sync();
+        const uint64_t dv = sdesc_sw128(smem_addr(ring + s * C::kSlot), C::kAtom, 1024);
+        const bool first = j < C::kStreams;  // the stream's first job of the item
+#pragma unroll
+        for (int kk = 0; kk < C::kKeys / 16; ++kk)
+          mma_bf16_ts_w(tmem + C::kColO + stream * D, tmem + buf * C::kKeys + 8 * kk,
+                        dv + kk * (2048 >> 4), idesc_o, (!first || kk > 0) ? 1u : 0u);
+        mma_commit_w(&o_done[buf]);
+        if (!two || (j & 1)) mma_commit_w(&empty[s]);
+      }
+      n_load += 2 * it.n;
+      ++items;
+    }
+    if (!ok && lane == 0) {
+      atomicOr(a.status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+    mma_commit_w(drain);
+    mbar_wait(drain, 0, nullptr, kWaitLimitNs);
+  } else {
+    // ============================================================ softmax: warps 0-3, 4-7
+    const int stream = warp / 4;
+    const int r = tid % kRows;
+    const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    int done[2] = {0, 0};  // this stream's jobs in each S buffer so far
+    int items = 0;
+    bool ok = true;
+    while (ok && walk_next(a, w, it)) {
+      const bool two = split(it);
+      const int J = two ? 2 * it.n : it.n;
+      // ---- queries: rows 0-127 to Q tile 0, the others to tile 1 (16 bytes a step)
+      if (items > 0 && !mbar_wait_warp(q_empty, (items - 1) & 1, abort_flag, kWaitLimitNs)) {
+        ok = false;
+        break;
+      }
+      for (int x = tid; x < (two ? 2 : 1) * kRows * (D / 8); x += 256) {
+        const int pr = x / (D / 8), c = x % (D / 8);  // row of the item, 16-byte chunk
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (pr < it.rows) {
+          const int e = it.first + (it.row0 + pr) / a.G;
+          const int b = a.rows ? a.rows[e] : e;
+          if (b >= 0 && b < a.B)
+            v = *reinterpret_cast<const uint4*>(
+                a.q + (static_cast<size_t>(b) * a.Hq + it.h * a.G + (it.row0 + pr) % a.G) * D +
+                c * 8);
+        }
+        const int row = pr % kRows;
+        *reinterpret_cast<uint4*>(smem + (pr / kRows) * C::kQTile + (c / 8) * C::kQAtom +
+                                  row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+      ++items;
+      if (stream >= C::kStreams) continue;  // d = 256: the other warps only load queries
+      // ---- this thread's pair and the keys it sees
+      const int pr = two ? stream * kRows + r : r;
+      int lim = 0;
+      if (pr < it.rows) {
+        const int e = it.first + (it.row0 + pr) / a.G;
+        const int b = a.rows ? a.rows[e] : e;
+        if (b >= 0 && b < a.B) lim = min(row_length(a, b), it.keys);
+      }
+      const int lim_min = __reduce_min_sync(0xffffffffu, pr < it.rows ? lim : INT_MAX);
+      float m_run = -INFINITY, m_used = -INFINITY, l = 0.f, corr = 0.f;
+      int last = -1;  // S buffer of this stream's last job
+      for (int j = C::kStreams == 2 ? stream : 0; j < J; j += C::kStreams) {
+        const int buf = j & 1;
+        const int i = two ? j / 2 : j;
+        if (!mbar_wait_warp(&s_full[buf], done[buf] & 1, abort_flag, kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t tS = tmem + lanes + buf * C::kKeys;
+        uint32_t x[C::kKeys];
+#pragma unroll
+        for (int c = 0; c < C::kKeys / 32; ++c) tmem_ld_x32(tS + 32 * c, x + 32 * c);
+#pragma unroll
+        for (int c = 0; c < C::kKeys / 32; ++c) tmem_ld_wait_x32(x + 32 * c);
+        const int ka = (it.kt + i) * C::kKeys;
+        if (ka + C::kKeys > lim_min) {
+#pragma unroll
+          for (int c = 0; c < C::kKeys; ++c)
+            if (ka + c >= lim) x[c] = __float_as_uint(-INFINITY);
+        }
+        float mx[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx[e] = __uint_as_float(x[e]);
+#pragma unroll
+        for (int c = 8; c < C::kKeys; ++c) mx[c & 7] = fmaxf(mx[c & 7], __uint_as_float(x[c]));
+        const float tmax = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                 fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        m_run = fmaxf(m_run, tmax);
+        // The reference maximum moves only when the scores outgrew it by 2^8; O is then
+        // scaled once the product before has been added (by the whole warp).
+        const bool first = m_used == -INFINITY;
+        const bool grow =
+            first ? m_run != -INFINITY : (m_run - m_used) * a.scale2 > kRescaleLog2;
+        const bool resc = grow && !first;
+        if (__any_sync(0xffffffffu, resc)) {
+          if (!mbar_wait_warp(&o_done[last], (done[last] - 1) & 1, abort_flag, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const float alpha = resc ? ex2_approx((m_used - m_run) * a.scale2) : 1.f;
+          const uint32_t tO = tmem + lanes + C::kColO + stream * D;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_x32(tO + 32 * c, o);
+            tmem_ld_wait_x32(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st_x32(tO + 32 * c, o);
+          }
+          tmem_st_wait();
+          l *= alpha;
+          corr *= alpha;
+        }
+        if (grow) m_used = m_run;
+        const float nms = m_used == -INFINITY ? 0.f : -m_used * a.scale2;
+        float sum0 = 0.f, sum1 = 0.f;
+        uint32_t pk[C::kKeys / 2];
+#pragma unroll
+        for (int e = 0; e < C::kKeys / 2; ++e) {
+          const float p0 = ex2_approx(fmaf(__uint_as_float(x[2 * e]), a.scale2, nms));
+          const float p1 = ex2_approx(fmaf(__uint_as_float(x[2 * e + 1]), a.scale2, nms));
+          if (e & 1)
+            sum1 += p0 + p1;
+          else
+            sum0 += p0 + p1;
+          pk[e] = pack_bf16x2(p0, p1);
+        }
+        l += sum0 + sum1;
+        // O sums P rounded to bf16, l the fp32 values: what the tile's largest lost leaves O's
+        // normaliser too
+        const float ptop = ex2_approx(fmaf(tmax, a.scale2, nms));
+        corr += ptop - __uint_as_float(pack_bf16x2(0.f, ptop) & 0xffff0000u);
+#pragma unroll
+        for (int c = 0; c < C::kKeys / 64; ++c) tmem_st_x32(tS + 32 * c, pk + 32 * c);
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[buf]);
+        ++done[buf];
+        last = buf;
+      }
+      if (!ok) break;
+      // ---- partial result: O / l and the log-sum-exp, rows of this stream
+      if (last >= 0) {
+        if (!mbar_wait_warp(&o_done[last], (done[last] - 1) & 1, abort_flag, kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+      }
+      const bool seen = last >= 0 && l > 0.f;
+      const float inv = seen ? 1.f / (l - corr) : 0.f;
+      const long long prow = it.part + (two ? pr : stream * it.rows + r);
+      if (pr < it.rows) a.part_lse[prow] = seen ? fmaf(m_used, a.scale, logf(l)) : -INFINITY;
+      if (last >= 0) {
+        float* dst = a.part_o + prow * D;
+        const uint32_t tO = tmem + lanes + C::kColO + stream * D;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld_x32(tO + 32 * c, o);
+          tmem_ld_wait_x32(o);
+          if (pr < it.rows) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(dst + 32 * c + e) = make_float4(
+                  seen ? __uint_as_float(o[e]) * inv : 0.f,
+                  seen ? __uint_as_float(o[e + 1]) * inv : 0.f,
+                  seen ? __uint_as_float(o[e + 2]) * inv : 0.f,
+                  seen ? __uint_as_float(o[e + 3]) * inv : 0.f);
+          }
+        }
+        // the next item's first product waits for this warp's next p_ready
+        tc_fence_before_sync();
+      }
+    }
+    if (!ok && lane == 0) {
+      atomicOr(a.status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- merge
+// One block for each (row, query head): the partial results of its group's prefix, CTA by
+// CTA, then those of its own pages, split by split.
+template <int D>
+__global__ void __launch_bounds__(D)
+    attn_shared_merge_kernel(const SharedArgs a, const DecodeLaunch dec, int ctas) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const size_t row = blockIdx.x;
+  const int b = static_cast<int>(row / a.Hq), hq = static_cast<int>(row % a.Hq);
+  const int t = threadIdx.x, S = dec.num_splits;
+  const int g = a.group[b];
+  long long part = 0;
+  int c0 = 0, c1 = -1, streams = 1;
+  long long second = 0;  // distance of the second stream's partial result
+  if (g >= 0 && a.pages[g] > 0) {
+    const int e0 = a.cu_groups[g], pairs = (a.cu_groups[g + 1] - e0) * a.G;
+    const int pr = (a.entry[b] - e0) * a.G + hq % a.G, h = hq / a.G;
+    const int mt = pr / a.tile_rows, in = pr % a.tile_rows;
+    const int rows = min(a.tile_rows, pairs - mt * a.tile_rows);
+    const int mts = (pairs + a.tile_rows - 1) / a.tile_rows;
+    const int tiles = (a.pages[g] + a.tile_pages - 1) / a.tile_pages;
+    const long long u = a.base[g] + (static_cast<long long>(h) * mts + mt) * tiles;
+    const long long T = a.base[a.n_groups], C = min(T, static_cast<long long>(ctas));
+    c0 = static_cast<int>(((u + 1) * C - 1) / T);
+    c1 = static_cast<int>(((u + tiles) * C - 1) / T);
+    part = 2 * (static_cast<long long>(e0) * a.Hq + static_cast<long long>(h) * pairs +
+                mt * a.tile_rows) + in;
+    if (D != 256 && rows <= kRows) {
+      streams = 2;
+      second = rows;
+    }
+  }
+  const float* ls = dec.ws_lse + row * S;
+  const float sg = dec.sink ? dec.sink[hq] : -INFINITY;
+  float M = sg;
+  for (int c = c0; c <= c1; ++c)
+    for (int s = 0; s < streams; ++s)
+      M = fmaxf(M, a.part_lse[part + static_cast<long long>(kItemRows) * c + s * second]);
+  for (int s = 0; s < S; ++s) M = fmaxf(M, ls[s]);
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(dec.o);
+  if (M == -INFINITY) {
+    o[row * D + t] = __float2bfloat16(0.f);
+    if (dec.lse && t == 0) dec.lse[row] = -INFINITY;
+    return;
+  }
+  float wsum = (sg == -INFINITY) ? 0.f : expf(sg - M), acc = 0.f;
+  for (int c = c0; c <= c1; ++c)
+    for (int s = 0; s < streams; ++s) {
+      const long long p = part + static_cast<long long>(kItemRows) * c + s * second;
+      const float lp = a.part_lse[p];
+      if (lp == -INFINITY) continue;  // a part without a key: its O is not written
+      const float w = expf(lp - M);
+      wsum += w;
+      acc += w * a.part_o[p * D + t];
+    }
+  for (int s = 0; s < S; ++s) {
+    const float w = expf(ls[s] - M);
+    wsum += w;
+    acc += w * dec.ws_o[(row * S + s) * D + t];
+  }
+  o[row * D + t] = __float2bfloat16(acc / wsum);
+  if (dec.lse && t == 0) dec.lse[row] = M + logf(wsum);
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_shared(SharedArgs a, const DecodeLaunch& dec, int num_sms,
+                          cudaStream_t stream) {
+  using C = Cfg<D>;
+  a.tile_rows = C::kTileRows;
+  a.tile_pages = C::kPages;
+  static SharedMemoryLimit limit;
+  cudaError_t e = limit.raise(attn_shared_prefix_kernel<D>, C::kSmem);
+  if (e != cudaSuccess) return e;
+  attn_shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int ctas = std::min(num_sms, kSharedMaxCtas);
+  e = launch_dependent(attn_shared_prefix_kernel<D>, dim3(ctas), kThr, C::kSmem, stream, dec.tmK,
+                       dec.tmV, a);
+  if (e != cudaSuccess) return e;
+  if ((e = launch_attn_decode_own(dec, stream)) != cudaSuccess) return e;
+  return launch_dependent(attn_shared_merge_kernel<D>, dim3(a.B * a.Hq), D, 0, stream, a, dec, ctas);
+}
+
+}  // namespace
+
+size_t shared_part_rows(int Hq, int Hkv, int d, int n_groups, int n_rows, int max_pages) {
+  const size_t tile = d == 256 ? Cfg<256>::kTileRows : Cfg<128>::kTileRows;
+  const size_t pages = d == 256 ? Cfg<256>::kPages : Cfg<128>::kPages;
+  const size_t pairs = static_cast<size_t>(n_rows) * (Hq / Hkv);
+  const size_t units = (pairs / tile + n_groups) * Hkv * ((max_pages + pages - 1) / pages);
+  return 2 * static_cast<size_t>(n_rows) * Hq +
+         kItemRows * std::min<size_t>(units, kSharedMaxCtas);
+}
+
+cudaError_t launch_attn_shared(const SharedArgs& a, const DecodeLaunch& dec, int num_sms,
+                               cudaStream_t stream) {
+  if (dec.d == 64) return launch_shared<64>(a, dec, num_sms, stream);
+  if (dec.d == 128) return launch_shared<128>(a, dec, num_sms, stream);
+  if (dec.d == 256) return launch_shared<256>(a, dec, num_sms, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace attn

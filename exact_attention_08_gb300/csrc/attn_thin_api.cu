@@ -14,6 +14,7 @@ using namespace attn;
 namespace {
 
 constexpr int kGridMax = 65535;  // blocks along y or z of a grid
+constexpr int kGroupsMax = 1 << 20;
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -28,8 +29,9 @@ int check_heads(int B, int Hq, int Hkv, int d, int page_size, int max_pages, int
   if (page_size != 16) return set_error(ATTN_ERR_UNSUPPORTED, "page size %d (16)", page_size);
   if (static_cast<long long>(max_pages) * page_size > (1 << 30))
     return set_error(ATTN_ERR_INVALID_ARG, "max_pages_per_seq too large");
-  if (B > kGridMax || Hq > kGridMax)
-    return set_error(ATTN_ERR_INVALID_ARG, "B=%d or Hq=%d above %d", B, Hq, kGridMax);
+  if (B > kGridMax || Hq > kGridMax || static_cast<long long>(B) * Hq > (1 << 30))
+    return set_error(ATTN_ERR_INVALID_ARG, "B=%d or Hq=%d above %d, or B * Hq above 2^30", B, Hq,
+                     kGridMax);
   return ATTN_OK;
 }
 
@@ -98,9 +100,110 @@ size_t mass_tiles(int max_pages) {
 
 size_t pad16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
+// Workspace of attn_decode_paged_shared, in bytes from its start.
+struct SharedLayout {
+  size_t decode, base, ints, part_lse, part_o, bytes;
+};
+
+SharedLayout shared_layout(int B, int Hq, int Hkv, int d, int n_groups, int n_rows, int max_pages,
+                           int num_splits) {
+  SharedLayout l;
+  const size_t rows = shared_part_rows(Hq, Hkv, d, n_groups, n_rows, max_pages);
+  l.decode = 0;
+  l.part_o = pad16(attn_decode_workspace_size(B, Hq, d, num_splits));
+  l.part_lse = l.part_o + rows * d * sizeof(float);
+  l.base = pad16(l.part_lse + rows * sizeof(float));
+  l.ints = l.base + (static_cast<size_t>(n_groups) + 1) * sizeof(long long);
+  l.bytes = l.ints + (2 * static_cast<size_t>(n_groups) + 4 * static_cast<size_t>(B)) * sizeof(int);
+  return l;
+}
+
+int check_groups(int Hq, int n_groups, int n_rows) {
+  if (n_groups < 0 || n_rows < 0 || n_groups > kGroupsMax || n_rows > kGroupsMax ||
+      static_cast<long long>(n_rows) * Hq > (1 << 30))
+    return set_error(ATTN_ERR_INVALID_ARG, "bad sizes (n_groups=%d n_rows=%d)", n_groups, n_rows);
+  return ATTN_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+ATTN_API size_t attn_decode_shared_workspace_size(int B, int Hq, int Hkv, int d, int n_groups,
+                                                  int n_rows, int max_pages_per_seq,
+                                                  int num_splits) {
+  if (check_heads(B, Hq, Hkv, d, 16, max_pages_per_seq, 1) != ATTN_OK ||
+      check_groups(Hq, n_groups, n_rows) != ATTN_OK || num_splits < 1 || num_splits > 64) {
+    clear_error();
+    return 0;
+  }
+  return shared_layout(B, Hq, Hkv, d, n_groups, n_rows, max_pages_per_seq, num_splits).bytes;
+}
+
+ATTN_API int attn_decode_paged_shared(const void* q, const void* k_pages, const void* v_pages,
+                                      const int* page_table, const int* seqlens,
+                                      const int* cu_groups, const int* prefix_lens,
+                                      const int* group_rows, void* o, float* lse, int B, int Hq,
+                                      int Hkv, int d, int page_size, int max_pages_per_seq,
+                                      int num_pages_total, int n_groups, int n_rows,
+                                      int num_splits, float scale, const float* sink_logit,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  int rc = check_heads(B, Hq, Hkv, d, page_size, max_pages_per_seq, num_pages_total);
+  if (rc != ATTN_OK) return rc;
+  if ((rc = check_groups(Hq, n_groups, n_rows)) != ATTN_OK) return rc;
+  if (group_rows == nullptr && n_rows > B)
+    return set_error(ATTN_ERR_INVALID_ARG, "n_rows=%d of B=%d rows", n_rows, B);
+  DecodeLaunch dec;
+  rc = decode_common(&dec, q, k_pages, v_pages, page_table, seqlens, o, lse, B, Hq, Hkv, d,
+                     max_pages_per_seq, num_pages_total, num_splits, scale, sink_logit);
+  if (rc != ATTN_OK || B == 0) return rc;
+  if (n_groups > 0 && (!cu_groups || !prefix_lens))
+    return set_error(ATTN_ERR_INVALID_ARG, "null pointer");
+  if (!aligned4(cu_groups) || !aligned4(prefix_lens) || !aligned4(group_rows))
+    return set_error(ATTN_ERR_INVALID_ARG, "misaligned pointer");
+  const SharedLayout l =
+      shared_layout(B, Hq, Hkv, d, n_groups, n_rows, max_pages_per_seq, num_splits);
+  if ((rc = check_workspace(workspace, workspace_bytes, l.bytes)) != ATTN_OK) return rc;
+  char* ws = static_cast<char*>(workspace);
+  const size_t rows = static_cast<size_t>(B) * Hq * num_splits;
+  SharedArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.page_table = page_table;
+  a.seqlens = seqlens;
+  a.cu_groups = cu_groups;
+  a.prefix_lens = prefix_lens;
+  a.rows = group_rows;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.n_groups = n_groups;
+  a.n_rows = n_rows;
+  a.max_pages = max_pages_per_seq;
+  a.num_pages = num_pages_total;
+  a.scale = scale;
+  a.scale2 = scale * 1.4426950408889634f;
+  a.part_o = reinterpret_cast<float*>(ws + l.part_o);
+  a.part_lse = reinterpret_cast<float*>(ws + l.part_lse);
+  a.base = reinterpret_cast<long long*>(ws + l.base);
+  a.pages = reinterpret_cast<int*>(ws + l.ints);
+  a.source = a.pages + n_groups;
+  a.entry = a.source + n_groups;
+  a.group = a.entry + B;
+  a.start = a.group + B;
+  a.order = a.start + B;
+  dec.ws_o = reinterpret_cast<float*>(ws);
+  dec.ws_lse = dec.ws_o + rows * d;
+  dec.order = a.order;
+  dec.start = a.start;
+  int num_sms = 0;
+  if ((rc = decode_maps(&dec, k_pages, v_pages, &num_sms)) != ATTN_OK) return rc;
+  a.status = dec.status;
+  const cudaError_t e = launch_attn_shared(a, dec, num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_error(e, "attn_decode_paged_shared launch");
+}
 
 ATTN_API size_t attn_decode_mass_workspace_size(int B, int Hq, int d, int max_pages_per_seq,
                                                 int num_splits) {

@@ -553,6 +553,47 @@ ATTN_API int attn_pages_compact(int* page_table, const int* seqlens, int* refs, 
                                 void* stream);
 
 /*
+ * One-token decode of rows that share the leading pages of their caches: the
+ * samples of one prompt (attn_pages_fork), chats under one system prompt.  The
+ * shared keys are read once a group instead of once a row.  There is no
+ * counterpart on the source pages.  o and lse are those of attn_decode_paged
+ * (_sink: sink_logit may be NULL) on the same cache, up to rounding.
+ *   group_rows [n_rows] DEVICE int32: rows of the batch, group by group; group g
+ *     is entries cu_groups[g] .. cu_groups[g+1]-1 (DEVICE int32 [n_groups + 1]).
+ *     NULL: entry i is row i.  Rows in no group are decoded by themselves.
+ *   prefix_lens [n_groups] DEVICE int32: the first prefix_lens[g] / 16 (whole)
+ *     pages hold the same keys and values in every row of group g, as far as
+ *     the row reaches; each row's own table names them too (they are read
+ *     through the table of the group's longest row).  seqlens [B] counts all
+ *     keys of a row, shared ones among them; a row may end inside the prefix
+ *     or hold nothing.
+ *   num_splits (1..64): splits of each row's own keys.
+ *   Device-side checks (ATTN_ERR_BAD_INPUT; the results stay those of
+ *   attn_decode_paged): offsets that decrease or leave [0, n_rows] (no group is
+ *   used); a row index out of [0, B) (skipped) or listed twice (it belongs where
+ *   it stands first); a prefix below 0 (0) or past the table (the longest row's
+ *   length); a length out of range (taken into [0, max_pages_per_seq * 16]).  A
+ *   page out of range reads page 0 in the prefix, zeros in a row's own pages.
+ *   Partial results are merged in a fixed order: repeated calls give identical
+ *   bits.
+ *   workspace: attn_decode_shared_workspace_size(...) bytes (0 on invalid
+ *   sizes), 16-byte aligned, overwritten; calls that may overlap need one
+ *   each.  B and Hq at most 65,535, n_groups and n_rows at most 2^20, B * Hq
+ *   and n_rows * Hq at most 2^30.
+ */
+ATTN_API size_t attn_decode_shared_workspace_size(int B, int Hq, int Hkv, int d, int n_groups,
+                                                  int n_rows, int max_pages_per_seq,
+                                                  int num_splits);
+ATTN_API int attn_decode_paged_shared(const void* q, const void* k_pages, const void* v_pages,
+                                      const int* page_table, const int* seqlens,
+                                      const int* cu_groups, const int* prefix_lens,
+                                      const int* group_rows, void* o, float* lse, int B, int Hq,
+                                      int Hkv, int d, int page_size, int max_pages_per_seq,
+                                      int num_pages_total, int n_groups, int n_rows,
+                                      int num_splits, float scale, const float* sink_logit,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Attention weight that the keys of a cache accumulate, and eviction by it.
  * There is no counterpart on the source pages: these calls are additions of
  * this library for caches that outgrow their memory.
@@ -577,7 +618,7 @@ ATTN_API int attn_pages_compact(int* page_table, const int* seqlens, int* refs, 
  * (ATTN_ERR_BAD_INPUT).  Sums run over the heads in order, in fp32.
  *   workspace: attn_decode_mass_workspace_size(...) bytes (the decode's, and
  *   the raw scores, fp32 [B, Hq, max_pages_per_seq * 16]), 16-byte aligned.
- *   B and Hq at most 65,535.
+ *   B and Hq at most 65,535, B * Hq at most 2^30.
  */
 ATTN_API size_t attn_decode_mass_workspace_size(int B, int Hq, int d, int max_pages_per_seq,
                                                 int num_splits);
@@ -611,7 +652,7 @@ ATTN_API int attn_decode_paged_mass(const void* q, const void* k_pages, const vo
  *   Each partial sum is formed by one CTA and they are added in a fixed order:
  *   repeated calls give identical bits.
  *   workspace: attn_mass_workspace_size(...) bytes, 16-byte aligned.  B and Hq
- *   at most 65,535, max_Sq and total_q at most 2^30.
+ *   at most 65,535, B * Hq, max_Sq and total_q at most 2^30.
  */
 ATTN_API size_t attn_mass_workspace_size(int B, int Hkv, int max_pages_per_seq);
 ATTN_API int attn_mass_paged(const void* q, const float* lse, const void* k_pages,

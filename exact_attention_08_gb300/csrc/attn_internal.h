@@ -161,17 +161,20 @@ struct MassArgs {
   const int* new_tokens;      // [B], may be null
   int B, Hq, Hkv, G, d;
   int GP, TQ, HC;  // heads and tokens of a query tile; tiles that the group's heads take
+  unsigned long long tq_mul;  // 2^40 / TQ, rounded up
   int max_Sq, total_q, max_pages, num_pages, slots, max_kt;
   float scale2;  // scale log2 e
   int causal, window, n_sink;
   long long* ws_plan;  // [B, max_kt + 1] units before a key tile; [B + 1] before a sequence
-  float* ws_part;      // partial sums [B * Hkv * max_kt + CTAs, key tile]
+  float* ws_part;      // partial sums [B * Hkv * max_kt + CTAs, mass_partial_floats]
   int* status;
 };
 
-// Columns of a query tile and keys of a key tile of launch_attn_mass.
+// Columns of a query tile, keys of a key tile and floats of a partial sum of
+// launch_attn_mass.
 int mass_query_tile(int d);
 int mass_key_tile();
+int mass_partial_floats();
 
 // The decode of rows that share a prefix: the groups, and the workspace.
 struct SharedArgs {

@@ -18,8 +18,11 @@
 //
 //   tensor memory  S[row tile][2], kQN columns each
 //   shared memory  K ring (256 keys a slot), Q ring, LSEs, barriers
-//   warps          0-3 row tile 0, 4-7 row tile 1, 8 TMA producer, 9 MMA issuer,
-//                  10 LSEs of the query tiles (two tiles ahead, in column order)
+//   warps          0-3 and 8-11 row tile 0, 4-7 and 12-15 row tile 1 (each half the
+//                  columns: with one warp a scheduler and row tile the exponential
+//                  units idled between tensor-memory reads, 1,660 cycles a unit against
+//                  the 1,024 they need), 16 TMA producer, 17 MMA issuer, 18 LSEs of the
+//                  query tiles (in column order, loaded a tile ahead)
 //
 // Split.  The work is cut into units, a query tile against a key tile, in the order
 // (sequence, key head, key tile, query tile), and each of the persistent CTAs (one an
@@ -36,6 +39,7 @@
 #include "sm103_ptx.cuh"
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 namespace attn {
@@ -47,10 +51,12 @@ constexpr int kPage = 16;
 constexpr int kRows = 128;            // keys of a row tile
 constexpr int kKeys = 2 * kRows;      // keys of a key tile
 constexpr int kPagesPerTile = kKeys / kPage;
-constexpr int kThr = 352;
-constexpr int kWarpProducer = 8;
-constexpr int kWarpIssuer = 9;
-constexpr int kWarpLse = 10;
+constexpr int kHalves = 2;            // warps that share a quarter of a row tile's rows
+constexpr int kSumWarps = 8 * kHalves;
+constexpr int kThr = 32 * (kSumWarps + 3);
+constexpr int kWarpProducer = kSumWarps;
+constexpr int kWarpIssuer = kSumWarps + 1;
+constexpr int kWarpLse = kSumWarps + 2;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -89,6 +95,22 @@ __device__ __forceinline__ bool load_seq(const MassArgs& a, int b, Seq& s) {
 
 __device__ __forceinline__ int key_tiles(const Seq& s) { return (s.L + kKeys - 1) / kKeys; }
 
+// x / TQ for 0 <= x < 2^31: the multiplier is 2^40 / TQ rounded up, so the error, x (TQ - 1)
+// / 2^40 at most, stays below 1 / TQ (a division by a run-time value is 100 cycles and
+// more, and stands in every step of the walk).
+__device__ __forceinline__ int in_tiles(const MassArgs& a, int x) {
+  return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(x)) * a.tq_mul) >>
+                          40);
+}
+
+// The query tile of a unit: its first token and its head group.
+__device__ __forceinline__ int tile_token(const MassArgs& a, int u) {
+  return (a.HC == 1 ? u : u / a.HC) * a.TQ;
+}
+__device__ __forceinline__ int tile_head(const MassArgs& a, int u) {
+  return a.HC == 1 ? 0 : (u % a.HC) * a.GP;
+}
+
 // Query tiles (of TQ tokens) with a query that sees a key of key tile kt: the first, and how
 // many.
 __device__ __forceinline__ int query_tiles(const MassArgs& a, const Seq& s, int kt, int* first) {
@@ -98,8 +120,8 @@ __device__ __forceinline__ int query_tiles(const MassArgs& a, const Seq& s, int 
   if (a.window > 0 && ka >= a.n_sink)
     hi = static_cast<int>(min(static_cast<long long>(hi),
                               static_cast<long long>(kb) + a.window - 1 - s.off));
-  *first = lo / a.TQ;
-  return hi < lo ? 0 : hi / a.TQ - lo / a.TQ + 1;
+  *first = in_tiles(a, lo);
+  return hi < lo ? 0 : in_tiles(a, hi) - *first + 1;
 }
 
 __device__ __forceinline__ long long* ws_cum(const MassArgs& a, int b) {
@@ -186,21 +208,69 @@ __device__ __forceinline__ int walk_units(const Walk& w) {
   return static_cast<int>(min(static_cast<long long>(w.n - w.u), w.left));
 }
 
-// Sums of a thread's weights over 32 columns.  kMasked: only columns [lo, hi) count.
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+
+// Adds a thread's weights over 32 columns.  kMasked: only columns [lo, hi) count.
 template <bool kMasked>
 __device__ __forceinline__ void add_columns(const uint32_t* r, const float* nl, int c0,
-                                            float scale2, int lo, int hi, float* acc) {
+                                            float scale2, int lo, int hi, float2* acc) {
+  const float2 sc = make_float2(scale2, scale2);
 #pragma unroll
   for (int j = 0; j < 32; j += 4) {
     const float4 l = *reinterpret_cast<const float4*>(nl + c0 + j);
-    const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float p = ex2_approx(fmaf(__uint_as_float(r[j + e]), scale2, lv[e]));
-      if (kMasked) p = (c0 + j + e >= lo && c0 + j + e < hi) ? p : 0.f;
-      acc[e] += p;
+    float2 x = fma2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), sc,
+                    make_float2(l.x, l.y));
+    float2 y = fma2(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), sc,
+                    make_float2(l.z, l.w));
+    x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+    y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+    if (kMasked) {
+      const int c = c0 + j;
+      x.x = c >= lo && c < hi ? x.x : 0.f;
+      x.y = c + 1 >= lo && c + 1 < hi ? x.y : 0.f;
+      y.x = c + 2 >= lo && c + 2 < hi ? y.x : 0.f;
+      y.y = c + 3 >= lo && c + 3 < hi ? y.y : 0.f;
     }
+    acc[0] = add2(acc[0], x);
+    acc[1] = add2(acc[1], y);
   }
+}
+
+// All columns of a tile, the next 32 on their way from tensor memory meanwhile; `free` is
+// called once the tile has been read.
+template <int kQN, bool kMasked, typename Free>
+__device__ __forceinline__ float add_tile(uint32_t tS, const float* nl, float scale2, int lo,
+                                          int hi, Free free) {
+  float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  uint32_t x[2][32];
+  tmem_ld_x32(tS, x[0]);
+#pragma unroll
+  for (int c = 0; c < kQN / 32; ++c) {
+    tmem_ld_wait_x32(x[c & 1]);
+    if (c + 1 < kQN / 32)
+      tmem_ld_x32(tS + 32 * (c + 1), x[(c + 1) & 1]);
+    else
+      free();
+    add_columns<kMasked>(x[c & 1], nl, 32 * c, scale2, lo, hi, acc);
+  }
+  const float2 s = add2(acc[0], acc[1]);
+  return s.x + s.y;
 }
 
 template <int D>
@@ -240,11 +310,11 @@ __global__ void __launch_bounds__(kThr, 1)
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 4);
+      mbar_init(&s_empty[i], kSumWarps / 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&l_full[i], 1);
-      mbar_init(&l_empty[i], 8);
+      mbar_init(&l_empty[i], kSumWarps);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -381,8 +451,7 @@ __global__ void __launch_bounds__(kThr, 1)
 #pragma unroll
           for (int at = 0; at < C::kAtoms; ++at)
             tma_load_4d_w(smem + C::kOffQ + qs * C::kQBytes + at * C::kQAtom, &tmQ, &q_full[qs],
-                          at * 64, w.h * a.G + (u % a.HC) * a.GP,
-                          w.s.q_base + (u / a.HC) * a.TQ, 0);
+                          at * 64, w.h * a.G + tile_head(a, u), w.s.q_base + tile_token(a, u), 0);
           ++qn;
         }
         w.left -= units;
@@ -466,42 +535,65 @@ __global__ void __launch_bounds__(kThr, 1)
       mbar_wait(drain, 0, nullptr, kWaitLimitNs);
     } else if (warp == kWarpLse) {
       // ============================================================ LSEs
-      // -LSE log2 e of every column of a query tile, -inf where there is no query.
+      // -LSE log2 e of every column of a query tile, -inf where there is no query; the loads of
+      // a tile are in flight while the one before waits for its buffer.
       constexpr int kPer = C::kQN / 32;
-      int n = 0;
-      bool ok = true;
-      do {
-        const int units = walk_units(w);
-        for (int i = 0; i < units; ++i, ++n) {
-          const int u = w.first * a.HC + w.u + i;
-          float v[kPer];
+      int tok[kPer], head[kPer];  // of this lane's columns
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            const int c = j * 32 + lane, tok = (u / a.HC) * a.TQ + c / a.GP;
-            v[j] = -INFINITY;
-            if (c < a.GP * a.TQ && tok < w.s.Lq)
-              v[j] = -kLog2e * a.lse[static_cast<size_t>(w.h * a.G + (u % a.HC) * a.GP + c % a.GP) *
-                                         a.total_q + w.s.q_base + tok];
-          }
-          if (n >= 2 && !mbar_wait_warp(&l_empty[n & 1], (n / 2 - 1) & 1, abort_flag, kWaitLimitNs)) {
-            ok = false;
-            break;
-          }
-          float* nl = reinterpret_cast<float*>(smem + C::kOffLse) + (n & 1) * C::kQN;
+      for (int j = 0; j < kPer; ++j) {
+        const int c = j * 32 + lane;
+        tok[j] = c < a.GP * a.TQ ? c / a.GP : INT_MAX / 2;
+        head[j] = c % a.GP;
+      }
+      int n = 0, units = walk_units(w), i = 0;
+      int pb = -1, ph = -1, pu = -1;
+      float v[kPer], next[kPer];
+      auto fetch = [&] {
+        const int u = w.first * a.HC + w.u + i;
+        if (w.b == pb && w.h == ph && u == pu) return;
+        pb = w.b, ph = w.h, pu = u;
+        const int t0 = tile_token(a, u);
+        const float* lse = a.lse + static_cast<size_t>(w.h * a.G + tile_head(a, u)) * a.total_q +
+                           w.s.q_base + t0;
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) nl[j * 32 + lane] = v[j];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&l_full[n & 1]);
+        for (int j = 0; j < kPer; ++j)
+          next[j] = t0 + tok[j] < w.s.Lq
+                        ? lse[static_cast<size_t>(head[j]) * a.total_q + tok[j]]
+                        : INFINITY;
+      };
+      fetch();
+      bool ok = true, more = true;
+      while (more) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) v[j] = next[j] * -kLog2e;
+        if (++i == units) {
+          w.left -= units;
+          more = walk_next(a, w);
+          if (more) {
+            units = walk_units(w);
+            i = 0;
+          }
         }
-        w.left -= units;
-      } while (ok && walk_next(a, w));
+        if (more) fetch();
+        if (n >= 2 && !mbar_wait_warp(&l_empty[n & 1], (n / 2 - 1) & 1, abort_flag, kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        float* nl = reinterpret_cast<float*>(smem + C::kOffLse) + (n & 1) * C::kQN;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) nl[j * 32 + lane] = v[j];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&l_full[n & 1]);
+        ++n;
+      }
       if (!ok && lane == 0) {
         atomicOr(a.status, kStatusTimeout);
         *abort_flag = 1;
       }
     } else {
-      // ============================================================ sums: warps 0-3, 4-7
-      const int t = warp / 4;
+      // ============================================================ sums: warps 0-15
+      constexpr int kCols = C::kQN / kHalves;  // columns of this warp
+      const int t = (warp / 4) % 2, half = warp / 8, c0 = half * kCols;
       const int r = tid % kRows;  // the row of this thread
       const uint32_t taddr = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
       int cnt = 0;
@@ -519,23 +611,21 @@ __global__ void __launch_bounds__(kThr, 1)
             break;
           }
           tc_fence_after_sync();
-          const float* nl = reinterpret_cast<const float*>(smem + C::kOffLse) + buf * C::kQN;
-          const int i0 = ((w.first * a.HC + w.u + i) / a.HC) * a.TQ;  // the tile's first token
-          const uint32_t tS = taddr + (t * 2 + buf) * C::kQN;
+          const float* nl = reinterpret_cast<const float*>(smem + C::kOffLse) + buf * C::kQN + c0;
+          const int i0 = tile_token(a, w.first * a.HC + w.u + i);  // the tile's first token
+          const uint32_t tS = taddr + (t * 2 + buf) * C::kQN + c0;
           // Does every row see every query of the tile?
           const bool interior =
               i0 + a.TQ <= w.s.Lq && (!a.causal || ka + kRows - 1 <= i0 + w.s.off) &&
               (a.window <= 0 || ka + kRows <= a.n_sink ||
                static_cast<long long>(ka) + a.window > i0 + a.TQ - 1 + w.s.off);
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          auto free = [&] {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[t * 2 + buf]);
+          };
           if (interior) {
-#pragma unroll
-            for (int c = 0; c < C::kQN; c += 32) {
-              uint32_t x[32];
-              tmem_ld_x32(tS + c, x);
-              tmem_ld_wait_x32(x);
-              add_columns<false>(x, nl, c, a.scale2, 0, 0, acc);
-            }
+            sum += add_tile<kCols, false>(tS, nl, a.scale2, 0, 0, free);
           } else {
             // columns [lo, hi): the tokens of the tile that see key ka + r
             const int key = ka + r;
@@ -543,29 +633,19 @@ __global__ void __launch_bounds__(kThr, 1)
             if (a.causal) lo = max(0, key - w.s.off - i0);
             if (a.window > 0 && key >= a.n_sink)
               hi = min(hi, static_cast<long long>(key) + a.window - w.s.off - i0);
-            const int clo = static_cast<int>(min(lo, static_cast<long long>(a.TQ))) * a.GP;
-            const int chi = static_cast<int>(max(hi, 0LL)) * a.GP;
-#pragma unroll 1
-            for (int c = 0; c < C::kQN; c += 32) {
-              uint32_t x[32];
-              tmem_ld_x32(tS + c, x);
-              tmem_ld_wait_x32(x);
-              add_columns<true>(x, nl, c, a.scale2, clo, chi, acc);
-            }
+            sum += add_tile<kCols, true>(
+                tS, nl, a.scale2,
+                static_cast<int>(min(lo, static_cast<long long>(a.TQ))) * a.GP - c0,
+                static_cast<int>(max(hi, 0LL)) * a.GP - c0, free);
           }
-          tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&s_empty[t * 2 + buf]);
-            mbar_arrive(&l_empty[buf]);
-          }
+          if (lane == 0) mbar_arrive(&l_empty[buf]);
           ++cnt;
-          sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
         }
         if (!ok) break;
         const size_t slot =
             (static_cast<size_t>(w.b) * a.Hkv + w.h) * a.max_kt + w.kt + blockIdx.x;
-        a.ws_part[slot * kKeys + t * kRows + r] = sum;
+        a.ws_part[(slot * kHalves + half) * kKeys + t * kRows + r] = sum;
         w.left -= units;
       } while (walk_next(a, w));
       if (!ok && lane == 0) {
@@ -612,7 +692,9 @@ __global__ void __launch_bounds__(kAddThreads) attn_mass_add_kernel(const MassAr
       const int c0 = static_cast<int>(((u + 1) * C - 1) / T);
       const int c1 = static_cast<int>(((u + n) * C - 1) / T);
       const size_t slot = (static_cast<size_t>(b) * a.Hkv + h) * a.max_kt + kt;
-      for (int c = c0; c <= c1; ++c) w += a.ws_part[(slot + c) * kKeys + t % kKeys];
+      for (int c = c0; c <= c1; ++c)
+        for (int i = 0; i < kHalves; ++i)
+          w += a.ws_part[((slot + c) * kHalves + i) * kKeys + t % kKeys];
     }
     const bool is_new = t >= s.L - fresh;
     a.mass_out[row + t] = is_new ? w : a.mass[row + t] + w;
@@ -656,6 +738,7 @@ cudaError_t launch_mass(const MassArgs& a, int num_sms, cudaStream_t stream) {
 
 int mass_query_tile(int d) { return d == 256 ? Cfg<256>::kQN : Cfg<128>::kQN; }
 int mass_key_tile() { return kKeys; }
+int mass_partial_floats() { return kHalves * kKeys; }
 
 cudaError_t launch_attn_mass(const MassArgs& a, int num_sms, cudaStream_t stream) {
   if (a.d == 64) return launch_mass<64>(a, num_sms, stream);

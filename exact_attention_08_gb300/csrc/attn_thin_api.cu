@@ -255,7 +255,7 @@ ATTN_API size_t attn_mass_workspace_size(int B, int Hkv, int max_pages_per_seq) 
   if (B < 0 || Hkv <= 0 || max_pages_per_seq <= 0) return 0;
   const size_t kt = mass_tiles(max_pages_per_seq);
   return pad16((static_cast<size_t>(B) * (kt + 2) + 1) * sizeof(long long)) +
-         (static_cast<size_t>(B) * Hkv * kt + kMaxSms) * mass_key_tile() * sizeof(float);
+         (static_cast<size_t>(B) * Hkv * kt + kMaxSms) * mass_partial_floats() * sizeof(float);
 }
 
 ATTN_API int attn_mass_paged(const void* q, const float* lse, const void* k_pages,
@@ -303,6 +303,7 @@ ATTN_API int attn_mass_paged(const void* q, const float* lse, const void* k_page
   }
   a.TQ = tile / a.GP;
   a.HC = a.G / a.GP;
+  a.tq_mul = ((1ull << 40) + a.TQ - 1) / a.TQ;
   if ((rc = page_pool_map(&a.tmK, k_pages, d, Hkv, num_pages_total, "k_pages")) != ATTN_OK)
     return rc;
   // with no query at all the map is of nothing that is read

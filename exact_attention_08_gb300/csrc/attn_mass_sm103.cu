@@ -11,18 +11,24 @@
 // (query, key), and the tensor cores' 512 cycles for 128 x 128 x 128 against 512
 // of the exponential units.
 //
-// Tile.  256 keys (two row tiles) against each query tile: one row tile alone
-// would read 64 bytes of Q a cycle and SM from L2, more than it delivers.  Four
-// warps for each row tile; two S buffers each, so that the product of the next
-// query tile runs under the exponentials of this one.
+// Operands.  With both in shared memory, M = N = 128, the tensor cores read 128 bytes
+// of it a cycle, all there is, and the tiles' arrival and the LSEs come on top: 1,570
+// cycles a unit (two row tiles against one query tile) instead of 1,024.  So a key
+// tile with kMinTs query tiles or more is copied to tensor memory once and read from
+// there as the A operand; the copy costs about a unit's time, which shorter runs
+// would not win back.
 //
-//   tensor memory  S[row tile][2], kQN columns each
+// Tile.  256 keys (two row tiles) against each query tile: one row tile alone
+// would read 64 bytes of Q a cycle and SM from L2, more than it delivers.  Eight
+// warps for each row tile, and a ring of S buffers, so that the next products run under the
+// exponentials of these.
+//
+//   tensor memory  ring of S (kQN columns each), K of both row tiles (d / 2 columns each)
 //   shared memory  K ring (256 keys a slot), Q ring, LSEs, barriers
-//   warps          0-3 and 8-11 row tile 0, 4-7 and 12-15 row tile 1 (each half the
-//                  columns: with one warp a scheduler and row tile the exponential
-//                  units idled between tensor-memory reads, 1,660 cycles a unit against
-//                  the 1,024 they need), 16 TMA producer, 17 MMA issuer, 18 LSEs of the
-//                  query tiles (in column order, loaded a tile ahead)
+//   warps          0-3 and 8-11 sums of row tile 0 (half the columns each), 4-7 and
+//                  12-15 of row tile 1; 16 TMA producer; 17 MMA issuer (which waits
+//                  for the next product's barriers between the halves of this one);
+//                  18 LSEs of the query tiles (in column order, loaded a tile ahead)
 //
 // Split.  The work is cut into units, a query tile against a key tile, in the order
 // (sequence, key head, key tile, query tile), and each of the persistent CTAs (one an
@@ -51,12 +57,13 @@ constexpr int kPage = 16;
 constexpr int kRows = 128;            // keys of a row tile
 constexpr int kKeys = 2 * kRows;      // keys of a key tile
 constexpr int kPagesPerTile = kKeys / kPage;
-constexpr int kHalves = 2;            // warps that share a quarter of a row tile's rows
+constexpr int kHalves = 2;  // warps that share 32 rows of a row tile, half the columns each
 constexpr int kSumWarps = 8 * kHalves;
-constexpr int kThr = 32 * (kSumWarps + 3);
 constexpr int kWarpProducer = kSumWarps;
 constexpr int kWarpIssuer = kSumWarps + 1;
 constexpr int kWarpLse = kSumWarps + 2;
+constexpr int kThr = 32 * (kSumWarps + 3);
+constexpr int kMinTs = 4;  // query tiles from which a key tile is copied to tensor memory
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -73,7 +80,10 @@ struct Cfg {
   static constexpr int kOffQ = kKSlots * kKBytes;
   static constexpr int kOffLse = kOffQ + kQSlots * kQBytes;
   static constexpr int kOffBar = kOffLse + 2 * kQN * 4;
-  static constexpr int kNumBars = 2 * kKSlots + 2 * kQSlots + 4 + 4 + 2 + 2 + 1;
+  static constexpr int kSBufs = D == 256 ? 4 : 3;
+  static constexpr uint32_t kColA = kSBufs * kQN;
+  static_assert(kColA + D <= 512, "tensor memory");
+  static constexpr int kNumBars = 2 * kKSlots + 2 * kQSlots + 2 * kSBufs + 2 + 2 + 1 + 1;
   static constexpr int kSmem = kOffBar + (kNumBars + 1) * 8 + 1024;
   static_assert(kSmem <= 227 * 1024 - 512, "shared memory (512 bytes of it static)");
 };
@@ -226,51 +236,29 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return r;
 }
 
-// Adds a thread's weights over 32 columns.  kMasked: only columns [lo, hi) count.
-template <bool kMasked>
-__device__ __forceinline__ void add_columns(const uint32_t* r, const float* nl, int c0,
-                                            float scale2, int lo, int hi, float2* acc) {
+// Adds a thread's weights over kCols columns.  kMasked: only columns [lo, hi) count.
+template <int kCols, bool kMasked>
+__device__ __forceinline__ void add_columns(const uint32_t* x, const float* nl, float scale2,
+                                            int lo, int hi, float2* acc) {
   const float2 sc = make_float2(scale2, scale2);
 #pragma unroll
-  for (int j = 0; j < 32; j += 4) {
-    const float4 l = *reinterpret_cast<const float4*>(nl + c0 + j);
-    float2 x = fma2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), sc,
+  for (int c = 0; c < kCols; c += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(nl + c);
+    float2 u = fma2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc,
                     make_float2(l.x, l.y));
-    float2 y = fma2(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), sc,
+    float2 v = fma2(make_float2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sc,
                     make_float2(l.z, l.w));
-    x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-    y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+    u = make_float2(ex2_approx(u.x), ex2_approx(u.y));
+    v = make_float2(ex2_approx(v.x), ex2_approx(v.y));
     if (kMasked) {
-      const int c = c0 + j;
-      x.x = c >= lo && c < hi ? x.x : 0.f;
-      x.y = c + 1 >= lo && c + 1 < hi ? x.y : 0.f;
-      y.x = c + 2 >= lo && c + 2 < hi ? y.x : 0.f;
-      y.y = c + 3 >= lo && c + 3 < hi ? y.y : 0.f;
+      u.x = c >= lo && c < hi ? u.x : 0.f;
+      u.y = c + 1 >= lo && c + 1 < hi ? u.y : 0.f;
+      v.x = c + 2 >= lo && c + 2 < hi ? v.x : 0.f;
+      v.y = c + 3 >= lo && c + 3 < hi ? v.y : 0.f;
     }
-    acc[0] = add2(acc[0], x);
-    acc[1] = add2(acc[1], y);
+    acc[0] = add2(acc[0], u);
+    acc[1] = add2(acc[1], v);
   }
-}
-
-// All columns of a tile, the next 32 on their way from tensor memory meanwhile; `free` is
-// called once the tile has been read.
-template <int kQN, bool kMasked, typename Free>
-__device__ __forceinline__ float add_tile(uint32_t tS, const float* nl, float scale2, int lo,
-                                          int hi, Free free) {
-  float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  uint32_t x[2][32];
-  tmem_ld_x32(tS, x[0]);
-#pragma unroll
-  for (int c = 0; c < kQN / 32; ++c) {
-    tmem_ld_wait_x32(x[c & 1]);
-    if (c + 1 < kQN / 32)
-      tmem_ld_x32(tS + 32 * (c + 1), x[(c + 1) & 1]);
-    else
-      free();
-    add_columns<kMasked>(x[c & 1], nl, 32 * c, scale2, lo, hi, acc);
-  }
-  const float2 s = add2(acc[0], acc[1]);
-  return s.x + s.y;
 }
 
 template <int D>
@@ -288,11 +276,12 @@ __global__ void __launch_bounds__(kThr, 1)
   uint64_t* k_empty = k_full + C::kKSlots;
   uint64_t* q_full = k_empty + C::kKSlots;
   uint64_t* q_empty = q_full + C::kQSlots;
-  uint64_t* s_full = q_empty + C::kQSlots;  // [row tile][buffer]
-  uint64_t* s_empty = s_full + 4;
-  uint64_t* l_full = s_empty + 4;
+  uint64_t* s_full = q_empty + C::kQSlots;
+  uint64_t* s_empty = s_full + C::kSBufs;
+  uint64_t* l_full = s_empty + C::kSBufs;
   uint64_t* l_empty = l_full + 2;
-  uint64_t* drain = l_empty + 2;
+  uint64_t* a_full = l_empty + 2;  // K of both row tiles is in tensor memory
+  uint64_t* drain = a_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = &abort_s;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -308,7 +297,7 @@ __global__ void __launch_bounds__(kThr, 1)
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < C::kSBufs; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], kSumWarps / 2);
     }
@@ -316,6 +305,7 @@ __global__ void __launch_bounds__(kThr, 1)
       mbar_init(&l_full[i], 1);
       mbar_init(&l_empty[i], kSumWarps);
     }
+    mbar_init(a_full, kSumWarps);
     mbar_init(drain, 1);
     fence_mbar_init();
     abort_s = 0;
@@ -473,59 +463,85 @@ __global__ void __launch_bounds__(kThr, 1)
       // ============================================================ MMA issuer
       constexpr uint32_t idesc = idesc_bf16_f32(kRows, C::kQN, false);
       int kn = 0, qn = 0;
-      int cnt[2] = {0, 0};  // products of each row tile
-      int pb = -1, ph = -1, pu = -1;
+      int buf = 0, phase = 0, n_ts = 0;  // next S buffer; key tiles copied so far
+      int pb = -1, ph = -1, pu = -1;     // the query tile before
+      uint64_t dq = 0;
       bool ok = true;
+      // The next S buffer is free: its products before have been read (on its first use: the
+      // parity of the phase before the barrier's first).
+      auto wait_buffer = [&]() -> bool {
+        return mbar_wait_warp(&s_empty[buf], phase ^ 1, abort_flag, kWaitLimitNs);
+      };
+      // Unit i's query tile is there.
+      auto wait_queries = [&](int i) -> bool {
+        const int u = w.first * a.HC + w.u + i;
+        if (w.b == pb && w.h == ph && u == pu) return true;
+        pb = w.b, ph = w.h, pu = u;
+        const int qs = qn % C::kQSlots;
+        if (!mbar_wait_warp(&q_full[qs], (qn / C::kQSlots) & 1, abort_flag, kWaitLimitNs))
+          return false;
+        ++qn;
+        return true;
+      };
       do {
         const int ks = kn % C::kKSlots;
-        if (!mbar_wait_warp(&k_full[ks], (kn / C::kKSlots) & 1, abort_flag, kWaitLimitNs)) {
+        const int units = walk_units(w);
+        const bool ts = units >= kMinTs;
+        const int before = qn;
+        if ((ts ? !mbar_wait_warp(a_full, n_ts & 1, abort_flag, kWaitLimitNs)
+                : !mbar_wait_warp(&k_full[ks], (kn / C::kKSlots) & 1, abort_flag,
+                                  kWaitLimitNs)) ||
+            !wait_queries(0) || !wait_buffer()) {
           ok = false;
           break;
         }
-        const int units = walk_units(w);
-        for (int i = 0; ok && i < units; ++i) {
-          const int u = w.first * a.HC + w.u + i;
-          if (!(w.b == pb && w.h == ph && u == pu)) {
-            // the tile before this one is done with once its products are
-            if (pu >= 0) mma_commit_w(&q_empty[(qn - 1) % C::kQSlots]);
-            pb = w.b, ph = w.h, pu = u;
-            if (!mbar_wait_warp(&q_full[qn % C::kQSlots], (qn / C::kQSlots) & 1, abort_flag,
-                                kWaitLimitNs)) {
-              ok = false;
-              break;
-            }
-            ++qn;
-          }
-          tc_fence_after_sync();
-          const int qs = (qn - 1) % C::kQSlots;
-          const uint64_t dq = sdesc_sw128(smem_addr(smem + C::kOffQ + qs * C::kQBytes), 16, 1024);
-          // Keys past the last one: whatever the slot holds, in rows that nothing reads.
-          for (int t = 0; t < 2; ++t) {
-            const int buf = cnt[t] & 1;
-            if (cnt[t] >= 2 &&
-                !mbar_wait_warp(&s_empty[t * 2 + buf], (cnt[t] / 2 - 1) & 1, abort_flag,
-                                kWaitLimitNs)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-            const uint64_t dk = sdesc_sw128(
-                smem_addr(smem + ks * C::kKBytes + t * C::kKRow), 16, 1024);
-            const uint32_t tS = tmem + (t * 2 + buf) * C::kQN;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t ko = static_cast<uint64_t>(((kk / 4) * C::kKAtom + (kk % 4) * 32) >> 4);
-              const uint64_t qo = static_cast<uint64_t>(((kk / 4) * C::kQAtom + (kk % 4) * 32) >> 4);
-              mma_bf16_ss_w(tS, dk + ko, dq + qo, idesc, kk > 0 ? 1u : 0u);
-            }
-            mma_commit_w(&s_full[t * 2 + buf]);
-            ++cnt[t];
-          }
+        // the tile of the key tile before is done with once its products are
+        if (before > 0 && qn > before) mma_commit_w(&q_empty[(before - 1) % C::kQSlots]);
+        if (ts) {
+          ++n_ts;
+          if (lane == 0) mbar_arrive(&k_empty[ks]);
+          __syncwarp();
         }
-        mma_commit_w(&k_empty[ks]);
+        for (int i = 0; ok && i < units; ++i) {
+          const int now = qn;
+          dq = sdesc_sw128(smem_addr(smem + C::kOffQ + ((now - 1) % C::kQSlots) * C::kQBytes), 16,
+                           1024);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            tc_fence_after_sync();
+            const uint32_t tS = tmem + buf * C::kQN, tA = tmem + C::kColA + t * (D / 2);
+            uint64_t* done = &s_full[buf];
+            const uint64_t dk =
+                sdesc_sw128(smem_addr(smem + ks * C::kKBytes + t * C::kKRow), 16, 1024);
+            // Keys past the last one: whatever the slot holds, in rows that nothing reads.
+            auto issue = [&](int at0, int at1) {
+#pragma unroll
+              for (int at = at0; at < at1; ++at) {
+                if (ts)
+                  mma_ts_atom_w(tS, tA + 32 * at, dq + at * (C::kQAtom >> 4), idesc, at > 0);
+                else
+                  mma_ss_atom_w(tS, dk + at * (C::kKAtom >> 4), dq + at * (C::kQAtom >> 4), idesc,
+                                at > 0);
+              }
+            };
+            issue(0, (C::kAtoms + 1) / 2);
+            if (++buf == C::kSBufs) buf = 0, phase ^= 1;
+            if (t == 0 || i + 1 < units) {
+              if ((t == 1 && !wait_queries(i + 1)) || !wait_buffer()) {
+                ok = false;
+                break;
+              }
+            }
+            issue((C::kAtoms + 1) / 2, C::kAtoms);
+            mma_commit_w(done);
+          }
+          if (ok && qn > now) mma_commit_w(&q_empty[(now - 1) % C::kQSlots]);
+        }
+        if (!ok) break;
+        if (!ts) mma_commit_w(&k_empty[ks]);
         ++kn;
         w.left -= units;
-      } while (ok && walk_next(a, w));
+      } while (walk_next(a, w));
       if (!ok && lane == 0) {
         atomicOr(a.status, kStatusTimeout);
         *abort_flag = 1;
@@ -596,56 +612,96 @@ __global__ void __launch_bounds__(kThr, 1)
       const int t = (warp / 4) % 2, half = warp / 8, c0 = half * kCols;
       const int r = tid % kRows;  // the row of this thread
       const uint32_t taddr = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-      int cnt = 0;
+      const float* nl = reinterpret_cast<const float*>(smem + C::kOffLse) + c0;
+      int kn = 0, lbuf = 0, lphase = 0;  // LSE buffer of the next unit
+      int buf = t, phase = 0;            // S buffer of this row tile's next product
       bool ok = true;
       do {
-        const int ka = w.kt * kKeys + t * kRows;
+        const int ka = w.kt * kKeys + t * kRows, key = ka + r;
         const int units = walk_units(w);
-        float sum = 0.f;
+        if (units >= kMinTs) {
+          // ---- half of this row of K to tensor memory.  The key tile's products before have
+          // been read by this warp, so nothing reads the old K any more.
+          const int ks = kn % C::kKSlots;
+          if (!mbar_wait_warp(&k_full[ks], (kn / C::kKSlots) & 1, abort_flag, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          constexpr int kChunks = D / 16;  // 16-byte chunks of half a row
+          const uint8_t* src = smem + ks * C::kKBytes + t * C::kKRow + r * 128;
+          const uint32_t dst = taddr + C::kColA + t * (D / 2) + half * (D / 4);
+#pragma unroll
+          for (int c = 0; c < kChunks; c += 4) {
+            uint32_t y[16];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int ch = half * kChunks + c + e;
+              const uint4 v = *reinterpret_cast<const uint4*>(
+                  src + (ch / 8) * C::kKAtom + (((ch % 8) ^ (r & 7)) << 4));
+              y[4 * e] = v.x, y[4 * e + 1] = v.y, y[4 * e + 2] = v.z, y[4 * e + 3] = v.w;
+            }
+            tmem_st_x16(dst + 4 * c, y);
+          }
+          tmem_st_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(a_full);
+        }
+        ++kn;
+        // Tokens that this row sees, and first tokens of the tiles that all rows see whole.
+        int see0 = 0, see1 = w.s.Lq, all0 = 0, all1 = w.s.Lq - a.TQ;
+        if (a.causal) {
+          see0 = key - w.s.off;
+          all0 = ka + kRows - 1 - w.s.off;
+        }
+        if (a.window > 0 && key >= a.n_sink)
+          see1 = static_cast<int>(
+              min(static_cast<long long>(see1), static_cast<long long>(key) + a.window - w.s.off));
+        if (a.window > 0 && ka + kRows > a.n_sink)
+          all1 = static_cast<int>(min(static_cast<long long>(all1),
+                                      static_cast<long long>(ka) + a.window - w.s.off - a.TQ));
+        const int u0 = w.first * a.HC + w.u;
+        int i0 = tile_token(a, u0);
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         for (int i = 0; i < units; ++i) {
-          const int buf = cnt & 1;
-          const uint32_t parity = (cnt / 2) & 1;
-          if (!mbar_wait_warp(&l_full[buf], parity, abort_flag, kWaitLimitNs) ||
-              !mbar_wait_warp(&s_full[t * 2 + buf], parity, abort_flag, kWaitLimitNs)) {
+          if (!mbar_wait_warp(&s_full[buf], phase, abort_flag, kWaitLimitNs)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const float* nl = reinterpret_cast<const float*>(smem + C::kOffLse) + buf * C::kQN + c0;
-          const int i0 = tile_token(a, w.first * a.HC + w.u + i);  // the tile's first token
-          const uint32_t tS = taddr + (t * 2 + buf) * C::kQN + c0;
-          // Does every row see every query of the tile?
-          const bool interior =
-              i0 + a.TQ <= w.s.Lq && (!a.causal || ka + kRows - 1 <= i0 + w.s.off) &&
-              (a.window <= 0 || ka + kRows <= a.n_sink ||
-               static_cast<long long>(ka) + a.window > i0 + a.TQ - 1 + w.s.off);
-          auto free = [&] {
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[t * 2 + buf]);
-          };
-          if (interior) {
-            sum += add_tile<kCols, false>(tS, nl, a.scale2, 0, 0, free);
-          } else {
-            // columns [lo, hi): the tokens of the tile that see key ka + r
-            const int key = ka + r;
-            long long lo = 0, hi = min(a.TQ, w.s.Lq - i0);
-            if (a.causal) lo = max(0, key - w.s.off - i0);
-            if (a.window > 0 && key >= a.n_sink)
-              hi = min(hi, static_cast<long long>(key) + a.window - w.s.off - i0);
-            sum += add_tile<kCols, true>(
-                tS, nl, a.scale2,
-                static_cast<int>(min(lo, static_cast<long long>(a.TQ))) * a.GP - c0,
-                static_cast<int>(max(hi, 0LL)) * a.GP - c0, free);
+          uint32_t x[kCols];
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) tmem_ld_x32(taddr + buf * C::kQN + c0 + c, x + c);
+          // while they come: the LSEs, and which columns count
+          if (!mbar_wait_warp(&l_full[lbuf], lphase, abort_flag, kWaitLimitNs)) {
+            ok = false;
+            break;
           }
+          const float* l = nl + lbuf * C::kQN;
+          const bool interior = i0 >= all0 && i0 <= all1;
+          const int lo = min(max(see0 - i0, 0), a.TQ) * a.GP - c0;
+          const int hi = min(max(see1 - i0, 0), a.TQ) * a.GP - c0;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) tmem_ld_wait_x32(x + c);
+          tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&l_empty[buf]);
-          ++cnt;
+          if (lane == 0) mbar_arrive(&s_empty[buf]);
+          if (interior)
+            add_columns<kCols, false>(x, l, a.scale2, 0, 0, acc);
+          else if (__any_sync(0xffffffffu, lo < min(hi, kCols) && hi > 0))
+            add_columns<kCols, true>(x, l, a.scale2, lo, hi, acc);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&l_empty[lbuf]);
+          buf += 2;
+          if (buf >= C::kSBufs) buf -= C::kSBufs, phase ^= 1;
+          if (++lbuf == 2) lbuf = 0, lphase ^= 1;
+          i0 = a.HC == 1 ? i0 + a.TQ : tile_token(a, u0 + i + 1);
         }
         if (!ok) break;
         const size_t slot =
             (static_cast<size_t>(w.b) * a.Hkv + w.h) * a.max_kt + w.kt + blockIdx.x;
-        a.ws_part[(slot * kHalves + half) * kKeys + t * kRows + r] = sum;
+        const float2 sum = add2(acc[0], acc[1]);
+        a.ws_part[(slot * kHalves + half) * kKeys + t * kRows + r] = sum.x + sum.y;
         w.left -= units;
       } while (walk_next(a, w));
       if (!ok && lane == 0) {

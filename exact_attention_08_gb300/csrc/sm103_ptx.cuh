@@ -444,6 +444,43 @@ __device__ __forceinline__ void mma_ss_k64_w(uint32_t d, uint64_t a, uint64_t b,
       : "memory");
 }
 
+// One atom (64 columns, 4 K-steps) of a product over several: acc == 0 makes the first
+// K-step overwrite D.  Both operands K-major with the 128-byte swizzle.
+__device__ __forceinline__ void mma_ss_atom_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                              uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b32 al, ah, bl, bh, x, y;\n\t.reg .b64 da, db;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 {al, ah}, %1;\n\tmov.b64 {bl, bh}, %2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.u32 x, al, 2;\n\tadd.u32 y, bl, 2;\n\tmov.b64 da, {x, ah};\n\tmov.b64 db, {y, bh};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, 1;\n\t"
+      "add.u32 x, al, 4;\n\tadd.u32 y, bl, 4;\n\tmov.b64 da, {x, ah};\n\tmov.b64 db, {y, bh};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, 1;\n\t"
+      "add.u32 x, al, 6;\n\tadd.u32 y, bl, 6;\n\tmov.b64 da, {x, ah};\n\tmov.b64 db, {y, bh};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, 1;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// The same with A from tensor memory (bf16 pairs, 8 columns per K-step).
+__device__ __forceinline__ void mma_ts_atom_w(uint32_t d, uint32_t a_tmem, uint64_t b,
+                                              uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b32 bl, bh, x, y;\n\t.reg .b64 db;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 {bl, bh}, %2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.u32 x, %1, 8;\n\tadd.u32 y, bl, 2;\n\tmov.b64 db, {y, bh};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, 1;\n\t"
+      "add.u32 x, %1, 16;\n\tadd.u32 y, bl, 4;\n\tmov.b64 db, {y, bh};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, 1;\n\t"
+      "add.u32 x, %1, 24;\n\tadd.u32 y, bl, 6;\n\tmov.b64 db, {y, bh};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, 1;\n\t}" ::"r"(d),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
 // D += A B over 64 keys (4 K-steps of 16): A from tensor memory (bf16 pairs,
 // 8 columns per K-step), B MN-major in shared memory (2048 bytes, 128 x 16 B,
 // per K-step).  acc == 0 makes the first K-step overwrite D.

@@ -124,6 +124,27 @@ int make_map(CUtensorMap* m, const void* ptr, uint64_t d, uint64_t n1, uint64_t 
   return ATTN_OK;
 }
 
+// Page pool [pages, 16, Hkv, d] as (64 columns, 16 tokens, d / 64 atoms, Hkv, pages): a box is
+// a whole page of one head, atom by atom, each 16 rows of 128 bytes with the 128-byte swizzle.
+int make_page_map(CUtensorMap* m, const void* ptr, int d, int Hkv, int pages, const char* what) {
+  auto fn = encode_fn();
+  if (!fn) return set_error(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2, token = row * Hkv;
+  cuuint64_t dims[5] = {64, 16, static_cast<cuuint64_t>(d) / 64, static_cast<cuuint64_t>(Hkv),
+                        static_cast<cuuint64_t>(pages)};
+  cuuint64_t strides[4] = {token, 128, row, token * 16};
+  cuuint32_t box[5] = {64, 16, static_cast<cuuint32_t>(d / 64), 1, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims,
+                        strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return set_error(ATTN_ERR_INVALID_ARG, "tensor map for %s rejected (CUresult %d)", what,
+                     static_cast<int>(r));
+  return ATTN_OK;
+}
+
 }  // namespace
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -131,6 +152,11 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 int page_pool_map(CUtensorMap* m, const void* pool, int d, int Hkv, int num_pages,
                   const char* what) {
   return make_map(m, pool, d, Hkv, 16, num_pages, 16, what);
+}
+
+int whole_page_map(CUtensorMap* m, const void* pool, int d, int Hkv, int num_pages,
+                   const char* what) {
+  return make_page_map(m, pool, d, Hkv, num_pages, what);
 }
 
 int packed_rows_map(CUtensorMap* m, const void* x, int d, int H, int rows, int box_heads,

@@ -18,6 +18,11 @@
 // there as the A operand; the copy costs about a unit's time, which shorter runs
 // would not win back.
 //
+// Rows.  A page (16 tokens of one head) arrives in one copy: [d / 64 atoms][16 rows][128
+// bytes].  Its rows 0-7 belong to row tile 0 and 8-15 to row tile 1, so that the 16
+// eight-row groups of a row tile are evenly spaced, as the product's operand needs:
+// row r of row tile t is key (r / 8) * 16 + t * 8 + r % 8 of the key tile.
+//
 // Tile.  256 keys (two row tiles) against each query tile: one row tile alone
 // would read 64 bytes of Q a cycle and SM from L2, more than it delivers.  Eight
 // warps for each row tile, and a ring of S buffers, so that the next products run under the
@@ -32,7 +37,7 @@
 //
 // Split.  The work is cut into units, a query tile against a key tile, in the order
 // (sequence, key head, key tile, query tile), and each of the persistent CTAs (one an
-// SM) takes an equal run of units: causal triangles, windows and ragged lengths
+// SM) takes an equal run of them: causal triangles, windows and ragged lengths
 // balance by themselves, and few keys with many queries still fill the GPU.  A plan
 // kernel counts the units of every key tile.  A key tile that several CTAs share has
 // one partial sum from each; partial sums go to workspace slot (key tile + CTA), both
@@ -63,6 +68,9 @@ constexpr int kWarpProducer = kSumWarps;
 constexpr int kWarpIssuer = kSumWarps + 1;
 constexpr int kWarpLse = kSumWarps + 2;
 constexpr int kThr = 32 * (kSumWarps + 3);
+// What starting a key tile costs, in units (8,192 tokens, causal, 32 heads over 8: 258 us
+// at 0, 242 at 2, 236 at 4, 237 at 6; short blocks of 300 queries 39.9, 36.9, 38.3, 40.3).
+constexpr int kItemCost = 3;
 constexpr int kMinTs = 4;  // query tiles from which a key tile is copied to tensor memory
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -72,9 +80,9 @@ struct Cfg {
   static constexpr int kQN = D == 256 ? 64 : 128;  // queries (token, head) of a query tile
   static constexpr int kKSlots = D == 256 ? 1 : 2;
   static constexpr int kQSlots = D == 64 ? 4 : 3;
-  static constexpr int kKAtom = kRows * 128;       // one row tile x 64 columns
-  static constexpr int kKRow = kAtoms * kKAtom;    // one row tile
-  static constexpr int kKBytes = 2 * kKRow;        // a K slot
+  static constexpr int kPageAtom = kPage * 128;    // a page's 64 columns
+  static constexpr int kPageBytes = kAtoms * kPageAtom;
+  static constexpr int kKBytes = kPagesPerTile * kPageBytes;  // a K slot
   static constexpr int kQAtom = kQN * 128;
   static constexpr int kQBytes = kAtoms * kQAtom;  // a Q slot
   static constexpr int kOffQ = kKSlots * kKBytes;
@@ -87,6 +95,9 @@ struct Cfg {
   static constexpr int kSmem = kOffBar + (kNumBars + 1) * 8 + 1024;
   static_assert(kSmem <= 227 * 1024 - 512, "shared memory (512 bytes of it static)");
 };
+
+// Key of row r of row tile t, in its key tile.
+__device__ __forceinline__ int row_key(int t, int r) { return (r / 8) * kPage + t * 8 + r % 8; }
 
 // One sequence: its queries and keys.
 struct Seq {
@@ -142,7 +153,9 @@ __device__ __forceinline__ long long* ws_base(const MassArgs& a) {  // [B + 1]
 }
 
 // ---------------------------------------------------------------- plan
-// cum[b][kt]: units of sequence b's key tiles before kt, one key head; cum[b][max_kt]: all.
+// Work is measured in positions: a key tile with n units has kItemCost + n of them, the units
+// last (so that a CTA with many short key tiles gets fewer units).  cum[b][kt]: positions
+// of sequence b's key tiles before kt, one key head; cum[b][max_kt]: all.
 constexpr int kPlanThreads = 256;
 __global__ void __launch_bounds__(kPlanThreads) attn_mass_plan_kernel(const MassArgs a) {
   __shared__ long long s_part[kPlanThreads / 32];
@@ -157,8 +170,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_mass_plan_kernel(const Mass
   for (int k0 = 0; k0 < n; k0 += kPlanThreads) {
     const int kt = k0 + tid;
     int first;
-    const long long v =
-        kt < n ? static_cast<long long>(query_tiles(a, s, kt, &first)) * a.HC : 0;
+    long long v = kt < n ? static_cast<long long>(query_tiles(a, s, kt, &first)) * a.HC : 0;
+    if (v > 0) v += kItemCost;
     long long x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -183,7 +196,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_mass_plan_kernel(const Mass
 // A CTA's run of units: the key tiles in order, each with its query tiles.
 struct Walk {
   int b, h, kt, first, n, u;  // key tile; its first query tile, units, and the next unit
-  long long left;             // units left in the run
+                              // (below 0: positions before its first)
+  long long left;             // positions left in the run
   int tiles;                  // key tiles of the sequence
   Seq s;
 };
@@ -196,7 +210,7 @@ __device__ __forceinline__ bool walk_item(const MassArgs& a, Walk& w) {
 
 // The next key tile with units.
 __device__ __forceinline__ bool walk_next(const MassArgs& a, Walk& w) {
-  w.u = 0;
+  w.u = -kItemCost;
   while (w.left > 0) {
     if (++w.kt >= w.tiles) {
       w.kt = 0;
@@ -213,9 +227,14 @@ __device__ __forceinline__ bool walk_next(const MassArgs& a, Walk& w) {
   return false;
 }
 
-// Units of the current key tile that belong to this run.
-__device__ __forceinline__ int walk_units(const Walk& w) {
-  return static_cast<int>(min(static_cast<long long>(w.n - w.u), w.left));
+// Takes the positions before the current key tile's first unit; then, how many of its units
+// belong to this run (none, if the run ends before them).
+__device__ __forceinline__ int walk_units(Walk& w) {
+  if (w.u < 0) {
+    w.left += w.u;
+    w.u = 0;
+  }
+  return static_cast<int>(max(0LL, min(static_cast<long long>(w.n - w.u), w.left)));
 }
 
 // Two fp32 operations an instruction.
@@ -236,8 +255,10 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return r;
 }
 
-// Adds a thread's weights over kCols columns.  kMasked: only columns [lo, hi) count.
-template <int kCols, bool kMasked>
+// Adds a thread's weights over kCols columns: all of them, those in [lo, hi) where both are
+// multiples of four (the group's heads are), or those in any [lo, hi).
+enum MaskMode { kAll, kFours, kAny };
+template <int kCols, MaskMode kMask>
 __device__ __forceinline__ void add_columns(const uint32_t* x, const float* nl, float scale2,
                                             int lo, int hi, float2* acc) {
   const float2 sc = make_float2(scale2, scale2);
@@ -250,11 +271,15 @@ __device__ __forceinline__ void add_columns(const uint32_t* x, const float* nl, 
                     make_float2(l.z, l.w));
     u = make_float2(ex2_approx(u.x), ex2_approx(u.y));
     v = make_float2(ex2_approx(v.x), ex2_approx(v.y));
-    if (kMasked) {
+    if (kMask == kAny) {
       u.x = c >= lo && c < hi ? u.x : 0.f;
       u.y = c + 1 >= lo && c + 1 < hi ? u.y : 0.f;
       v.x = c + 2 >= lo && c + 2 < hi ? v.x : 0.f;
       v.y = c + 3 >= lo && c + 3 < hi ? v.y : 0.f;
+    }
+    if (kMask == kFours) {
+      const bool in = c >= lo && c < hi;
+      u.x = in ? u.x : 0.f, u.y = in ? u.y : 0.f, v.x = in ? v.x : 0.f, v.y = in ? v.y : 0.f;
     }
     acc[0] = add2(acc[0], u);
     acc[1] = add2(acc[1], v);
@@ -323,7 +348,7 @@ __global__ void __launch_bounds__(kThr, 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // ---- this CTA's run: units [u0, u1) of the T in all
+  // ---- this CTA's run: positions [u0, u1) of the T in all
   {
     const int per = (a.B + kThr - 1) / kThr;
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
@@ -342,7 +367,7 @@ __global__ void __launch_bounds__(kThr, 1)
       if (w < warp) before += s_part[w];
       T += s_part[w];
     }
-    // with fewer units than CTAs the last CTAs have none, the others one each
+    // with fewer positions than CTAs the last CTAs have none, the others one each
     const long long n = min(T, static_cast<long long>(gridDim.x)), c = blockIdx.x;
     const long long u0 = c < n ? T * c / n : 0, u1 = c < n ? T * (c + 1) / n : 0;
     for (int b = b0; b < b1; ++b) {
@@ -350,7 +375,7 @@ __global__ void __launch_bounds__(kThr, 1)
       if (blockIdx.x == 0) ws_base(a)[b] = before;
       if (u0 < u1 && u0 >= before && u0 < before + here) {
         const long long in = u0 - before;
-        const long long v = in % per_head;  // unit within the head
+        const long long v = in % per_head;  // position within the head
         const long long* cum = ws_cum(a, b);
         Seq s;
         load_seq(a, b, s);
@@ -365,7 +390,7 @@ __global__ void __launch_bounds__(kThr, 1)
         s_start[0] = b;
         s_start[1] = static_cast<int>(in / per_head);
         s_start[2] = lo;
-        s_run[0] = v - cum[lo];
+        s_run[0] = v - cum[lo] - kItemCost;
       }
       before += here;
     }
@@ -388,25 +413,33 @@ __global__ void __launch_bounds__(kThr, 1)
     load_seq(a, w.b, w.s);
     w.tiles = key_tiles(w.s);
     walk_item(a, w);
-    w.u = static_cast<int>(s_run[0]);
+    w.u = static_cast<int>(s_run[0]);  // may stand before the first unit
 
     if (warp == kWarpProducer) {
       // ============================================================ TMA producer
       int kn = 0, qn = 0;  // K and Q slots filled
       int pb = -1, ph = -1, pu = -1;
-      bool ok = true;
-      do {
-        const int ka = w.kt * kKeys;
-        const int two = w.s.L - ka > kRows ? 2 : 1;
-        const int np = (w.s.L + kPage - 1) / kPage;
-        int page = 0;
-        if (lane < kPagesPerTile) {
-          page = a.page_table[static_cast<size_t>(w.b) * a.max_pages +
-                              min(w.kt * kPagesPerTile + lane, np - 1)];
-          if (page < 0 || page >= a.num_pages) {
-            atomicOr(a.status, kStatusBadInput);
-            page = 0;
-          }
+      bool ok = true, more = true;
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmQ);
+      // Physical page of this lane, read a key tile ahead of its loads.
+      auto lookup = [&]() -> int {
+        if (lane >= kPagesPerTile) return 0;
+        const int page = w.kt * kPagesPerTile + lane;
+        if (page * kPage >= w.s.L) return 0;
+        return a.page_table[static_cast<size_t>(w.b) * a.max_pages + page];
+      };
+      int page = lookup();
+      while (more) {
+        const int units = walk_units(w);
+        if (units == 0) break;
+        const int pages = min(kPagesPerTile, (w.s.L - w.kt * kKeys + kPage - 1) / kPage);
+        const int b = w.b, h = w.h, u0 = w.first * a.HC + w.u, q_base = w.s.q_base;
+        w.left -= units;
+        more = walk_next(a, w);
+        if (page < 0 || page >= a.num_pages) {
+          atomicOr(a.status, kStatusBadInput);
+          page = 0;
         }
         __syncwarp();
         const int ks = kn % C::kKSlots;
@@ -415,21 +448,16 @@ __global__ void __launch_bounds__(kThr, 1)
           ok = false;
           break;
         }
-        mbar_arrive_expect_tx_w(&k_full[ks], two * C::kKRow);
-        if (lane < two * (kRows / kPage)) {
-#pragma unroll
-          for (int at = 0; at < C::kAtoms; ++at)
-            tma_load_4d(smem + ks * C::kKBytes + (lane / 8) * C::kKRow + at * C::kKAtom +
-                            (lane % 8) * kPage * 128,
-                        &tmK, &k_full[ks], at * 64, w.h, 0, page);
-        }
+        mbar_arrive_expect_tx_w(&k_full[ks], pages * C::kPageBytes);
+        if (lane < pages)
+          tma_load_5d(smem + ks * C::kKBytes + lane * C::kPageBytes, &tmK, &k_full[ks], 0, 0, 0, h,
+                      page);
         __syncwarp();
         ++kn;
-        const int units = walk_units(w);
-        for (int i = 0; ok && i < units; ++i) {
-          const int u = w.first * a.HC + w.u + i;  // the tile's number in the sequence
-          if (w.b == pb && w.h == ph && u == pu) continue;
-          pb = w.b, ph = w.h, pu = u;
+        if (more) page = lookup();
+        for (int u = u0; u < u0 + units; ++u) {
+          if (b == pb && h == ph && u == pu) continue;
+          pb = b, ph = h, pu = u;
           const int qs = qn % C::kQSlots;
           if (qn >= C::kQSlots &&
               !mbar_wait_warp(&q_empty[qs], (qn / C::kQSlots - 1) & 1, abort_flag,
@@ -441,11 +469,11 @@ __global__ void __launch_bounds__(kThr, 1)
 #pragma unroll
           for (int at = 0; at < C::kAtoms; ++at)
             tma_load_4d_w(smem + C::kOffQ + qs * C::kQBytes + at * C::kQAtom, &tmQ, &q_full[qs],
-                          at * 64, w.h * a.G + tile_head(a, u), w.s.q_base + tile_token(a, u), 0);
+                          at * 64, h * a.G + tile_head(a, u), q_base + tile_token(a, u), 0);
           ++qn;
         }
-        w.left -= units;
-      } while (ok && walk_next(a, w));
+        if (!ok) break;
+      }
       if (!ok && lane == 0) {
         atomicOr(a.status, kStatusTimeout);
         *abort_flag = 1;
@@ -461,86 +489,82 @@ __global__ void __launch_bounds__(kThr, 1)
       }
     } else if (warp == kWarpIssuer) {
       // ============================================================ MMA issuer
+      // Slots and phases are counted along rather than worked out of running numbers, and the
+      // descriptors are sums of constants: one warp issues everything, and each instruction
+      // between two products costs it some eight cycles next to the summing warps.
       constexpr uint32_t idesc = idesc_bf16_f32(kRows, C::kQN, false);
-      int kn = 0, qn = 0;
-      int buf = 0, phase = 0, n_ts = 0;  // next S buffer; key tiles copied so far
-      int pb = -1, ph = -1, pu = -1;     // the query tile before
-      uint64_t dq = 0;
+      int ks = 0, kphase = 0, aphase = 0;
+      int qs = 0, qphase = 0, held = -1;  // next Q slot; the slot of the tile before
+      int buf = 0, sphase = 1;            // next S buffer (its first wait passes at once)
+      int pb = -1, ph = -1, pu = -1;      // the query tile before
+      const uint64_t dq0 = sdesc_sw128(smem_addr(smem + C::kOffQ), 16, 1024);
+      const uint64_t dk0 = sdesc_sw128(smem_addr(smem), 16, C::kPageBytes);
+      const uint32_t tA = tmem + C::kColA;
       bool ok = true;
-      // The next S buffer is free: its products before have been read (on its first use: the
-      // parity of the phase before the barrier's first).
-      auto wait_buffer = [&]() -> bool {
-        return mbar_wait_warp(&s_empty[buf], phase ^ 1, abort_flag, kWaitLimitNs);
-      };
-      // Unit i's query tile is there.
-      auto wait_queries = [&](int i) -> bool {
-        const int u = w.first * a.HC + w.u + i;
-        if (w.b == pb && w.h == ph && u == pu) return true;
-        pb = w.b, ph = w.h, pu = u;
-        const int qs = qn % C::kQSlots;
-        if (!mbar_wait_warp(&q_full[qs], (qn / C::kQSlots) & 1, abort_flag, kWaitLimitNs))
-          return false;
-        ++qn;
-        return true;
-      };
       do {
-        const int ks = kn % C::kKSlots;
-        const int units = walk_units(w);
+        int units = walk_units(w);
+        if (units == 0) break;
         const bool ts = units >= kMinTs;
-        const int before = qn;
-        if ((ts ? !mbar_wait_warp(a_full, n_ts & 1, abort_flag, kWaitLimitNs)
-                : !mbar_wait_warp(&k_full[ks], (kn / C::kKSlots) & 1, abort_flag,
-                                  kWaitLimitNs)) ||
-            !wait_queries(0) || !wait_buffer()) {
+        int u = w.first * a.HC + w.u;
+        bool fresh = !(w.b == pb && w.h == ph && u == pu);  // another query tile
+        pb = w.b, ph = w.h, pu = u + units - 1;
+        w.left -= units;
+        if ((ts ? !mbar_wait_warp(a_full, aphase, abort_flag, kWaitLimitNs)
+                : !mbar_wait_warp(&k_full[ks], kphase, abort_flag, kWaitLimitNs)) ||
+            (fresh && !mbar_wait_warp(&q_full[qs], qphase, abort_flag, kWaitLimitNs)) ||
+            !mbar_wait_warp(&s_empty[buf], sphase, abort_flag, kWaitLimitNs)) {
           ok = false;
           break;
         }
-        // the tile of the key tile before is done with once its products are
-        if (before > 0 && qn > before) mma_commit_w(&q_empty[(before - 1) % C::kQSlots]);
+        uint64_t* const k_done = &k_empty[ks];
+        const uint64_t dk = dk0 + ks * (C::kKBytes >> 4);
+        if (++ks == C::kKSlots) ks = 0, kphase ^= 1;
         if (ts) {
-          ++n_ts;
-          if (lane == 0) mbar_arrive(&k_empty[ks]);
+          aphase ^= 1;
+          if (lane == 0) mbar_arrive(k_done);
           __syncwarp();
         }
-        for (int i = 0; ok && i < units; ++i) {
-          const int now = qn;
-          dq = sdesc_sw128(smem_addr(smem + C::kOffQ + ((now - 1) % C::kQSlots) * C::kQBytes), 16,
-                           1024);
+        while (units > 0) {
+          if (fresh) {
+            // the tile before is done with once its products are
+            if (held >= 0) mma_commit_w(&q_empty[held]);
+            held = qs;
+            if (++qs == C::kQSlots) qs = 0, qphase ^= 1;
+          }
+          const uint64_t dq = dq0 + held * (C::kQBytes >> 4);
+          --units;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             tc_fence_after_sync();
-            const uint32_t tS = tmem + buf * C::kQN, tA = tmem + C::kColA + t * (D / 2);
-            uint64_t* done = &s_full[buf];
-            const uint64_t dk =
-                sdesc_sw128(smem_addr(smem + ks * C::kKBytes + t * C::kKRow), 16, 1024);
+            const uint32_t tS = tmem + buf * C::kQN;
+            uint64_t* const s_done = &s_full[buf];
+            if (++buf == C::kSBufs) buf = 0, sphase ^= 1;
             // Keys past the last one: whatever the slot holds, in rows that nothing reads.
-            auto issue = [&](int at0, int at1) {
-#pragma unroll
-              for (int at = at0; at < at1; ++at) {
-                if (ts)
-                  mma_ts_atom_w(tS, tA + 32 * at, dq + at * (C::kQAtom >> 4), idesc, at > 0);
-                else
-                  mma_ss_atom_w(tS, dk + at * (C::kKAtom >> 4), dq + at * (C::kQAtom >> 4), idesc,
-                                at > 0);
-              }
+            auto issue = [&](int at) {
+              const uint64_t q = dq + at * (C::kQAtom >> 4);
+              if (ts)
+                mma_ts_atom_w(tS, tA + t * (D / 2) + 32 * at, q, idesc, at > 0);
+              else
+                mma_ss_atom_w(tS, dk + ((t * 1024 + at * C::kPageAtom) >> 4), q, idesc, at > 0);
             };
-            issue(0, (C::kAtoms + 1) / 2);
-            if (++buf == C::kSBufs) buf = 0, phase ^= 1;
-            if (t == 0 || i + 1 < units) {
-              if ((t == 1 && !wait_queries(i + 1)) || !wait_buffer()) {
+#pragma unroll
+            for (int at = 0; at < (C::kAtoms + 1) / 2; ++at) issue(at);
+            if (t == 0 || units > 0) {
+              if ((t == 1 && !mbar_wait_warp(&q_full[qs], qphase, abort_flag, kWaitLimitNs)) ||
+                  !mbar_wait_warp(&s_empty[buf], sphase, abort_flag, kWaitLimitNs)) {
                 ok = false;
                 break;
               }
             }
-            issue((C::kAtoms + 1) / 2, C::kAtoms);
-            mma_commit_w(done);
+#pragma unroll
+            for (int at = (C::kAtoms + 1) / 2; at < C::kAtoms; ++at) issue(at);
+            mma_commit_w(s_done);
           }
-          if (ok && qn > now) mma_commit_w(&q_empty[(now - 1) % C::kQSlots]);
+          if (!ok) break;
+          fresh = true;  // within a key tile every unit has another query tile
         }
         if (!ok) break;
-        if (!ts) mma_commit_w(&k_empty[ks]);
-        ++kn;
-        w.left -= units;
+        if (!ts) mma_commit_w(k_done);
       } while (walk_next(a, w));
       if (!ok && lane == 0) {
         atomicOr(a.status, kStatusTimeout);
@@ -577,8 +601,8 @@ __global__ void __launch_bounds__(kThr, 1)
                         ? lse[static_cast<size_t>(head[j]) * a.total_q + tok[j]]
                         : INFINITY;
       };
-      fetch();
-      bool ok = true, more = true;
+      bool ok = true, more = units > 0;
+      if (more) fetch();
       while (more) {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) v[j] = next[j] * -kLog2e;
@@ -587,6 +611,7 @@ __global__ void __launch_bounds__(kThr, 1)
           more = walk_next(a, w);
           if (more) {
             units = walk_units(w);
+            more = units > 0;
             i = 0;
           }
         }
@@ -615,10 +640,13 @@ __global__ void __launch_bounds__(kThr, 1)
       const float* nl = reinterpret_cast<const float*>(smem + C::kOffLse) + c0;
       int kn = 0, lbuf = 0, lphase = 0;  // LSE buffer of the next unit
       int buf = t, phase = 0;            // S buffer of this row tile's next product
+      const bool fours = a.GP % 4 == 0;
       bool ok = true;
       do {
-        const int ka = w.kt * kKeys + t * kRows, key = ka + r;
+        const int ka = w.kt * kKeys, kb = ka + kKeys - 1;  // of this row tile too, nearly
+        const int key = ka + row_key(t, r);
         const int units = walk_units(w);
+        if (units == 0) break;
         if (units >= kMinTs) {
           // ---- half of this row of K to tensor memory.  The key tile's products before have
           // been read by this warp, so nothing reads the old K any more.
@@ -628,7 +656,8 @@ __global__ void __launch_bounds__(kThr, 1)
             break;
           }
           constexpr int kChunks = D / 16;  // 16-byte chunks of half a row
-          const uint8_t* src = smem + ks * C::kKBytes + t * C::kKRow + r * 128;
+          const uint8_t* src = smem + ks * C::kKBytes + (r / 8) * C::kPageBytes + t * 1024 +
+                               (r % 8) * 128;
           const uint32_t dst = taddr + C::kColA + t * (D / 2) + half * (D / 4);
 #pragma unroll
           for (int c = 0; c < kChunks; c += 4) {
@@ -637,7 +666,7 @@ __global__ void __launch_bounds__(kThr, 1)
             for (int e = 0; e < 4; ++e) {
               const int ch = half * kChunks + c + e;
               const uint4 v = *reinterpret_cast<const uint4*>(
-                  src + (ch / 8) * C::kKAtom + (((ch % 8) ^ (r & 7)) << 4));
+                  src + (ch / 8) * C::kPageAtom + (((ch % 8) ^ (r & 7)) << 4));
               y[4 * e] = v.x, y[4 * e + 1] = v.y, y[4 * e + 2] = v.z, y[4 * e + 3] = v.w;
             }
             tmem_st_x16(dst + 4 * c, y);
@@ -652,12 +681,12 @@ __global__ void __launch_bounds__(kThr, 1)
         int see0 = 0, see1 = w.s.Lq, all0 = 0, all1 = w.s.Lq - a.TQ;
         if (a.causal) {
           see0 = key - w.s.off;
-          all0 = ka + kRows - 1 - w.s.off;
+          all0 = kb - w.s.off;
         }
         if (a.window > 0 && key >= a.n_sink)
           see1 = static_cast<int>(
               min(static_cast<long long>(see1), static_cast<long long>(key) + a.window - w.s.off));
-        if (a.window > 0 && ka + kRows > a.n_sink)
+        if (a.window > 0 && kb >= a.n_sink)
           all1 = static_cast<int>(min(static_cast<long long>(all1),
                                       static_cast<long long>(ka) + a.window - w.s.off - a.TQ));
         const int u0 = w.first * a.HC + w.u;
@@ -687,9 +716,11 @@ __global__ void __launch_bounds__(kThr, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_empty[buf]);
           if (interior)
-            add_columns<kCols, false>(x, l, a.scale2, 0, 0, acc);
-          else if (__any_sync(0xffffffffu, lo < min(hi, kCols) && hi > 0))
-            add_columns<kCols, true>(x, l, a.scale2, lo, hi, acc);
+            add_columns<kCols, kAll>(x, l, a.scale2, 0, 0, acc);
+          else if (fours)
+            add_columns<kCols, kFours>(x, l, a.scale2, lo, hi, acc);
+          else
+            add_columns<kCols, kAny>(x, l, a.scale2, lo, hi, acc);
           __syncwarp();
           if (lane == 0) mbar_arrive(&l_empty[lbuf]);
           buf += 2;
@@ -701,7 +732,7 @@ __global__ void __launch_bounds__(kThr, 1)
         const size_t slot =
             (static_cast<size_t>(w.b) * a.Hkv + w.h) * a.max_kt + w.kt + blockIdx.x;
         const float2 sum = add2(acc[0], acc[1]);
-        a.ws_part[(slot * kHalves + half) * kKeys + t * kRows + r] = sum.x + sum.y;
+        a.ws_part[(slot * kHalves + half) * kKeys + row_key(t, r)] = sum.x + sum.y;
         w.left -= units;
       } while (walk_next(a, w));
       if (!ok && lane == 0) {
@@ -724,13 +755,13 @@ constexpr int kAddTokens = 4 * kAddThreads;
 __global__ void __launch_bounds__(kAddThreads) attn_mass_add_kernel(const MassArgs a, int ctas) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int h = blockIdx.y, b = blockIdx.z;
+  const long long* cum = ws_cum(a, b);
+  const long long per_head = cum[a.max_kt], T = ws_base(a)[a.B], before = ws_base(a)[b];
   Seq s;
   if (!load_seq(a, b, s)) return;
   const int t0 = blockIdx.x * kAddTokens;
   if (t0 >= s.L) return;
-  const long long* cum = ws_cum(a, b);
-  const long long per_head = cum[a.max_kt], T = ws_base(a)[a.B];
-  const long long head0 = ws_base(a)[b] + per_head * h;
+  const long long head0 = before + per_head * h;
   int fresh = a.new_tokens ? a.new_tokens[b] : s.Lq;
   fresh = max(0, min(fresh, s.L));
   const int last = a.last_positions ? a.last_positions[b] : s.L - 1;
@@ -740,11 +771,12 @@ __global__ void __launch_bounds__(kAddThreads) attn_mass_add_kernel(const MassAr
     const int t = t0 + j * kAddThreads + threadIdx.x;
     if (t >= s.L) break;
     const int kt = t / kKeys;
-    const long long n = (kt + 1 < key_tiles(s) ? cum[kt + 1] : per_head) - cum[kt];
+    const long long n =
+        (kt + 1 < key_tiles(s) ? cum[kt + 1] : per_head) - cum[kt] - kItemCost;
     float w = 0.f;
     if (n > 0) {
-      // of C CTAs with units, unit u belongs to CTA ((u + 1) C - 1) / T
-      const long long u = head0 + cum[kt], C = min(T, static_cast<long long>(ctas));
+      // of C CTAs with work, position u belongs to CTA ((u + 1) C - 1) / T
+      const long long u = head0 + cum[kt] + kItemCost, C = min(T, static_cast<long long>(ctas));
       const int c0 = static_cast<int>(((u + 1) * C - 1) / T);
       const int c1 = static_cast<int>(((u + n) * C - 1) / T);
       const size_t slot = (static_cast<size_t>(b) * a.Hkv + h) * a.max_kt + kt;

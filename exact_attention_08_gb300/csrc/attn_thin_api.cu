@@ -304,7 +304,7 @@ ATTN_API int attn_mass_paged(const void* q, const float* lse, const void* k_page
   a.TQ = tile / a.GP;
   a.HC = a.G / a.GP;
   a.tq_mul = ((1ull << 40) + a.TQ - 1) / a.TQ;
-  if ((rc = page_pool_map(&a.tmK, k_pages, d, Hkv, num_pages_total, "k_pages")) != ATTN_OK)
+  if ((rc = whole_page_map(&a.tmK, k_pages, d, Hkv, num_pages_total, "k_pages")) != ATTN_OK)
     return rc;
   // with no query at all the map is of nothing that is read
   if ((rc = packed_rows_map(&a.tmQ, total_q > 0 ? q : k_pages, d, total_q > 0 ? Hq : Hkv,

@@ -99,7 +99,8 @@ struct Cfg {
 // Key of row r of row tile t, in its key tile.
 __device__ __forceinline__ int row_key(int t, int r) { return (r / 8) * kPage + t * 8 + r % 8; }
 
-// One sequence: its queries and keys.
+// One sequence: its queries and keys.  Lengths are at most 2^29 and the window at most the
+// longest row, so that sums of three of them stay below 2^31.
 struct Seq {
   int Lq, L, off, q_base;
 };
@@ -138,9 +139,7 @@ __device__ __forceinline__ int query_tiles(const MassArgs& a, const Seq& s, int 
   const int ka = kt * kKeys, kb = min(ka + kKeys, s.L) - 1;
   int lo = 0, hi = s.Lq - 1;
   if (a.causal) lo = max(lo, ka - s.off);
-  if (a.window > 0 && ka >= a.n_sink)
-    hi = static_cast<int>(min(static_cast<long long>(hi),
-                              static_cast<long long>(kb) + a.window - 1 - s.off));
+  if (a.window > 0 && ka >= a.n_sink) hi = min(hi, kb + a.window - 1 - s.off);
   *first = in_tiles(a, lo);
   return hi < lo ? 0 : in_tiles(a, hi) - *first + 1;
 }
@@ -150,6 +149,10 @@ __device__ __forceinline__ long long* ws_cum(const MassArgs& a, int b) {
 }
 __device__ __forceinline__ long long* ws_base(const MassArgs& a) {  // [B + 1]
   return a.ws_plan + static_cast<size_t>(a.B) * (a.max_kt + 1);
+}
+// [B, max_kt] the first query tile of a key tile, and its units.
+__device__ __forceinline__ int2* ws_tiles(const MassArgs& a, int b) {
+  return reinterpret_cast<int2*>(ws_base(a) + a.B + 1) + static_cast<size_t>(b) * a.max_kt;
 }
 
 // ---------------------------------------------------------------- plan
@@ -169,9 +172,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_mass_plan_kernel(const Mass
   long long base = 0;
   for (int k0 = 0; k0 < n; k0 += kPlanThreads) {
     const int kt = k0 + tid;
-    int first;
-    long long v = kt < n ? static_cast<long long>(query_tiles(a, s, kt, &first)) * a.HC : 0;
-    if (v > 0) v += kItemCost;
+    int first = 0;
+    const int units = kt < n ? query_tiles(a, s, kt, &first) * a.HC : 0;
+    if (kt < n) ws_tiles(a, b)[kt] = make_int2(first * a.HC, units);
+    const long long v = units > 0 ? units + kItemCost : 0;
     long long x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -193,27 +197,38 @@ __global__ void __launch_bounds__(kPlanThreads) attn_mass_plan_kernel(const Mass
 }
 
 // ---------------------------------------------------------------- the walk
-// A CTA's run of units: the key tiles in order, each with its query tiles.
+// A CTA's run: the key tiles in order, each with its units.  Every role walks for itself; what
+// a key tile has to do was worked out by the plan and is read one key tile ahead.
 struct Walk {
-  int b, h, kt, first, n, u;  // key tile; its first query tile, units, and the next unit
-                              // (below 0: positions before its first)
-  long long left;             // positions left in the run
-  int tiles;                  // key tiles of the sequence
+  int b, h, kt, n, u;  // key tile; its units, and the next of them (below 0: positions before
+                       // its first)
+  int tile;            // query tile of unit 0 (times HC, by head groups)
+  long long left;      // positions left in the run
+  int tiles;           // key tiles of the sequence
+  int2 next;           // query tile and units of the key tile behind this one
+  const int2* plan;
   Seq s;
 };
 
-__device__ __forceinline__ bool walk_item(const MassArgs& a, Walk& w) {
-  if (w.left <= 0) return false;
-  w.n = query_tiles(a, w.s, w.kt, &w.first) * a.HC;
-  return true;
+__device__ __forceinline__ void walk_row(const MassArgs& a, Walk& w, int kt) {
+  w.plan = ws_tiles(a, w.b);
+  w.kt = kt;
+  const int2 t = w.plan[kt];
+  w.tile = t.x;
+  w.n = t.y;
+  w.next = w.plan[min(kt + 1, w.tiles - 1)];
 }
 
 // The next key tile with units.
 __device__ __forceinline__ bool walk_next(const MassArgs& a, Walk& w) {
   w.u = -kItemCost;
   while (w.left > 0) {
-    if (++w.kt >= w.tiles) {
-      w.kt = 0;
+    if (w.kt + 1 < w.tiles) {
+      ++w.kt;
+      w.tile = w.next.x;
+      w.n = w.next.y;
+      if (w.kt + 1 < w.tiles) w.next = w.plan[w.kt + 1];
+    } else {
       if (++w.h >= a.Hkv) {
         w.h = 0;
         do {
@@ -221,8 +236,9 @@ __device__ __forceinline__ bool walk_next(const MassArgs& a, Walk& w) {
           w.tiles = load_seq(a, w.b, w.s) ? key_tiles(w.s) : 0;
         } while (w.tiles == 0);
       }
+      walk_row(a, w, 0);
     }
-    if (walk_item(a, w) && w.n > 0) return true;
+    if (w.n > 0) return true;
   }
   return false;
 }
@@ -408,11 +424,10 @@ __global__ void __launch_bounds__(kThr, 1)
     Walk w;
     w.b = s_start[0];
     w.h = s_start[1];
-    w.kt = s_start[2];
     w.left = s_run[1];
     load_seq(a, w.b, w.s);
     w.tiles = key_tiles(w.s);
-    walk_item(a, w);
+    walk_row(a, w, s_start[2]);
     w.u = static_cast<int>(s_run[0]);  // may stand before the first unit
 
     if (warp == kWarpProducer) {
@@ -434,7 +449,7 @@ __global__ void __launch_bounds__(kThr, 1)
         const int units = walk_units(w);
         if (units == 0) break;
         const int pages = min(kPagesPerTile, (w.s.L - w.kt * kKeys + kPage - 1) / kPage);
-        const int b = w.b, h = w.h, u0 = w.first * a.HC + w.u, q_base = w.s.q_base;
+        const int b = w.b, h = w.h, u0 = w.tile + w.u, q_base = w.s.q_base;
         w.left -= units;
         more = walk_next(a, w);
         if (page < 0 || page >= a.num_pages) {
@@ -505,7 +520,7 @@ __global__ void __launch_bounds__(kThr, 1)
         int units = walk_units(w);
         if (units == 0) break;
         const bool ts = units >= kMinTs;
-        int u = w.first * a.HC + w.u;
+        int u = w.tile + w.u;
         bool fresh = !(w.b == pb && w.h == ph && u == pu);  // another query tile
         pb = w.b, ph = w.h, pu = u + units - 1;
         w.left -= units;
@@ -589,7 +604,7 @@ __global__ void __launch_bounds__(kThr, 1)
       int pb = -1, ph = -1, pu = -1;
       float v[kPer], next[kPer];
       auto fetch = [&] {
-        const int u = w.first * a.HC + w.u + i;
+        const int u = w.tile + w.u + i;
         if (w.b == pb && w.h == ph && u == pu) return;
         pb = w.b, ph = w.h, pu = u;
         const int t0 = tile_token(a, u);
@@ -684,12 +699,10 @@ __global__ void __launch_bounds__(kThr, 1)
           all0 = kb - w.s.off;
         }
         if (a.window > 0 && key >= a.n_sink)
-          see1 = static_cast<int>(
-              min(static_cast<long long>(see1), static_cast<long long>(key) + a.window - w.s.off));
+          see1 = min(see1, key + a.window - w.s.off);
         if (a.window > 0 && kb >= a.n_sink)
-          all1 = static_cast<int>(min(static_cast<long long>(all1),
-                                      static_cast<long long>(ka) + a.window - w.s.off - a.TQ));
-        const int u0 = w.first * a.HC + w.u;
+          all1 = min(all1, ka + a.window - w.s.off - a.TQ);
+        const int u0 = w.tile + w.u;
         int i0 = tile_token(a, u0);
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         for (int i = 0; i < units; ++i) {

@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kGridMax = 65535;  // blocks along y or z of a grid
 constexpr int kGroupsMax = 1 << 20;
+constexpr int kMassMaxTokens = 1 << 29;  // queries, or keys of a row, of attn_mass_paged
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -99,6 +100,11 @@ size_t mass_tiles(int max_pages) {
 }
 
 size_t pad16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
+
+// Positions before each key tile and sequence, and the key tiles' units.
+size_t mass_plan_bytes(int B, size_t kt) {
+  return pad16((static_cast<size_t>(B) * (2 * kt + 2) + 1) * sizeof(long long));
+}
 
 // Workspace of attn_decode_paged_shared, in bytes from its start.
 struct SharedLayout {
@@ -254,7 +260,7 @@ ATTN_API int attn_decode_paged_mass(const void* q, const void* k_pages, const vo
 ATTN_API size_t attn_mass_workspace_size(int B, int Hkv, int max_pages_per_seq) {
   if (B < 0 || Hkv <= 0 || max_pages_per_seq <= 0) return 0;
   const size_t kt = mass_tiles(max_pages_per_seq);
-  return pad16((static_cast<size_t>(B) * (kt + 2) + 1) * sizeof(long long)) +
+  return mass_plan_bytes(B, kt) +
          (static_cast<size_t>(B) * Hkv * kt + kMaxSms) * mass_partial_floats() * sizeof(float);
 }
 
@@ -269,9 +275,11 @@ ATTN_API int attn_mass_paged(const void* q, const float* lse, const void* k_page
   clear_error();
   int rc = check_heads(B, Hq, Hkv, d, page_size, max_pages_per_seq, num_pages_total);
   if (rc != ATTN_OK) return rc;
-  if (mass_slots <= 0 || max_Sq < 0 || total_q < 0 || max_Sq > (1 << 30) || total_q > (1 << 30))
-    return set_error(ATTN_ERR_INVALID_ARG, "bad sizes (mass_slots=%d max_Sq=%d total_q=%d)",
-                     mass_slots, max_Sq, total_q);
+  if (mass_slots <= 0 || max_Sq < 0 || total_q < 0 || max_Sq > kMassMaxTokens ||
+      total_q > kMassMaxTokens || max_pages_per_seq > kMassMaxTokens / 16)
+    return set_error(ATTN_ERR_INVALID_ARG,
+                     "bad sizes (mass_slots=%d max_Sq=%d total_q=%d max_pages=%d)", mass_slots,
+                     max_Sq, total_q, max_pages_per_seq);
   if (causal != 0 && causal != 1) return set_error(ATTN_ERR_INVALID_ARG, "causal must be 0 or 1");
   if (window > 0 && !causal)
     return set_error(ATTN_ERR_INVALID_ARG, "a sliding window requires causal");
@@ -332,12 +340,12 @@ ATTN_API int attn_mass_paged(const void* q, const float* lse, const void* k_page
   a.max_kt = static_cast<int>(mass_tiles(max_pages_per_seq));
   a.scale2 = scale * 1.4426950408889634f;
   a.causal = causal;
-  a.window = window > 0 ? window : 0;
+  const int longest = max_pages_per_seq * 16;
+  a.window = window <= 0 ? 0 : window < longest ? window : longest;
   a.n_sink = n_sink;
   a.ws_plan = static_cast<long long*>(workspace);
   a.ws_part = reinterpret_cast<float*>(
-      static_cast<char*>(workspace) +
-      pad16((static_cast<size_t>(B) * (a.max_kt + 2) + 1) * sizeof(long long)));
+      static_cast<char*>(workspace) + mass_plan_bytes(B, a.max_kt));
   const cudaError_t e = launch_attn_mass(a, num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : cuda_error(e, "attn_mass_paged launch");
 }

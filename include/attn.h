@@ -652,7 +652,8 @@ ATTN_API int attn_decode_paged_mass(const void* q, const void* k_pages, const vo
  *   Each partial sum is formed by one CTA and they are added in a fixed order:
  *   repeated calls give identical bits.
  *   workspace: attn_mass_workspace_size(...) bytes, 16-byte aligned.  B and Hq
- *   at most 65,535, B * Hq, max_Sq and total_q at most 2^30.
+ *   at most 65,535, B * Hq at most 2^30, max_Sq, total_q and
+ *   max_pages_per_seq * 16 at most 2^29.
  */
 ATTN_API size_t attn_mass_workspace_size(int B, int Hkv, int max_pages_per_seq);
 ATTN_API int attn_mass_paged(const void* q, const float* lse, const void* k_pages,

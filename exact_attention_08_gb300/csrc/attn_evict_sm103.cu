@@ -14,11 +14,22 @@
 // waits for another, and a row 64 tokens over its budget of 1,024 moves about
 // 60 tokens where closing the gaps in order would move about a thousand.
 //
-// Split.  One CTA per (layer, row, key head) selects: its keys sit in shared
-// memory (16 bytes of histogram and key work a token against 8 read), and it
-// writes its moves as (from, to) pairs and moves mass and position.  The keys
-// and values are then moved by the whole GPU, launched as a programmatic
-// dependent, 16 bytes a thread and four in flight.
+// Selection.  One CTA per (layer, row, key head).  Its keys go to shared memory once, and
+// with them a histogram of their top 11 bits (sign, exponent, two bits of the
+// mantissa: some 50 bins in use for masses, so few lanes meet in one); the next bits
+// count only the keys of the bin that holds the keep-th largest, and the search ends as
+// soon as that bin holds no more than are wanted, after two rounds as a rule.  Another
+// look at the keys leaves two bits a token (above T, at T) as words of 32, and ties,
+// holes and moves are counted over words.  Rows past kMaxCached tokens do not fit in
+// shared memory: they are read again from memory for each of six steps
+// (attn_evict_select_long_kernel).
+//
+// A CTA runs through its code once, so the code's size is its time as much as the work:
+// with every loop unrolled (62 KB) rows of 1,088 tokens took 23 us.
+//
+// Split.  The selecting CTA writes its moves as (from, to) pairs and moves mass and
+// position.  The keys and values are then moved by the whole GPU, launched as a
+// programmatic dependent, 16 bytes a thread and four in flight.
 #include "attn_internal.h"
 
 #include <algorithm>
@@ -33,6 +44,9 @@ constexpr int kBins = 2048;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVecs = 4;
 constexpr int kMaxCached = 40960;  // tokens whose keys fit in a CTA's shared memory (160 KB)
+// Threads of the selecting CTA: rows of up to 4,096 tokens take 256 (a longer block waits
+// longer at its barriers), longer ones 384, four CTAs an SM.
+constexpr int kSmallRow = 4096, kSmallThreads = 256, kLargeThreads = 384;
 constexpr uint32_t kProtected = 0xffffffffu;
 
 // Larger mass, larger key; 0 for NaN.
@@ -44,6 +58,10 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
 
 __device__ __forceinline__ int2* unit_moves(const EvictArgs& a, int unit) {
   return reinterpret_cast<int2*>(a.ws) + static_cast<size_t>(unit) * a.most_moves;
+}
+// Row of a pool (page * 16 + token) that holds a slot.
+__device__ __forceinline__ int pool_row(const EvictArgs& a, int b, int slot) {
+  return a.page_table[static_cast<size_t>(b) * a.max_pages + slot / kPage] * kPage + slot % kPage;
 }
 __device__ __forceinline__ int* unit_count(const EvictArgs& a, int unit) {
   return a.ws + 2 * static_cast<size_t>(a.units) * a.most_moves + unit;
@@ -72,9 +90,8 @@ __device__ __forceinline__ int block_scan(int v, int* warp_part, int* total) {
   return base + x - v;
 }
 
-template <bool kCached>
-__global__ void __launch_bounds__(kThreads) attn_evict_select_kernel(const EvictArgs a) {
-  extern __shared__ uint32_t s_keys[];
+// Rows of any length: the keys are formed again for every step.
+__global__ void __launch_bounds__(kThreads) attn_evict_select_long_kernel(const EvictArgs a) {
   __shared__ int s_hist[kBins];
   __shared__ int s_part[kWarps];
   __shared__ int s_flag, s_newest, s_bin, s_above;
@@ -105,6 +122,7 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_kernel(const Evict
     const int* row = a.page_table + static_cast<size_t>(b) * a.max_pages;
     const int pages = (L + kPage - 1) / kPage, written = (K + kPage - 1) / kPage;
     bool wrong = false;
+#pragma unroll 1
     for (int i = tid; i < pages; i += kThreads) {
       const int p = row[i];
       if (p < 0 || p >= a.num_pages)
@@ -118,6 +136,7 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_kernel(const Evict
   int* pos = a.positions + static_cast<size_t>(unit) * a.slots;
   if (a.recent > 0) {
     int newest = INT32_MIN;
+#pragma unroll 1
     for (int t = tid; t < L; t += kThreads) newest = max(newest, pos[t]);
     newest = __reduce_max_sync(0xffffffffu, newest);
     if (lane == 0) atomicMax(&s_newest, newest);
@@ -137,11 +156,6 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_kernel(const Evict
     const int p = pos[t];
     return (p < a.n_sink || p > recent_from) ? kProtected : mass_key(mass[t]);
   };
-  if (kCached) {
-    for (int t = tid; t < L; t += kThreads) s_keys[t] = make_key(t);
-    __syncthreads();
-  }
-  auto key_of = [&](int t) -> uint32_t { return kCached ? s_keys[t] : make_key(t); };
 
   // ---- the K-th largest key: its bits from the top, 11, 11 and 10 of them
   uint32_t prefix = 0;
@@ -150,11 +164,13 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_kernel(const Evict
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const int bits = pass == 2 ? 10 : 11;
+#pragma unroll 1
     for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
     __syncthreads();
     const uint32_t mask = (1u << bits) - 1u;
+#pragma unroll 1
     for (int t = tid; t < L; t += kThreads) {
-      const uint32_t k = key_of(t);
+      const uint32_t k = make_key(t);
       const uint32_t up = pass == 0 ? 0u : k >> (shift + bits);
       if (up == prefix) atomicAdd(&s_hist[(k >> shift) & mask], 1);
     }
@@ -189,13 +205,15 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_kernel(const Evict
   const int t0 = min(warp * run, L), t1 = min(t0 + run, L);
   const uint32_t below = (1u << lane) - 1u;
   int ties = 0;
+#pragma unroll 1
   for (int t = t0; t < t1; t += 32) {
-    const bool tie = t + lane < t1 && key_of(t + lane) == T;
+    const bool tie = t + lane < t1 && make_key(t + lane) == T;
     ties += __popc(__ballot_sync(0xffffffffu, tie));
   }
   if (lane == 0) s_part[warp] = ties;
   __syncthreads();
   int tie_base = 0;
+#pragma unroll 1
   for (int w = 0; w < warp; ++w) tie_base += s_part[w];
   __syncthreads();
   int2* moves = unit_moves(a, unit);
@@ -203,10 +221,11 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_kernel(const Evict
 #pragma unroll 1
   for (int phase = 0; phase < 2; ++phase) {  // count, then write
     int tie_rank = tie_base, holes = hole_base, movers = mover_base;
+#pragma unroll 1
     for (int t = t0; t < t1; t += 32) {
       const int at = t + lane;
       const bool valid = at < t1;
-      const uint32_t k = valid ? key_of(at) : 0u;
+      const uint32_t k = valid ? make_key(at) : 0u;
       const bool tie = valid && k == T;
       const uint32_t tie_mask = __ballot_sync(0xffffffffu, tie);
       const bool stays = valid && (k > T || (tie && tie_rank + __popc(tie_mask & below) < want));
@@ -227,6 +246,7 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_kernel(const Evict
         s_movers[warp] = movers;
       }
       __syncthreads();
+#pragma unroll 1
       for (int w = 0; w < kWarps; ++w) {
         if (w < warp) {
           hole_base += s_part[w];
@@ -237,14 +257,277 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_kernel(const Evict
     }
   }
   __syncthreads();
+#pragma unroll 1
   for (int i = tid; i < total; i += kThreads) {
     const int2 m = moves[i];
     mass[m.y] = mass[m.x];
     pos[m.y] = pos[m.x];
+    moves[i] = make_int2(pool_row(a, b, m.x), pool_row(a, b, m.y));
   }
   if (tid == 0) {
     *unit_count(a, unit) = total;
     if (lead) a.new_seqlens[b] = K;
+  }
+}
+
+// Sum before this thread and total over a block of up to 16 warps (part: 32 values).
+template <typename T>
+__device__ __forceinline__ T scan_block(T v, T* part, T* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  T x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  T p = lane < warps ? part[lane] : 0;
+  T sum = p;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += y;
+  }
+  *total = __shfl_sync(0xffffffffu, sum, warps - 1);
+  return x - v + __shfl_sync(0xffffffffu, sum - p, warp);
+}
+
+// Lowest n set bits of x (all of them in every word but one).
+__device__ __forceinline__ uint32_t lowest_bits(uint32_t x, int n) {
+#pragma unroll 1
+  while (__popc(x) > max(n, 0)) x ^= 0x80000000u >> __clz(x);
+  return x;
+}
+
+// Rows whose keys fit in shared memory: keys [slots rounded up to 32], then two words for
+// every 32 of them.
+// kFours: rows of mass and positions start on 16 bytes, four tokens a load.
+template <bool kFours>
+__global__ void __launch_bounds__(kLargeThreads, 4) attn_evict_select_kernel(const EvictArgs a,
+                                                                             int words) {
+  extern __shared__ uint32_t s_keys[];
+  __shared__ int s_hist[kBins];
+  __shared__ int s_group[kBins / 32];
+  __shared__ int s_part[32];
+  __shared__ long long s_part2[32];
+  __shared__ int s_flag, s_newest, s_bin, s_want;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  const int warps = threads >> 5;
+  const int unit = blockIdx.x;
+  const int h = unit % a.Hkv, b = (unit / a.Hkv) % a.B, layer = unit / (a.Hkv * a.B);
+  const int L = a.seqlens[b], K = a.keep[b];
+  const int cap = min(a.slots, a.max_pages * kPage);
+  const bool lead = h == 0 && layer == 0;
+  const bool bad = L < 0 || L > cap || K < 0;
+  if (bad || K >= L || K == 0) {
+    if (tid == 0) {
+      *unit_count(a, unit) = 0;
+      if (lead) a.new_seqlens[b] = (bad || K >= L) ? L : 0;
+      if (bad) atomicOr(a.status, kStatusBadInput);
+    }
+    return;
+  }
+  float* mass = a.mass + static_cast<size_t>(unit) * a.slots;
+  int* pos = a.positions + static_cast<size_t>(unit) * a.slots;
+  if (tid == 0) {
+    s_flag = 0;
+    s_newest = INT32_MIN;
+  }
+#pragma unroll 1
+  for (int i = tid; i < kBins; i += threads) s_hist[i] = 0;
+  // Every page of the row must be one of the pool, and the pages written to must
+  // be the row's alone.
+  bool wrong = false;
+  {
+    const int* row = a.page_table + static_cast<size_t>(b) * a.max_pages;
+    const int pages = (L + kPage - 1) / kPage, written = (K + kPage - 1) / kPage;
+#pragma unroll 1
+    for (int i = tid; i < pages; i += threads) {
+      const int p = row[i];
+      if (p < 0 || p >= a.num_pages)
+        wrong = true;
+      else if (a.refs != nullptr && i < written && a.refs[p] > 1)
+        wrong = true;
+    }
+  }
+  // tokens four by four; those of the last, shorter group one by one
+  const int fours = kFours ? L / 4 : 0;
+  int newest = INT32_MIN;
+  if (a.recent > 0) {
+#pragma unroll 2
+    for (int i = tid; i < fours; i += threads) {
+      const int4 p = reinterpret_cast<const int4*>(pos)[i];
+      newest = max(max(max(newest, p.x), p.y), max(p.z, p.w));
+    }
+#pragma unroll 1
+    for (int t = 4 * fours + tid; t < L; t += threads) newest = max(newest, pos[t]);
+    newest = __reduce_max_sync(0xffffffffu, newest);
+  }
+  __syncthreads();
+  if (lane == 0 && a.recent > 0) atomicMax(&s_newest, newest);
+  if (wrong) s_flag = 1;
+  __syncthreads();
+  if (s_flag) {
+    if (tid == 0) {
+      *unit_count(a, unit) = 0;
+      if (lead) a.new_seqlens[b] = L;
+      atomicOr(a.status, kStatusBadInput);
+    }
+    return;
+  }
+  const long long recent_from =
+      a.recent > 0 ? static_cast<long long>(s_newest) - a.recent : INT64_MAX;
+  // (position > recent_from, as a 32-bit comparison: INT32_MAX + 1 stands for none)
+  const bool all_recent = recent_from < INT32_MIN;
+  const int after = all_recent ? INT32_MIN
+                               : static_cast<int>(min(recent_from, static_cast<long long>(INT32_MAX)));
+  auto make_key = [&](float m, int p) -> uint32_t {
+    const uint32_t k = (p < a.n_sink || p > after || all_recent) ? kProtected : mass_key(m);
+    atomicAdd(&s_hist[k >> 21], 1);
+    return k;
+  };
+#pragma unroll 2
+  for (int i = tid; i < fours; i += threads) {
+    const int4 p = reinterpret_cast<const int4*>(pos)[i];
+    const float4 m = reinterpret_cast<const float4*>(mass)[i];
+    reinterpret_cast<uint4*>(s_keys)[i] = make_uint4(make_key(m.x, p.x), make_key(m.y, p.y),
+                                                     make_key(m.z, p.z), make_key(m.w, p.w));
+  }
+#pragma unroll 1
+  for (int t = 4 * fours + tid; t < L; t += threads) s_keys[t] = make_key(mass[t], pos[t]);
+  // whole words of keys from here on: the last one is filled up with the least
+  for (int t = L + tid; t < (L + 31) / 32 * 32; t += threads) s_keys[t] = 0u;
+  __syncthreads();
+
+  // ---- the threshold's bits from the top, 11, 11 and 10 of them, until the keys that share
+  // them are just as many as are still wanted
+  uint32_t T = 0;   // the threshold's bits from `shift` up
+  int want = K;     // how many of the keys with these bits stay
+  int shift = 21;
+#pragma unroll 1
+  for (;;) {
+    // the bin in which the want-th key falls, from the largest down: groups of 32 first
+#pragma unroll 1
+    for (int j = warp; j < kBins / 32; j += warps) {
+      const int n = __reduce_add_sync(0xffffffffu, s_hist[kBins - 1 - (j * 32 + lane)]);
+      if (lane == 0) s_group[j] = n;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int lo = s_group[lane], x = lo;
+      int hi = s_group[32 + lane], y = hi;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) x += u, y += v;
+      }
+      y += __shfl_sync(0xffffffffu, x, 31);
+      const uint32_t hit0 = __ballot_sync(0xffffffffu, x >= want);
+      const uint32_t hit1 = __ballot_sync(0xffffffffu, y >= want);
+      const int at = __ffs(hit0 ? hit0 : hit1) - 1;
+      const int before = __shfl_sync(0xffffffffu, hit0 ? x - lo : y - hi, at);
+      const int group = hit0 ? at : 32 + at;
+      const int n = s_hist[kBins - 1 - (group * 32 + lane)];
+      x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += u;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, before + x >= want);
+      if (lane == __ffs(hit) - 1) {
+        s_bin = kBins - 1 - (group * 32 + lane);
+        s_want = want - (before + x - n);
+      }
+    }
+    __syncthreads();
+    const int bin = s_bin, in_bin = s_hist[bin];
+    T = shift == 0 ? (T << 10) | bin : (T << 11) | bin;
+    want = s_want;
+    if (shift == 0 || in_bin == want) break;
+    const int next = shift == 21 ? 10 : 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = tid; i < kBins; i += threads) s_hist[i] = 0;
+    __syncthreads();
+    const uint32_t mask = next == 0 ? 0x3ffu : 0x7ffu;
+#pragma unroll 1
+    for (int i = tid; i < (L + 3) / 4; i += threads) {
+      const uint4 k4 = reinterpret_cast<const uint4*>(s_keys)[i];
+      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((k[e] >> shift) == T && 4 * i + e < L) atomicAdd(&s_hist[(k[e] >> next) & mask], 1);
+    }
+    __syncthreads();
+    shift = next;
+  }
+
+  // ---- above T and at T, a bit a token
+  uint32_t* s_gt = s_keys + words * 32;
+  uint32_t* s_eq = s_gt + words;
+  const int n_words = (L + 31) / 32;
+#pragma unroll 1
+  for (int i = warp; i < n_words; i += warps) {
+    const int t = i * 32 + lane;
+    const uint32_t k = t < L ? s_keys[t] >> shift : 0u;
+    const uint32_t gt = __ballot_sync(0xffffffffu, t < L && k > T);
+    const uint32_t eq = __ballot_sync(0xffffffffu, t < L && k == T);
+    if (lane == 0) {
+      s_gt[i] = gt;
+      s_eq[i] = eq;
+    }
+  }
+  __syncthreads();
+  // ---- ties by slot, then holes and movers: a run of words a thread
+  const int per = (n_words + threads - 1) / threads;
+  const int w0 = min(tid * per, n_words), w1 = min(w0 + per, n_words);
+  int ties = 0;
+#pragma unroll 1
+  for (int i = w0; i < w1; ++i) ties += __popc(s_eq[i]);
+  int all_ties;
+  int rank = scan_block(ties, s_part, &all_ties);
+  int holes = 0, movers = 0;
+#pragma unroll 1
+  for (int i = w0; i < w1; ++i) {
+    const uint32_t eq = s_eq[i];
+    const uint32_t stay = s_gt[i] | lowest_bits(eq, want - rank);
+    rank += __popc(eq);
+    s_gt[i] = stay;
+    // slots of this word before K
+    const int below = min(max(K - i * 32, 0), 32);
+    const uint32_t low = below == 32 ? 0xffffffffu : (1u << below) - 1u;
+    holes += __popc(~stay & low);
+    movers += __popc(stay & ~low);
+  }
+  long long total2;
+  const long long first = scan_block((static_cast<long long>(holes) << 32) | movers, s_part2, &total2);
+  int at_hole = static_cast<int>(first >> 32), at_mover = static_cast<int>(first & 0xffffffff);
+  const int total = static_cast<int>(total2 & 0xffffffff);
+  int2* moves = unit_moves(a, unit);
+#pragma unroll 1
+  for (int i = w0; i < w1; ++i) {
+    const uint32_t stay = s_gt[i];
+    const int below = min(max(K - i * 32, 0), 32);
+    const uint32_t low = below == 32 ? 0xffffffffu : (1u << below) - 1u;
+#pragma unroll 1
+    for (uint32_t x = ~stay & low; x != 0; x &= x - 1) moves[at_hole++].y = i * 32 + __ffs(x) - 1;
+#pragma unroll 1
+    for (uint32_t x = stay & ~low; x != 0; x &= x - 1) moves[at_mover++].x = i * 32 + __ffs(x) - 1;
+  }
+  if (tid == 0) {
+    *unit_count(a, unit) = total;
+    if (lead) a.new_seqlens[b] = K;
+  }
+  __syncthreads();
+#pragma unroll 2
+  for (int i = tid; i < total; i += threads) {
+    const int2 m = moves[i];
+    mass[m.y] = mass[m.x];
+    pos[m.y] = pos[m.x];
+    moves[i] = make_int2(pool_row(a, b, m.x), pool_row(a, b, m.y));
   }
 }
 
@@ -254,13 +537,13 @@ template <int kVecs>
 __global__ void __launch_bounds__(kCopyThreads) attn_evict_copy_kernel(const EvictArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int unit = blockIdx.x / a.copy_blocks, part = blockIdx.x % a.copy_blocks;
-  const int h = unit % a.Hkv, b = (unit / a.Hkv) % a.B, layer = unit / (a.Hkv * a.B);
+  const int h = unit % a.Hkv, layer = unit / (a.Hkv * a.B);
   const int count = *unit_count(a, unit);
   const int2* moves = unit_moves(a, unit);
-  const int* row = a.page_table + static_cast<size_t>(b) * a.max_pages;
-  const size_t pool = static_cast<size_t>(layer) * a.num_pages;
+  const size_t layer0 = static_cast<size_t>(layer) * a.num_pages * kPage;
   const long long total = static_cast<long long>(count) * (2 * kVecs);
   const long long step = static_cast<long long>(a.copy_blocks) * kCopyThreads;
+#pragma unroll 1
   for (long long i0 = static_cast<long long>(part) * kCopyThreads + threadIdx.x; i0 < total;
        i0 += step * kCopyVecs) {
     uint4 v[kCopyVecs];
@@ -272,13 +555,9 @@ __global__ void __launch_bounds__(kCopyThreads) attn_evict_copy_kernel(const Evi
       if (i >= total) continue;
       const int2 m = moves[i / (2 * kVecs)];
       const int r = static_cast<int>(i % (2 * kVecs));
-      uint4* base = r < kVecs ? a.k_pages : a.v_pages;
-      const int vec = r < kVecs ? r : r - kVecs;
-      auto at = [&](int t) {
-        return (((pool + row[t / kPage]) * kPage + t % kPage) * a.Hkv + h) * kVecs + vec;
-      };
-      v[j] = base[at(m.x)];
-      to[j] = base + at(m.y);
+      uint4* base = (r < kVecs ? a.k_pages : a.v_pages) + (r < kVecs ? r : r - kVecs);
+      v[j] = base[((layer0 + m.x) * a.Hkv + h) * kVecs];
+      to[j] = base + ((layer0 + m.y) * a.Hkv + h) * kVecs;
     }
 #pragma unroll
     for (int j = 0; j < kCopyVecs; ++j)
@@ -290,21 +569,28 @@ __global__ void __launch_bounds__(kCopyThreads) attn_evict_copy_kernel(const Evi
 
 cudaError_t launch_attn_evict(EvictArgs a, int num_sms, cudaStream_t stream) {
   const int cap = std::min(a.slots, a.max_pages * kPage);
-  const bool cached = cap <= kMaxCached;
-  const size_t smem = cached ? static_cast<size_t>(cap) * 4 : 0;
-  auto select = cached ? attn_evict_select_kernel<true> : attn_evict_select_kernel<false>;
-  static SharedMemoryLimit limit;
-  cudaError_t e = limit.raise(attn_evict_select_kernel<true>, kMaxCached * 4);
-  if (e != cudaSuccess) return e;
-  select<<<a.units, kThreads, smem, stream>>>(a);
+  cudaError_t e;
+  if (cap <= kMaxCached) {
+    const int words = (cap + 31) / 32;
+    static SharedMemoryLimit limit, limit4;
+    const bool fours = a.slots % 4 == 0 && reinterpret_cast<uintptr_t>(a.mass) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(a.positions) % 16 == 0;
+    auto select = fours ? attn_evict_select_kernel<true> : attn_evict_select_kernel<false>;
+    e = (fours ? limit4 : limit).raise(select, (kMaxCached + 2 * kMaxCached / 32) * 4);
+    if (e != cudaSuccess) return e;
+    select<<<a.units, cap <= kSmallRow ? kSmallThreads : kLargeThreads,
+             static_cast<size_t>(words) * 34 * 4, stream>>>(a, words);
+  } else {
+    attn_evict_select_long_kernel<<<a.units, kThreads, 0, stream>>>(a);
+  }
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // about eight blocks for every SM, no more than there can be steps
+  // about sixteen blocks for every SM, no more than there can be steps
   const int per_step = kCopyThreads * kCopyVecs;
   const long long most = (static_cast<long long>(a.most_moves) * 2 * a.vecs + per_step - 1) /
                          per_step;
   a.copy_blocks = static_cast<int>(
-      std::max(1LL, std::min(most, (8LL * num_sms + a.units - 1) / a.units)));
+      std::max(1LL, std::min(most, (16LL * num_sms + a.units - 1) / a.units)));
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kCopyThreads);
   cfg.stream = stream;

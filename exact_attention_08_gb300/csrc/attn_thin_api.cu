@@ -374,6 +374,8 @@ ATTN_API int attn_evict_paged(float* mass, int* positions, const int* page_table
   if (units > kEvictMaxUnits)
     return set_error(ATTN_ERR_INVALID_ARG, "%lld rows, layers and heads, at most %d", units,
                      kEvictMaxUnits);
+  if (num_pages_total > kPagesMaxPages)
+    return set_error(ATTN_ERR_INVALID_ARG, "%d pages, at most %d", num_pages_total, kPagesMaxPages);
   if (B == 0) return ATTN_OK;
   if (!mass || !positions || !page_table || !seqlens || !keep || !new_seqlens || !k_pages ||
       !v_pages)

@@ -693,7 +693,7 @@ ATTN_API int attn_mass_paged(const void* q, const float* lse, const void* k_page
  *   New tokens of a thinned row: their slots no longer are their positions, so
  *     rotate q and k with attn_rope and append them with rotary_dim 0.
  *   workspace: attn_evict_workspace_size(...) bytes, 16-byte aligned.  layers *
- *   B * Hkv at most 2^24, B and Hkv at most 65,535.
+ *   B * Hkv at most 2^24, B and Hkv at most 65,535, 2^23 pages.
  */
 ATTN_API size_t attn_evict_workspace_size(int layers, int B, int Hkv, int slots,
                                           int max_pages_per_seq);

@@ -183,3 +183,14 @@ def test_streams_graphs_and_outputs():
     torch.cuda.synchronize()
     c.check(want, out)
     assert ea.attn_device_status() == ea.ATTN_OK
+
+
+@pytest.mark.parametrize("L,K", [(3000, 1400), (8000, 3999), (8000, 4001), (33, 32), (64, 31)])
+@pytest.mark.parametrize("values", [1, 2, 700])
+def test_many_equal_masses(L, K, values):
+    """Few distinct masses: more keys at the threshold than are listed, the first by slot."""
+    c = Cache([L, L], 1, 2, 64, seed=L + values)
+    g = torch.Generator().manual_seed(values)
+    c.mass = 0.5 + torch.randint(0, values, c.mass.shape, generator=g).float() / 1024
+    c.run([K, min(K, L // 3)], 4, 20)
+    assert ea.attn_device_status() == ea.ATTN_OK

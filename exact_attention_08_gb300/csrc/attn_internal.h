@@ -178,6 +178,7 @@ int mass_partial_floats();
 
 // The decode of rows that share a prefix: the groups, and the workspace.
 struct SharedArgs {
+  CUtensorMap tmK, tmV;    // whole pages
   const __nv_bfloat16* q;  // [B, Hq, d]
   const int* page_table;
   const int* seqlens;
@@ -186,9 +187,10 @@ struct SharedArgs {
   const int* rows;         // [n_rows], or null: row i is entry i
   int B, Hq, Hkv, G, n_groups, n_rows, max_pages, num_pages;
   float scale, scale2;       // scale2: scale log2 e
-  int tile_rows, tile_pages;  // set by the launcher
+  int tile_rows, tile_pages, ctas;  // set by the launcher
   // the plan
   long long* base;  // [n_groups + 1] units before a group
+  long long* runs;  // [kSharedMaxCtas + 1] first unit of a CTA
   int* pages;       // [n_groups] pages that its rows share
   int* source;      // [n_groups] the row whose table names them
   int* entry;       // [B] where the row stands in the list

@@ -11,6 +11,12 @@
 // many short ones alike fill the GPU.  An item that several CTAs share has a partial
 // result from each.
 //
+// Keys.  A page (16 tokens of one head) arrives in one copy: [d / 64 atoms][16 rows][128
+// bytes].  As the second operand of S its eight-row groups are evenly spaced only if
+// the first eight tokens of every page are taken together, and the others: two products
+// side by side, so column c of S is token key_of(c), and P is put back in order
+// where it is packed.  As the operand of O a page is just one step of 16 tokens.
+//
 // With S = Q K^T and O += P V on the tensor cores and the online softmax between them, a
 // key tile keeps an SM busy for less time than HBM needs to bring its keys and values
 // while an item has at most 256 rows; more rows find them in L2.
@@ -54,8 +60,9 @@ struct Cfg {
   static constexpr int kAtoms = D / 64;
   static constexpr int kQAtom = kRows * 128;
   static constexpr int kQTile = kAtoms * kQAtom;
-  static constexpr int kAtom = kKeys * 128;
-  static constexpr int kSlot = kAtoms * kAtom;         // a K or V tile
+  static constexpr int kPageAtom = kPage * 128;        // a page's 64 columns
+  static constexpr int kPageBytes = kAtoms * kPageAtom;
+  static constexpr int kSlot = kPages * kPageBytes;    // a K or V tile
   static constexpr int kSlots = D == 64 ? 8 : 5;
   static constexpr int kOffRing = kStreams * kQTile;
   static constexpr int kOffBar = kOffRing + kSlots * kSlot;
@@ -65,6 +72,17 @@ struct Cfg {
   static_assert(kSmem <= 227 * 1024 - 512, "shared memory (512 bytes of it static)");
   static constexpr uint32_t kColO = 256;
 };
+
+// Token of the key tile whose score stands in column c of S.
+template <int kKeys>
+__device__ __forceinline__ constexpr int key_of(int c) {
+  return (c % (kKeys / 2)) / 8 * kPage + c / (kKeys / 2) * 8 + c % 8;
+}
+// The column of token k.
+template <int kKeys>
+__device__ __forceinline__ constexpr int column_of(int k) {
+  return (k % kPage) / 8 * (kKeys / 2) + k / kPage * 8 + k % 8;
+}
 
 // ---------------------------------------------------------------- plan
 // Workspace of a call (ints): see SharedArgs.  One block: rows to groups, the pages that
@@ -111,14 +129,17 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) s_bad = 0;
+#pragma unroll 1
   for (int b = tid; b < a.B; b += kPlanThreads) {
     a.entry[b] = INT_MAX;
     a.start[b] = 0;
     a.group[b] = -1;
   }
+#pragma unroll 1
   for (int i = tid; i < kBuckets; i += kPlanThreads) s_cnt[i] = 0;
   __syncthreads();
   // offsets that decrease or leave the list: no group is used
+#pragma unroll 1
   for (int g = tid; g <= a.n_groups; g += kPlanThreads) {
     const int c = a.cu_groups[g];
     if (c < 0 || c > a.n_rows || (g > 0 && c < a.cu_groups[g - 1])) s_bad = 1;
@@ -129,6 +150,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
   const int n_groups = groups_ok ? a.n_groups : 0;
   // a row listed more than once belongs where it stands first
   if (n_groups > 0) {
+#pragma unroll 1
     for (int e = a.cu_groups[0] + tid; e < a.cu_groups[n_groups]; e += kPlanThreads) {
       const int b = a.rows ? a.rows[e] : e;
       if (b < 0 || b >= a.B)
@@ -139,9 +161,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
   }
   __syncthreads();
   // a warp for each group: its longest row, the pages it shares
+#pragma unroll 1
   for (int g = warp; g < n_groups; g += kPlanThreads / 32) {
     const int e0 = a.cu_groups[g], e1 = a.cu_groups[g + 1];
     int best = -1, at = INT_MAX, live = 0;
+#pragma unroll 1
     for (int e = e0 + lane; e < e1; e += 32) {
       const int b = a.rows ? a.rows[e] : e;
       if (b < 0 || b >= a.B || a.entry[b] != e) continue;
@@ -165,6 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
       a.pages[g] = pages;
       a.source[g] = at;
     }
+#pragma unroll 1
     for (int e = e0 + lane; e < e1; e += 32) {
       const int b = a.rows ? a.rows[e] : e;
       if (b < 0 || b >= a.B || a.entry[b] != e) continue;
@@ -176,6 +201,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
   // units before each group
   {
     long long base = 0;
+#pragma unroll 1
     for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
       const int g = g0 + tid;
       const long long v = g < n_groups ? group_units(a, a.cu_groups[g + 1] - a.cu_groups[g],
@@ -187,8 +213,13 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
       base += all;
     }
     if (tid == 0) a.base[a.n_groups] = base;
+    // with fewer units than CTAs the last CTAs have none, the others one each
+    const long long n = min(base, static_cast<long long>(a.ctas));
+#pragma unroll 1
+    for (int c = tid; c <= a.ctas; c += kPlanThreads) a.runs[c] = c < n ? base * c / n : base;
     // a list that is not used: every group ends where it begins
     if (n_groups == 0)
+#pragma unroll 1
       for (int g = tid; g < a.n_groups; g += kPlanThreads) a.base[g] = 0;
   }
   // rows by own pages, longest first (a counting sort; rows of one bucket in any order,
@@ -199,6 +230,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     const long long k = static_cast<long long>(a.max_pages - own) * nb / (a.max_pages + 1);
     return static_cast<int>(k < nb - 1 ? k : nb - 1);
   };
+#pragma unroll 1
   for (int b = tid; b < a.B; b += kPlanThreads) atomicAdd(&s_cnt[bucket(b)], 1);
   __syncthreads();
   constexpr int kPer = kBuckets / kPlanThreads;
@@ -214,13 +246,14 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
 #pragma unroll
   for (int j = 0; j < kPer; ++j) s_cnt[tid * kPer + j] = before + local[j];
   __syncthreads();
+#pragma unroll 1
   for (int b = tid; b < a.B; b += kPlanThreads) a.order[atomicAdd(&s_cnt[bucket(b)], 1)] = b;
 }
 
 // ---------------------------------------------------------------- items
 // One item of the prefix work and this CTA's part of it.
 struct Item {
-  int g, h, mt;           // group, key head, query tile pair
+  int g, h;               // group, key head
   int kt, n;              // first key tile of this CTA's part, key tiles in it
   int rows;               // (row, head) pairs of the item
   int row0;               // its first pair among the group's
@@ -229,42 +262,65 @@ struct Item {
   long long part;         // first row of its partial results
 };
 
+// A CTA's run: units left, and the item that it continues with.
 struct Walk {
-  long long at, end;      // units
-  int g;
+  long long left;
+  int g, h, mt, kt;
 };
 
-__device__ __forceinline__ bool walk_next(const SharedArgs& a, Walk& w, Item& it) {
-  if (w.at >= w.end) return false;
-  while (a.base[w.g + 1] <= w.at) ++w.g;
-  const int pages = a.pages[w.g];
-  const int e0 = a.cu_groups[w.g], n = a.cu_groups[w.g + 1] - e0;
-  const int tiles = (pages + a.tile_pages - 1) / a.tile_pages;
-  const int pairs = n * a.G;
-  const int mts = (pairs + a.tile_rows - 1) / a.tile_rows;
-  const long long in = w.at - a.base[w.g];
+__device__ __forceinline__ int ceil_div(int x, int y) { return (x + y - 1) / y; }
+
+// Where unit `at` stands.
+__device__ __noinline__ void walk_begin(const SharedArgs& a, Walk& w, long long at) {
+  int lo = 0, hi = a.n_groups;  // the last group with base <= at
+#pragma unroll 1
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (a.base[mid] <= at)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  w.g = lo;
+  if (w.left <= 0) return;
+  const int tiles = ceil_div(a.pages[lo], a.tile_pages);
+  const int mts = ceil_div((a.cu_groups[lo + 1] - a.cu_groups[lo]) * a.G, a.tile_rows);
+  const long long in = at - a.base[lo];
   const int item = static_cast<int>(in / tiles);
+  w.kt = static_cast<int>(in % tiles);
+  w.h = item / mts;
+  w.mt = item % mts;
+}
+
+__device__ __noinline__ bool walk_next(const SharedArgs& a, Walk& w, Item& it) {
+  if (w.left <= 0) return false;
+#pragma unroll 1
+  while (a.pages[w.g] == 0) ++w.g;  // a group with pages is behind, or nothing were left
+  const int pages = a.pages[w.g], e0 = a.cu_groups[w.g];
+  const int pairs = (a.cu_groups[w.g + 1] - e0) * a.G;
+  const int tiles = (pages + a.tile_pages - 1) / a.tile_pages;
   it.g = w.g;
-  it.h = item / mts;
-  it.mt = item % mts;
-  it.kt = static_cast<int>(in % tiles);
-  it.n = static_cast<int>(min(static_cast<long long>(tiles - it.kt), w.end - w.at));
-  it.row0 = it.mt * a.tile_rows;
+  it.h = w.h;
+  it.kt = w.kt;
+  it.n = static_cast<int>(min(static_cast<long long>(tiles - w.kt), w.left));
+  it.row0 = w.mt * a.tile_rows;
   it.rows = min(a.tile_rows, pairs - it.row0);
   it.first = e0;
   it.keys = pages * kPage;
-  it.part = 2 * (static_cast<long long>(e0) * a.Hq + static_cast<long long>(it.h) * pairs + it.row0) +
+  it.part = 2 * (static_cast<long long>(e0) * a.Hq + static_cast<long long>(w.h) * pairs + it.row0) +
             static_cast<long long>(kItemRows) * blockIdx.x;
-  w.at += it.n;
+  w.left -= it.n;
+  w.kt = 0;
+  if (it.row0 + a.tile_rows < pairs) {
+    ++w.mt;
+  } else {
+    w.mt = 0;
+    if (++w.h == a.Hkv) {
+      w.h = 0;
+      ++w.g;
+    }
+  }
   return true;
-}
-
-// Units [at, end) of CTA c among the first min(units, CTAs).
-__device__ __forceinline__ void run_of(const SharedArgs& a, int c, int ctas, long long* at,
-                                       long long* end) {
-  const long long T = a.base[a.n_groups], n = min(T, static_cast<long long>(ctas));
-  *at = c < n ? T * c / n : 0;
-  *end = c < n ? T * (c + 1) / n : 0;
 }
 
 template <int D>
@@ -318,17 +374,10 @@ __global__ void __launch_bounds__(kThr, 1)
   const uint32_t tmem = *tmem_slot;
 
   Walk w;
-  run_of(a, blockIdx.x, gridDim.x, &w.at, &w.end);
   {
-    int lo = 0, hi = a.n_groups;  // the last group with base <= at
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (a.base[mid] <= w.at)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    w.g = lo;
+    const long long at = a.runs[blockIdx.x];
+    w.left = a.runs[blockIdx.x + 1] - at;
+    walk_begin(a, w, at);
   }
   // An item's jobs, in order: S buffer and, with two streams, stream j % 2.  With a tile in
   // both streams job j is key tile j / 2, else key tile j.
@@ -355,18 +404,14 @@ __global__ void __launch_bounds__(kThr, 1)
       };
       auto load = [&](const CUtensorMap* map, int page) {
         const int s = n_load % C::kSlots;
-        if (n_load >= C::kSlots && !mbar_wait_warp(&empty[s], (n_load / C::kSlots - 1) & 1,
+        if (n_load >= C::kSlots && !mbar_wait_far(&empty[s], (n_load / C::kSlots - 1) & 1,
                                                    abort_flag, kWaitLimitNs)) {
           ok = false;
           return;
         }
         mbar_arrive_expect_tx_w(&full[s], C::kSlot);
-        if (lane < C::kPages) {
-#pragma unroll
-          for (int at = 0; at < C::kAtoms; ++at)
-            tma_load_4d(ring + s * C::kSlot + at * C::kAtom + lane * kPage * 128, map, &full[s],
-                        at * 64, it.h, 0, page);
-        }
+        if (lane < C::kPages)
+          tma_load_5d(ring + s * C::kSlot + lane * C::kPageBytes, map, &full[s], 0, 0, 0, it.h, page);
         __syncwarp();
         ++n_load;
       };
@@ -396,7 +441,7 @@ __global__ void __launch_bounds__(kThr, 1)
     }
   } else if (warp == kWarpIssuer) {
     // ============================================================ MMA issuer
-    constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, C::kKeys, false);
+    constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, C::kKeys / 2, false);
     constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, D, true);
     int n_load = 0;        // tiles of the ring before this item
     int jobs[2] = {0, 0};  // jobs of each S buffer so far
@@ -408,7 +453,7 @@ __global__ void __launch_bounds__(kThr, 1)
       const int J = two ? 2 * it.n : it.n;
       auto k_load = [&](int i) { return n_load + (i == 0 ? 0 : 2 * i - 1); };
       auto v_load = [&](int i) { return n_load + (i + 1 < it.n ? 2 * i + 2 : 2 * i + 1); };
-      if (!mbar_wait_warp(q_full, items & 1, abort_flag, kWaitLimitNs)) {
+      if (!mbar_wait_far(q_full, items & 1, abort_flag, kWaitLimitNs)) {
         ok = false;
         break;
       }
@@ -417,18 +462,19 @@ __global__ void __launch_bounds__(kThr, 1)
       auto issue_s = [&](int j) -> bool {
         const int i = two ? j / 2 : j, l = k_load(i), s = l % C::kSlots, buf = j & 1;
         if (!(two && (j & 1)) &&
-            !mbar_wait_warp(&full[s], (l / C::kSlots) & 1, abort_flag, kWaitLimitNs))
+            !mbar_wait_far(&full[s], (l / C::kSlots) & 1, abort_flag, kWaitLimitNs))
           return false;
         tc_fence_after_sync();
         const uint64_t dq =
             sdesc_sw128(smem_addr(smem + (two ? (j & 1) * C::kQTile : 0)), 16, 1024);
-        const uint64_t dk = sdesc_sw128(smem_addr(ring + s * C::kSlot), 16, 1024);
+        const uint64_t dk = sdesc_sw128(smem_addr(ring + s * C::kSlot), 16, C::kPageBytes);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t qo = static_cast<uint64_t>(((kk / 4) * C::kQAtom + (kk % 4) * 32) >> 4);
-          const uint64_t ko = static_cast<uint64_t>(((kk / 4) * C::kAtom + (kk % 4) * 32) >> 4);
-          mma_bf16_ss_w(tmem + buf * C::kKeys, dq + qo, dk + ko, idesc_s, kk > 0 ? 1u : 0u);
-        }
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int at = 0; at < C::kAtoms; ++at)
+            mma_ss_atom_w(tmem + buf * C::kKeys + half * (C::kKeys / 2),
+                          dq + at * (C::kQAtom >> 4),
+                          dk + ((half * 1024 + at * C::kPageAtom) >> 4), idesc_s, at > 0);
         mma_commit_w(&s_full[buf]);
         if (!two || (j & 1)) mma_commit_w(&empty[s]);
         if (j == J - 1) mma_commit_w(q_empty);
@@ -443,19 +489,19 @@ __global__ void __launch_bounds__(kThr, 1)
         // O += P V: P in the first half of its S buffer's columns, as bf16 pairs
         const int i = two ? j / 2 : j, l = v_load(i), s = l % C::kSlots, buf = j & 1;
         const int stream = C::kStreams == 2 ? buf : 0;
-        if (!mbar_wait_warp(&p_ready[buf], jobs[buf] & 1, abort_flag, kWaitLimitNs) ||
-            !mbar_wait_warp(&full[s], (l / C::kSlots) & 1, abort_flag, kWaitLimitNs)) {
+        if (!mbar_wait_far(&p_ready[buf], jobs[buf] & 1, abort_flag, kWaitLimitNs) ||
+            !mbar_wait_far(&full[s], (l / C::kSlots) & 1, abort_flag, kWaitLimitNs)) {
           ok = false;
           break;
         }
         ++jobs[buf];
         tc_fence_after_sync();
-        const uint64_t dv = sdesc_sw128(smem_addr(ring + s * C::kSlot), C::kAtom, 1024);
+        const uint64_t dv = sdesc_sw128(smem_addr(ring + s * C::kSlot), C::kPageAtom, 1024);
         const bool first = j < C::kStreams;  // the stream's first job of the item
 #pragma unroll
         for (int kk = 0; kk < C::kKeys / 16; ++kk)
           mma_bf16_ts_w(tmem + C::kColO + stream * D, tmem + buf * C::kKeys + 8 * kk,
-                        dv + kk * (2048 >> 4), idesc_o, (!first || kk > 0) ? 1u : 0u);
+                        dv + kk * (C::kPageBytes >> 4), idesc_o, (!first || kk > 0) ? 1u : 0u);
         mma_commit_w(&o_done[buf]);
         if (!two || (j & 1)) mma_commit_w(&empty[s]);
       }
@@ -480,7 +526,7 @@ __global__ void __launch_bounds__(kThr, 1)
       const bool two = split(it);
       const int J = two ? 2 * it.n : it.n;
       // ---- queries: rows 0-127 to Q tile 0, the others to tile 1 (16 bytes a step)
-      if (items > 0 && !mbar_wait_warp(q_empty, (items - 1) & 1, abort_flag, kWaitLimitNs)) {
+      if (items > 0 && !mbar_wait_far(q_empty, (items - 1) & 1, abort_flag, kWaitLimitNs)) {
         ok = false;
         break;
       }
@@ -518,7 +564,7 @@ __global__ void __launch_bounds__(kThr, 1)
       for (int j = C::kStreams == 2 ? stream : 0; j < J; j += C::kStreams) {
         const int buf = j & 1;
         const int i = two ? j / 2 : j;
-        if (!mbar_wait_warp(&s_full[buf], done[buf] & 1, abort_flag, kWaitLimitNs)) {
+        if (!mbar_wait_far(&s_full[buf], done[buf] & 1, abort_flag, kWaitLimitNs)) {
           ok = false;
           break;
         }
@@ -533,7 +579,7 @@ __global__ void __launch_bounds__(kThr, 1)
         if (ka + C::kKeys > lim_min) {
 #pragma unroll
           for (int c = 0; c < C::kKeys; ++c)
-            if (ka + c >= lim) x[c] = __float_as_uint(-INFINITY);
+            if (ka + key_of<C::kKeys>(c) >= lim) x[c] = __float_as_uint(-INFINITY);
         }
         float mx[8];
 #pragma unroll
@@ -550,7 +596,7 @@ __global__ void __launch_bounds__(kThr, 1)
             first ? m_run != -INFINITY : (m_run - m_used) * a.scale2 > kRescaleLog2;
         const bool resc = grow && !first;
         if (__any_sync(0xffffffffu, resc)) {
-          if (!mbar_wait_warp(&o_done[last], (done[last] - 1) & 1, abort_flag, kWaitLimitNs)) {
+          if (!mbar_wait_far(&o_done[last], (done[last] - 1) & 1, abort_flag, kWaitLimitNs)) {
             ok = false;
             break;
           }
@@ -573,24 +619,28 @@ __global__ void __launch_bounds__(kThr, 1)
         if (grow) m_used = m_run;
         const float nms = m_used == -INFINITY ? 0.f : -m_used * a.scale2;
         float sum0 = 0.f, sum1 = 0.f;
-        uint32_t pk[C::kKeys / 2];
 #pragma unroll
-        for (int e = 0; e < C::kKeys / 2; ++e) {
-          const float p0 = ex2_approx(fmaf(__uint_as_float(x[2 * e]), a.scale2, nms));
-          const float p1 = ex2_approx(fmaf(__uint_as_float(x[2 * e + 1]), a.scale2, nms));
-          if (e & 1)
-            sum1 += p0 + p1;
-          else
-            sum0 += p0 + p1;
-          pk[e] = pack_bf16x2(p0, p1);
+        for (int c = 0; c < C::kKeys / 2; c += 16) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            constexpr auto col = column_of<C::kKeys>;
+            const float p0 = ex2_approx(fmaf(__uint_as_float(x[col(2 * (c + e))]), a.scale2, nms));
+            const float p1 =
+                ex2_approx(fmaf(__uint_as_float(x[col(2 * (c + e) + 1)]), a.scale2, nms));
+            if (e & 1)
+              sum1 += p0 + p1;
+            else
+              sum0 += p0 + p1;
+            pk[e] = pack_bf16x2(p0, p1);
+          }
+          tmem_st_x16(tS + c, pk);
         }
         l += sum0 + sum1;
         // O sums P rounded to bf16, l the fp32 values: what the tile's largest lost leaves O's
         // normaliser too
         const float ptop = ex2_approx(fmaf(tmax, a.scale2, nms));
         corr += ptop - __uint_as_float(pack_bf16x2(0.f, ptop) & 0xffff0000u);
-#pragma unroll
-        for (int c = 0; c < C::kKeys / 64; ++c) tmem_st_x32(tS + 32 * c, pk + 32 * c);
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
@@ -601,7 +651,7 @@ __global__ void __launch_bounds__(kThr, 1)
       if (!ok) break;
       // ---- partial result: O / l and the log-sum-exp, rows of this stream
       if (last >= 0) {
-        if (!mbar_wait_warp(&o_done[last], (done[last] - 1) & 1, abort_flag, kWaitLimitNs)) {
+        if (!mbar_wait_far(&o_done[last], (done[last] - 1) & 1, abort_flag, kWaitLimitNs)) {
           ok = false;
           break;
         }
@@ -647,67 +697,124 @@ __global__ void __launch_bounds__(kThr, 1)
 }
 
 // ---------------------------------------------------------------- merge
-// One block for each (row, query head): the partial results of its group's prefix, CTA by
-// CTA, then those of its own pages, split by split.
+// A warp for each (row, query head): the partial results of its group's prefix, CTA by
+// CTA, then those of its own pages, split by split.  The log-sum-exps are read a lane
+// each, so that all outputs can be under way together (read one behind the other, 20
+// partial results took 25 us).
+constexpr int kMergeThreads = 256;
+
 template <int D>
-__global__ void __launch_bounds__(D)
-    attn_shared_merge_kernel(const SharedArgs a, const DecodeLaunch dec, int ctas) {
+__global__ void __launch_bounds__(kMergeThreads)
+    attn_shared_merge_kernel(const SharedArgs a, const DecodeLaunch dec) {
+  constexpr int kPer = D / 32;  // columns of a lane
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const size_t row = blockIdx.x;
-  const int b = static_cast<int>(row / a.Hq), hq = static_cast<int>(row % a.Hq);
-  const int t = threadIdx.x, S = dec.num_splits;
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  if (row >= a.B * a.Hq) return;
+  const int b = row / a.Hq, hq = row - b * a.Hq, S = dec.num_splits;
   const int g = a.group[b];
-  long long part = 0;
-  int c0 = 0, c1 = -1, streams = 1;
-  long long second = 0;  // distance of the second stream's partial result
-  if (g >= 0 && a.pages[g] > 0) {
+  const int pages = g >= 0 ? a.pages[g] : 0;
+  long long part = 0, second = 0;  // first partial result; distance of the second stream's
+  int c0 = 0, n_prefix = 0, streams = 1;
+  if (pages > 0) {
     const int e0 = a.cu_groups[g], pairs = (a.cu_groups[g + 1] - e0) * a.G;
-    const int pr = (a.entry[b] - e0) * a.G + hq % a.G, h = hq / a.G;
-    const int mt = pr / a.tile_rows, in = pr % a.tile_rows;
+    const int h = hq / a.G, pr = (a.entry[b] - e0) * a.G + hq - h * a.G;
+    const int mt = pr / a.tile_rows;
     const int rows = min(a.tile_rows, pairs - mt * a.tile_rows);
     const int mts = (pairs + a.tile_rows - 1) / a.tile_rows;
-    const int tiles = (a.pages[g] + a.tile_pages - 1) / a.tile_pages;
+    const int tiles = (pages + a.tile_pages - 1) / a.tile_pages;
     const long long u = a.base[g] + (static_cast<long long>(h) * mts + mt) * tiles;
-    const long long T = a.base[a.n_groups], C = min(T, static_cast<long long>(ctas));
-    c0 = static_cast<int>(((u + 1) * C - 1) / T);
-    c1 = static_cast<int>(((u + tiles) * C - 1) / T);
-    part = 2 * (static_cast<long long>(e0) * a.Hq + static_cast<long long>(h) * pairs +
-                mt * a.tile_rows) + in;
+    // the CTAs whose runs hold the item's units: runs that start at or before the first and
+    // the last of them
+    int first = 0, last = 0;
+#pragma unroll 1
+    for (int c = lane; c < a.ctas; c += 32) {
+      const long long start = a.runs[c];
+      const bool any = start < a.runs[c + 1];
+      first += any && start <= u;
+      last += any && start <= u + tiles - 1;
+    }
+    c0 = __reduce_add_sync(0xffffffffu, first) - 1;
+    n_prefix = __reduce_add_sync(0xffffffffu, last) - c0;
     if (D != 256 && rows <= kRows) {
       streams = 2;
       second = rows;
     }
+    part = 2 * (static_cast<long long>(e0) * a.Hq + static_cast<long long>(h) * pairs) +
+           2LL * mt * a.tile_rows + (pr - mt * a.tile_rows) +
+           static_cast<long long>(kItemRows) * c0;
+    n_prefix *= streams;
   }
-  const float* ls = dec.ws_lse + row * S;
+  const int n = n_prefix + S;
+  // partial result i: its log-sum-exp and output
+  auto prefix_row = [&](int i) -> long long {
+    return streams == 2 ? part + static_cast<long long>(kItemRows) * (i >> 1) + (i & 1) * second
+                        : part + static_cast<long long>(kItemRows) * i;
+  };
+  auto lse_of = [&](int i) -> float {
+    return i < n_prefix ? a.part_lse[prefix_row(i)]
+                        : dec.ws_lse[static_cast<long long>(row) * S + i - n_prefix];
+  };
   const float sg = dec.sink ? dec.sink[hq] : -INFINITY;
   float M = sg;
-  for (int c = c0; c <= c1; ++c)
-    for (int s = 0; s < streams; ++s)
-      M = fmaxf(M, a.part_lse[part + static_cast<long long>(kItemRows) * c + s * second]);
-  for (int s = 0; s < S; ++s) M = fmaxf(M, ls[s]);
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(dec.o);
-  if (M == -INFINITY) {
-    o[row * D + t] = __float2bfloat16(0.f);
-    if (dec.lse && t == 0) dec.lse[row] = -INFINITY;
-    return;
-  }
-  float wsum = (sg == -INFINITY) ? 0.f : expf(sg - M), acc = 0.f;
-  for (int c = c0; c <= c1; ++c)
-    for (int s = 0; s < streams; ++s) {
-      const long long p = part + static_cast<long long>(kItemRows) * c + s * second;
-      const float lp = a.part_lse[p];
-      if (lp == -INFINITY) continue;  // a part without a key: its O is not written
-      const float w = expf(lp - M);
+#pragma unroll 1
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, lse_of(i));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float acc[kPer], wsum = 0.f;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  if (M != -INFINITY) {
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      const float w = i < n ? expf(lse_of(i) - M) : 0.f;
+      const float* src = nullptr;
+      if (w > 0.f)  // (the output of a part without a key is not written)
+        src = i < n_prefix ? a.part_o + prefix_row(i) * D
+                           : dec.ws_o + (static_cast<long long>(row) * S + i - n_prefix) * D;
       wsum += w;
-      acc += w * a.part_o[p * D + t];
+      const int m = min(32, n - i0);
+#pragma unroll 4
+      for (int j = 0; j < m; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        const float* from = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), j));
+        if (from == nullptr) continue;
+        if constexpr (kPer == 2) {
+          const float2 v = reinterpret_cast<const float2*>(from)[lane];
+          acc[0] = fmaf(wj, v.x, acc[0]);
+          acc[1] = fmaf(wj, v.y, acc[1]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kPer; e += 4) {
+            const float4 v = reinterpret_cast<const float4*>(from)[lane * (kPer / 4) + e / 4];
+            acc[e] = fmaf(wj, v.x, acc[e]);
+            acc[e + 1] = fmaf(wj, v.y, acc[e + 1]);
+            acc[e + 2] = fmaf(wj, v.z, acc[e + 2]);
+            acc[e + 3] = fmaf(wj, v.w, acc[e + 3]);
+          }
+        }
+      }
     }
-  for (int s = 0; s < S; ++s) {
-    const float w = expf(ls[s] - M);
-    wsum += w;
-    acc += w * dec.ws_o[(row * S + s) * D + t];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
+    if (sg != -INFINITY) wsum += expf(sg - M);
   }
-  o[row * D + t] = __float2bfloat16(acc / wsum);
-  if (dec.lse && t == 0) dec.lse[row] = M + logf(wsum);
+  const bool seen = M != -INFINITY;
+  uint32_t out[kPer / 2];
+#pragma unroll
+  for (int e = 0; e < kPer / 2; ++e)
+    out[e] = seen ? pack_bf16x2(acc[2 * e] / wsum, acc[2 * e + 1] / wsum) : 0u;
+  uint32_t* o = reinterpret_cast<uint32_t*>(dec.o) +
+                static_cast<size_t>(row) * (D / 2) + lane * (kPer / 2);
+  if constexpr (kPer == 2)
+    o[0] = out[0];
+  else if constexpr (kPer == 4)
+    *reinterpret_cast<uint2*>(o) = make_uint2(out[0], out[1]);
+  else
+    *reinterpret_cast<uint4*>(o) = make_uint4(out[0], out[1], out[2], out[3]);
+  if (dec.lse && lane == 0) dec.lse[row] = seen ? M + logf(wsum) : -INFINITY;
 }
 
 template <typename... Params, typename... Args>
@@ -733,17 +840,19 @@ cudaError_t launch_shared(SharedArgs a, const DecodeLaunch& dec, int num_sms,
   using C = Cfg<D>;
   a.tile_rows = C::kTileRows;
   a.tile_pages = C::kPages;
+  a.ctas = std::min(num_sms, kSharedMaxCtas);
   static SharedMemoryLimit limit;
   cudaError_t e = limit.raise(attn_shared_prefix_kernel<D>, C::kSmem);
   if (e != cudaSuccess) return e;
   attn_shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int ctas = std::min(num_sms, kSharedMaxCtas);
-  e = launch_dependent(attn_shared_prefix_kernel<D>, dim3(ctas), kThr, C::kSmem, stream, dec.tmK,
-                       dec.tmV, a);
+  e = launch_dependent(attn_shared_prefix_kernel<D>, dim3(a.ctas), kThr, C::kSmem, stream, a.tmK,
+                       a.tmV, a);
   if (e != cudaSuccess) return e;
   if ((e = launch_attn_decode_own(dec, stream)) != cudaSuccess) return e;
-  return launch_dependent(attn_shared_merge_kernel<D>, dim3(a.B * a.Hq), D, 0, stream, a, dec, ctas);
+  const int blocks = (a.B * a.Hq + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
+  return launch_dependent(attn_shared_merge_kernel<D>, dim3(blocks), kMergeThreads, 0, stream, a,
+                          dec);
 }
 
 }  // namespace

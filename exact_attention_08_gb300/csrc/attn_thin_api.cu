@@ -119,7 +119,7 @@ SharedLayout shared_layout(int B, int Hq, int Hkv, int d, int n_groups, int n_ro
   l.part_o = pad16(attn_decode_workspace_size(B, Hq, d, num_splits));
   l.part_lse = l.part_o + rows * d * sizeof(float);
   l.base = pad16(l.part_lse + rows * sizeof(float));
-  l.ints = l.base + (static_cast<size_t>(n_groups) + 1) * sizeof(long long);
+  l.ints = l.base + (static_cast<size_t>(n_groups) + kSharedMaxCtas + 2) * sizeof(long long);
   l.bytes = l.ints + (2 * static_cast<size_t>(n_groups) + 4 * static_cast<size_t>(B)) * sizeof(int);
   return l;
 }
@@ -194,6 +194,7 @@ ATTN_API int attn_decode_paged_shared(const void* q, const void* k_pages, const 
   a.part_o = reinterpret_cast<float*>(ws + l.part_o);
   a.part_lse = reinterpret_cast<float*>(ws + l.part_lse);
   a.base = reinterpret_cast<long long*>(ws + l.base);
+  a.runs = a.base + n_groups + 1;
   a.pages = reinterpret_cast<int*>(ws + l.ints);
   a.source = a.pages + n_groups;
   a.entry = a.source + n_groups;
@@ -206,6 +207,9 @@ ATTN_API int attn_decode_paged_shared(const void* q, const void* k_pages, const 
   dec.start = a.start;
   int num_sms = 0;
   if ((rc = decode_maps(&dec, k_pages, v_pages, &num_sms)) != ATTN_OK) return rc;
+  if ((rc = whole_page_map(&a.tmK, k_pages, d, Hkv, num_pages_total, "k_pages")) != ATTN_OK ||
+      (rc = whole_page_map(&a.tmV, v_pages, d, Hkv, num_pages_total, "v_pages")) != ATTN_OK)
+    return rc;
   a.status = dec.status;
   const cudaError_t e = launch_attn_shared(a, dec, num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : cuda_error(e, "attn_decode_paged_shared launch");

@@ -151,6 +151,20 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, limit_ns));
 }
 
+// mbar_wait_warp with only the first test in line and the waiting itself out of line: a
+// role's loop with several waits then stays small (each in-line wait is about half a
+// kilobyte of code, and cold code costs its fetch).
+[[maybe_unused]] static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity,
+                                                   const volatile int* abort_flag,
+                                                   uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, limit_ns));
+}
+__device__ __forceinline__ bool mbar_wait_far(uint64_t* bar, uint32_t parity,
+                                              const volatile int* abort_flag, uint64_t limit_ns) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return mbar_wait_slow(bar, parity, abort_flag, limit_ns);
+}
+
 // 32-byte global store (sm_100 and later); the address must be 32-byte aligned.
 __device__ __forceinline__ void st_global_v8(void* ptr, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(v[0]),

@@ -189,12 +189,13 @@ struct SharedArgs {
   float scale, scale2;       // scale2: scale log2 e
   int tile_rows, tile_pages, ctas;  // set by the launcher
   // the plan
-  long long* base;  // [n_groups + 1] units before a group
+  long long* base;  // [n_groups] units before a group
   long long* runs;  // [kSharedMaxCtas + 1] first unit of a CTA
-  int* pages;       // [n_groups] pages that its rows share
-  int* source;      // [n_groups] the row whose table names them
+  int4* begin;      // [kSharedMaxCtas] where it stands: group, key head, query tile, key tile
+  int4* info;       // [n_groups] shared pages, first entry, (row, head) pairs, and the row
+                    // whose table names the pages
+  int4* rowinfo;    // [B] group (-1: none that shares pages) and first pair in it
   int* entry;       // [B] where the row stands in the list
-  int* group;       // [B] its group, -1: none
   int* start;       // [B] first page of its own
   int* order;       // [B] rows by own pages
   // partial results of the prefix

@@ -66,10 +66,10 @@ struct Cfg {
   static constexpr int kSlots = D == 64 ? 8 : 5;
   static constexpr int kOffRing = kStreams * kQTile;
   static constexpr int kOffBar = kOffRing + kSlots * kSlot;
-  // full, empty of the ring; s_full, p_ready, o_done [2]; q_full, q_empty; drain
-  static constexpr int kNumBars = 2 * kSlots + 6 + 2 + 1;
+  // full, empty of the ring; s_full, p_ready, o_done [2]; rows_full, q_full, q_empty; drain
+  static constexpr int kNumBars = 2 * kSlots + 6 + 3 + 1;
   static constexpr int kSmem = kOffBar + (kNumBars + 1) * 8 + 1024;
-  static_assert(kSmem <= 227 * 1024 - 512, "shared memory (512 bytes of it static)");
+  static_assert(kSmem + kItemRows * 4 + 16 <= 227 * 1024, "shared memory");
   static constexpr uint32_t kColO = 256;
 };
 
@@ -85,24 +85,26 @@ __device__ __forceinline__ constexpr int column_of(int k) {
 }
 
 // ---------------------------------------------------------------- plan
-// Workspace of a call (ints): see SharedArgs.  One block: rows to groups, the pages that
-// every group shares, units before each group, first own page of every row, and the
-// rows in the order of their own pages, longest first.
+// One block: rows to groups, the pages that every group shares, units before each group,
+// where each CTA of the prefix kernel begins, first own page of every row, and the rows in
+// the order of their own pages, longest first.  Steps that depend on one another, so
+// latency is all of it: what later kernels would have to work out again is written down
+// as records of 16 bytes.
 constexpr int kPlanThreads = 1024;
-constexpr int kBuckets = 4096;
+constexpr int kBuckets = kPlanThreads;
+constexpr int kEntries = 4096;  // rows whose list entries fit in shared memory
 
 __device__ __forceinline__ int row_length(const SharedArgs& a, int b) {
   const int L = a.seqlens[b];
   return max(0, min(L, a.max_pages * kPage));
 }
 
-// Item rows and units of a group of n rows that share `pages` pages.
-__device__ __forceinline__ long long group_units(const SharedArgs& a, int n, int pages) {
-  const long long tiles = (static_cast<long long>(n) * a.G + a.tile_rows - 1) / a.tile_rows;
-  return tiles * a.Hkv * ((pages + a.tile_pages - 1) / a.tile_pages);
-}
+__device__ __forceinline__ int ceil_div(int x, int y) { return (x + y - 1) / y; }
 
-__device__ __forceinline__ long long block_scan(long long v, long long* part, long long* total) {
+__device__ __noinline__ long long divide(long long x, long long y) { return x / y; }
+
+// Sum before this thread and over the block.
+__device__ __noinline__ long long block_scan(long long v, long long* part, long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long x = v;
 #pragma unroll
@@ -113,49 +115,48 @@ __device__ __forceinline__ long long block_scan(long long v, long long* part, lo
   __syncthreads();
   if (lane == 31) part[warp] = x;
   __syncthreads();
-  long long base = 0, all = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < warp) base += part[w];
-    all += part[w];
+  const long long p = part[lane];
+  long long sum = p;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += y;
   }
-  *total = all;
-  return base + x - v;
+  *total = __shfl_sync(0xffffffffu, sum, 31);
+  return __shfl_sync(0xffffffffu, sum - p, warp) + x - v;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const SharedArgs a) {
   __shared__ int s_cnt[kBuckets];
+  __shared__ int s_entry[kEntries];
   __shared__ long long s_part[kPlanThreads / 32];
-  __shared__ int s_bad;
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) s_bad = 0;
+  int* entry = a.B <= kEntries ? s_entry : a.entry;  // where a row stands in the list
 #pragma unroll 1
   for (int b = tid; b < a.B; b += kPlanThreads) {
-    a.entry[b] = INT_MAX;
+    entry[b] = INT_MAX;
     a.start[b] = 0;
-    a.group[b] = -1;
+    a.rowinfo[b] = make_int4(-1, 0, 0, 0);
   }
-#pragma unroll 1
-  for (int i = tid; i < kBuckets; i += kPlanThreads) s_cnt[i] = 0;
-  __syncthreads();
+  s_cnt[tid] = 0;
   // offsets that decrease or leave the list: no group is used
+  bool bad = false;
 #pragma unroll 1
   for (int g = tid; g <= a.n_groups; g += kPlanThreads) {
     const int c = a.cu_groups[g];
-    if (c < 0 || c > a.n_rows || (g > 0 && c < a.cu_groups[g - 1])) s_bad = 1;
+    bad |= c < 0 || c > a.n_rows || (g > 0 && c < a.cu_groups[g - 1]);
   }
-  __syncthreads();
-  const bool groups_ok = s_bad == 0;
-  if (!groups_ok && tid == 0) atomicOr(a.status, kStatusBadInput);
-  const int n_groups = groups_ok ? a.n_groups : 0;
+  bad = __syncthreads_or(bad);
+  if (bad && tid == 0) atomicOr(a.status, kStatusBadInput);
+  const int n_groups = bad ? 0 : a.n_groups;
   // a row listed more than once belongs where it stands first
   if (n_groups > 0) {
+    const int e1 = a.cu_groups[n_groups];
 #pragma unroll 1
-    for (int e = a.cu_groups[0] + tid; e < a.cu_groups[n_groups]; e += kPlanThreads) {
+    for (int e = a.cu_groups[0] + tid; e < e1; e += kPlanThreads) {
       const int b = a.rows ? a.rows[e] : e;
-      if (b < 0 || b >= a.B)
-        atomicOr(a.status, kStatusBadInput);
-      else if (atomicMin(&a.entry[b], e) != INT_MAX)
+      if (b < 0 || b >= a.B || atomicMin(&entry[b], e) != INT_MAX)
         atomicOr(a.status, kStatusBadInput);
     }
   }
@@ -163,101 +164,110 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
   // a warp for each group: its longest row, the pages it shares
 #pragma unroll 1
   for (int g = warp; g < n_groups; g += kPlanThreads / 32) {
-    const int e0 = a.cu_groups[g], e1 = a.cu_groups[g + 1];
+    const int e0 = a.cu_groups[g], e1 = a.cu_groups[g + 1], prefix = a.prefix_lens[g];
     int best = -1, at = INT_MAX, live = 0;
 #pragma unroll 1
     for (int e = e0 + lane; e < e1; e += 32) {
       const int b = a.rows ? a.rows[e] : e;
-      if (b < 0 || b >= a.B || a.entry[b] != e) continue;
+      if (b < 0 || b >= a.B || entry[b] != e) continue;
       ++live;
       const int L = row_length(a, b);
       if (L > best) best = L, at = b;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const int L = __shfl_xor_sync(0xffffffffu, best, o);
-      const int b = __shfl_xor_sync(0xffffffffu, at, o);
-      if (L > best || (L == best && b < at)) best = L, at = b;
-      live += __shfl_xor_sync(0xffffffffu, live, o);
-    }
-    const int prefix = a.prefix_lens[g];
+    const int longest = __reduce_max_sync(0xffffffffu, best);
+    at = __reduce_min_sync(0xffffffffu, best == longest ? at : INT_MAX);
+    live = __reduce_add_sync(0xffffffffu, live);
     if (lane == 0 && (prefix < 0 || prefix > a.max_pages * kPage))
       atomicOr(a.status, kStatusBadInput);
     // a group of one shares nothing: its row is done by the split decode alone
-    int pages = live < 2 || prefix < 0 ? 0 : min(prefix, best) / kPage;
-    if (lane == 0) {
-      a.pages[g] = pages;
-      a.source[g] = at;
-    }
+    const int pages = live < 2 || prefix < 0 ? 0 : min(prefix, longest) / kPage;
+    if (lane == 0) a.info[g] = make_int4(pages, e0, (e1 - e0) * a.G, at);
 #pragma unroll 1
     for (int e = e0 + lane; e < e1; e += 32) {
       const int b = a.rows ? a.rows[e] : e;
-      if (b < 0 || b >= a.B || a.entry[b] != e) continue;
+      if (b < 0 || b >= a.B || entry[b] != e) continue;
       a.start[b] = min(pages, (row_length(a, b) + kPage - 1) / kPage);
-      a.group[b] = g;
+      if (pages > 0) a.rowinfo[b] = make_int4(g, (e - e0) * a.G, 0, 0);
     }
   }
   __syncthreads();
-  // units before each group
-  {
-    long long base = 0;
-#pragma unroll 1
-    for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
-      const int g = g0 + tid;
-      const long long v = g < n_groups ? group_units(a, a.cu_groups[g + 1] - a.cu_groups[g],
-                                                     a.pages[g])
-                                       : 0;
-      long long all;
-      const long long before = block_scan(v, s_part, &all);
-      if (g < n_groups) a.base[g] = base + before;
-      base += all;
-    }
-    if (tid == 0) a.base[a.n_groups] = base;
-    // with fewer units than CTAs the last CTAs have none, the others one each
-    const long long n = min(base, static_cast<long long>(a.ctas));
-#pragma unroll 1
-    for (int c = tid; c <= a.ctas; c += kPlanThreads) a.runs[c] = c < n ? base * c / n : base;
-    // a list that is not used: every group ends where it begins
-    if (n_groups == 0)
-#pragma unroll 1
-      for (int g = tid; g < a.n_groups; g += kPlanThreads) a.base[g] = 0;
-  }
-  // rows by own pages, longest first (a counting sort; rows of one bucket in any order,
-  // which only says which CTA runs first)
-  const int nb = min(a.max_pages + 1, kBuckets);
+  // rows by own pages, longest first (a counting sort, of several page counts a bucket where
+  // there are more than buckets; rows of one bucket in any order, which only says which
+  // CTA runs first)
+  const int shift = max(0, 32 - __clz(a.max_pages) - 10);
   auto bucket = [&](int b) {
-    const int own = (row_length(a, b) + kPage - 1) / kPage - a.start[b];
-    const long long k = static_cast<long long>(a.max_pages - own) * nb / (a.max_pages + 1);
-    return static_cast<int>(k < nb - 1 ? k : nb - 1);
+    return (a.max_pages - ((row_length(a, b) + kPage - 1) / kPage - a.start[b])) >> shift;
   };
+  const bool one = a.B <= kPlanThreads;  // a thread a row
+  const int mine = one && tid < a.B ? min(bucket(tid), kBuckets - 1) : 0;
+  if (one) {
+    if (tid < a.B) atomicAdd(&s_cnt[mine], 1);
+  } else {
 #pragma unroll 1
-  for (int b = tid; b < a.B; b += kPlanThreads) atomicAdd(&s_cnt[bucket(b)], 1);
-  __syncthreads();
-  constexpr int kPer = kBuckets / kPlanThreads;
-  int local[kPer], run = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    local[j] = run;
-    run += s_cnt[tid * kPer + j];
+    for (int b = tid; b < a.B; b += kPlanThreads) atomicAdd(&s_cnt[min(bucket(b), kBuckets - 1)], 1);
   }
-  long long all;
-  const int before = static_cast<int>(block_scan(run, s_part, &all));
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) s_cnt[tid * kPer + j] = before + local[j];
-  __syncthreads();
+  // units before each group
+  long long units = 0;
 #pragma unroll 1
-  for (int b = tid; b < a.B; b += kPlanThreads) a.order[atomicAdd(&s_cnt[bucket(b)], 1)] = b;
+  for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
+    const int g = g0 + tid;
+    long long v = 0, all;
+    if (g < n_groups) {
+      const int4 info = a.info[g];
+      v = static_cast<long long>(ceil_div(info.z, a.tile_rows)) * a.Hkv *
+          ceil_div(info.x, a.tile_pages);
+    }
+    const long long before = block_scan(v, s_part, &all);
+    if (g < n_groups) a.base[g] = units + before;
+    units += all;
+  }
+  __syncthreads();
+  long long all;
+  const int before = static_cast<int>(block_scan(s_cnt[tid], s_part, &all));
+  __syncthreads();
+  s_cnt[tid] = before;
+  __syncthreads();
+  if (one) {
+    if (tid < a.B) a.order[atomicAdd(&s_cnt[mine], 1)] = tid;
+  } else {
+#pragma unroll 1
+    for (int b = tid; b < a.B; b += kPlanThreads)
+      a.order[atomicAdd(&s_cnt[min(bucket(b), kBuckets - 1)], 1)] = b;
+  }
+  // where each CTA begins; with fewer units than CTAs the last CTAs have none, the others one
+  if (tid <= a.ctas) {
+    const long long n = min(units, static_cast<long long>(a.ctas));
+    const long long at = tid < n ? divide(units * tid, n) : units;
+    a.runs[tid] = at;
+    if (at < units) {
+      int lo = 0, hi = n_groups - 1;  // the last group with base <= at
+#pragma unroll 1
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (a.base[mid] <= at)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const int4 info = a.info[lo];
+      const int tiles = ceil_div(info.x, a.tile_pages), mts = ceil_div(info.z, a.tile_rows);
+      const long long in = at - a.base[lo];
+      const int item = static_cast<int>(divide(in, tiles));
+      a.begin[tid] = make_int4(lo, item / mts, item % mts,
+                               static_cast<int>(in - static_cast<long long>(item) * tiles));
+    }
+  }
 }
 
 // ---------------------------------------------------------------- items
 // One item of the prefix work and this CTA's part of it.
 struct Item {
-  int g, h;               // group, key head
+  int h;                  // key head
   int kt, n;              // first key tile of this CTA's part, key tiles in it
   int rows;               // (row, head) pairs of the item
   int row0;               // its first pair among the group's
   int first;              // the group's first list entry
+  int source;             // the row whose table names the prefix's pages
   int keys;               // keys of the prefix
   long long part;         // first row of its partial results
 };
@@ -266,46 +276,33 @@ struct Item {
 struct Walk {
   long long left;
   int g, h, mt, kt;
+  int4 info;  // of group g
 };
 
-__device__ __forceinline__ int ceil_div(int x, int y) { return (x + y - 1) / y; }
-
-// Where unit `at` stands.
-__device__ __noinline__ void walk_begin(const SharedArgs& a, Walk& w, long long at) {
-  int lo = 0, hi = a.n_groups;  // the last group with base <= at
-#pragma unroll 1
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (a.base[mid] <= at)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  w.g = lo;
+__device__ __forceinline__ void walk_begin(const SharedArgs& a, Walk& w) {
+  const long long at = a.runs[blockIdx.x];
+  const int4 begin = a.begin[blockIdx.x];
+  w.left = a.runs[blockIdx.x + 1] - at;
   if (w.left <= 0) return;
-  const int tiles = ceil_div(a.pages[lo], a.tile_pages);
-  const int mts = ceil_div((a.cu_groups[lo + 1] - a.cu_groups[lo]) * a.G, a.tile_rows);
-  const long long in = at - a.base[lo];
-  const int item = static_cast<int>(in / tiles);
-  w.kt = static_cast<int>(in % tiles);
-  w.h = item / mts;
-  w.mt = item % mts;
+  w.g = begin.x;
+  w.h = begin.y;
+  w.mt = begin.z;
+  w.kt = begin.w;
+  w.info = a.info[w.g];
 }
 
-__device__ __noinline__ bool walk_next(const SharedArgs& a, Walk& w, Item& it) {
+__device__ __forceinline__ bool walk_next(const SharedArgs& a, Walk& w, Item& it) {
   if (w.left <= 0) return false;
 #pragma unroll 1
-  while (a.pages[w.g] == 0) ++w.g;  // a group with pages is behind, or nothing were left
-  const int pages = a.pages[w.g], e0 = a.cu_groups[w.g];
-  const int pairs = (a.cu_groups[w.g + 1] - e0) * a.G;
-  const int tiles = (pages + a.tile_pages - 1) / a.tile_pages;
-  it.g = w.g;
+  while (w.info.x == 0) w.info = a.info[++w.g];  // (a group with pages follows: units are left)
+  const int pages = w.info.x, e0 = w.info.y, pairs = w.info.z;
   it.h = w.h;
   it.kt = w.kt;
-  it.n = static_cast<int>(min(static_cast<long long>(tiles - w.kt), w.left));
+  it.n = static_cast<int>(min(static_cast<long long>(ceil_div(pages, a.tile_pages) - w.kt), w.left));
   it.row0 = w.mt * a.tile_rows;
   it.rows = min(a.tile_rows, pairs - it.row0);
   it.first = e0;
+  it.source = w.info.w;
   it.keys = pages * kPage;
   it.part = 2 * (static_cast<long long>(e0) * a.Hq + static_cast<long long>(w.h) * pairs + it.row0) +
             static_cast<long long>(kItemRows) * blockIdx.x;
@@ -317,7 +314,7 @@ __device__ __noinline__ bool walk_next(const SharedArgs& a, Walk& w, Item& it) {
     w.mt = 0;
     if (++w.h == a.Hkv) {
       w.h = 0;
-      ++w.g;
+      if (w.left > 0) w.info = a.info[++w.g];
     }
   }
   return true;
@@ -329,6 +326,7 @@ __global__ void __launch_bounds__(kThr, 1)
                               const __grid_constant__ CUtensorMap tmV, const SharedArgs a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ int s_row[kItemRows];  // rows of q of an item's pairs
   __shared__ int abort_s;
   uint8_t* smem = smem_align1024(smem_raw);
   uint8_t* ring = smem + C::kOffRing;
@@ -337,7 +335,8 @@ __global__ void __launch_bounds__(kThr, 1)
   uint64_t* s_full = empty + C::kSlots;  // [S buffer]
   uint64_t* p_ready = s_full + 2;        // [S buffer]
   uint64_t* o_done = p_ready + 2;        // [S buffer] O += P V of that buffer's P
-  uint64_t* q_full = o_done + 2;
+  uint64_t* rows_full = o_done + 2;
+  uint64_t* q_full = rows_full + 1;
   uint64_t* q_empty = q_full + 1;
   uint64_t* drain = q_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -354,6 +353,7 @@ __global__ void __launch_bounds__(kThr, 1)
       mbar_init(&p_ready[i], 4);
       mbar_init(&o_done[i], 1);
     }
+    mbar_init(rows_full, 8);
     mbar_init(q_full, 8);
     mbar_init(q_empty, 1);
     mbar_init(drain, 1);
@@ -374,11 +374,7 @@ __global__ void __launch_bounds__(kThr, 1)
   const uint32_t tmem = *tmem_slot;
 
   Walk w;
-  {
-    const long long at = a.runs[blockIdx.x];
-    w.left = a.runs[blockIdx.x + 1] - at;
-    walk_begin(a, w, at);
-  }
+  walk_begin(a, w);
   // An item's jobs, in order: S buffer and, with two streams, stream j % 2.  With a tile in
   // both streams job j is key tile j / 2, else key tile j.
   auto split = [&](const Item& it) { return C::kStreams == 2 && it.rows > kRows; };
@@ -389,7 +385,7 @@ __global__ void __launch_bounds__(kThr, 1)
     int n_load = 0;
     bool ok = true;
     while (ok && walk_next(a, w, it)) {
-      const int* row = a.page_table + static_cast<size_t>(a.source[it.g]) * a.max_pages;
+      const int* row = a.page_table + static_cast<size_t>(it.source) * a.max_pages;
       const int pages = it.keys / kPage;
       auto lookup = [&](int i) -> int {  // page of lane l of the part's key tile i
         if (i >= it.n || lane >= C::kPages) return 0;
@@ -525,39 +521,62 @@ __global__ void __launch_bounds__(kThr, 1)
     while (ok && walk_next(a, w, it)) {
       const bool two = split(it);
       const int J = two ? 2 * it.n : it.n;
-      // ---- queries: rows 0-127 to Q tile 0, the others to tile 1 (16 bytes a step)
+      // ---- queries: rows 0-127 to Q tile 0, the others to tile 1
       if (items > 0 && !mbar_wait_far(q_empty, (items - 1) & 1, abort_flag, kWaitLimitNs)) {
         ok = false;
         break;
       }
-      for (int x = tid; x < (two ? 2 : 1) * kRows * (D / 8); x += 256) {
-        const int pr = x / (D / 8), c = x % (D / 8);  // row of the item, 16-byte chunk
-        uint4 v = make_uint4(0, 0, 0, 0);
+      // This thread's pair, its row of q and the keys it sees (both streams' threads work out the
+      // same pairs where they share a tile).  The queries then come eight 16-byte chunks at
+      // a time: one by one, each behind its row's index, they took 15 us an item.
+      const int pr = two ? tid : r;
+      int lim = 0;
+      {
+        int row = -1;
         if (pr < it.rows) {
-          const int e = it.first + (it.row0 + pr) / a.G;
-          const int b = a.rows ? a.rows[e] : e;
-          if (b >= 0 && b < a.B)
-            v = *reinterpret_cast<const uint4*>(
-                a.q + (static_cast<size_t>(b) * a.Hq + it.h * a.G + (it.row0 + pr) % a.G) * D +
-                c * 8);
+          const int pair = it.row0 + pr, member = pair / a.G;
+          const int b = a.rows ? a.rows[it.first + member] : it.first + member;
+          if (b >= 0 && b < a.B) {
+            row = b * a.Hq + it.h * a.G + pair - member * a.G;
+            lim = min(row_length(a, b), it.keys);
+          }
         }
-        const int row = pr % kRows;
-        *reinterpret_cast<uint4*>(smem + (pr / kRows) * C::kQTile + (c / 8) * C::kQAtom +
-                                  row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+        s_row[pr] = row;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(rows_full);
+      if (!mbar_wait_far(rows_full, items & 1, abort_flag, kWaitLimitNs)) {
+        ok = false;
+        break;
+      }
+      {
+        constexpr int kChunks = D / 8, kStep = 256 / kChunks;
+        const int c = tid % kChunks, rows = two ? kItemRows : kRows;
+        const uint32_t dst = (c / 8) * C::kQAtom;
+#pragma unroll 1
+        for (int r0 = tid / kChunks; r0 < rows; r0 += 8 * kStep) {
+          uint4 v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int row = r0 + j * kStep, q = row < rows ? s_row[row] : -1;
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (q >= 0)
+              v[j] = *reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(q) * D + c * 8);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int row = r0 + j * kStep;
+            if (row >= rows) break;
+            *reinterpret_cast<uint4*>(smem + (row / kRows) * C::kQTile + dst +
+                                      (row % kRows) * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[j];
+          }
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
       ++items;
       if (stream >= C::kStreams) continue;  // d = 256: the other warps only load queries
-      // ---- this thread's pair and the keys it sees
-      const int pr = two ? stream * kRows + r : r;
-      int lim = 0;
-      if (pr < it.rows) {
-        const int e = it.first + (it.row0 + pr) / a.G;
-        const int b = a.rows ? a.rows[e] : e;
-        if (b >= 0 && b < a.B) lim = min(row_length(a, b), it.keys);
-      }
       const int lim_min = __reduce_min_sync(0xffffffffu, pr < it.rows ? lim : INT_MAX);
       float m_run = -INFINITY, m_used = -INFINITY, l = 0.f, corr = 0.f;
       int last = -1;  // S buffer of this stream's last job
@@ -697,7 +716,7 @@ __global__ void __launch_bounds__(kThr, 1)
 }
 
 // ---------------------------------------------------------------- merge
-// A warp for each (row, query head): the partial results of its group's prefix, CTA by
+// A warp for each (row, query head), two at d = 256: the partial results of its group's prefix, CTA by
 // CTA, then those of its own pages, split by split.  The log-sum-exps are read a lane
 // each, so that all outputs can be under way together (read one behind the other, 20
 // partial results took 25 us).
@@ -706,33 +725,38 @@ constexpr int kMergeThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
     attn_shared_merge_kernel(const SharedArgs a, const DecodeLaunch dec) {
-  constexpr int kPer = D / 32;  // columns of a lane
+  constexpr int kWarps = D == 256 ? 2 : 1;  // warps of a row: 128 columns each at most
+  constexpr int kPer = D / 32 / kWarps;      // columns of a lane
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  const int unit = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  const int row = unit / kWarps, column = unit % kWarps * 128;
   if (row >= a.B * a.Hq) return;
   const int b = row / a.Hq, hq = row - b * a.Hq, S = dec.num_splits;
-  const int g = a.group[b];
-  const int pages = g >= 0 ? a.pages[g] : 0;
+  const int4 info = a.rowinfo[b];  // group (-1: none that shares pages), first pair
+  long long runs[kSharedMaxCtas / 32 + 1];  // this lane's CTAs, and the one behind each
+#pragma unroll
+  for (int i = 0; i <= kSharedMaxCtas / 32; ++i) {
+    const int c = i * 32 + lane;
+    runs[i] = c <= a.ctas ? a.runs[c] : LLONG_MAX;
+  }
   long long part = 0, second = 0;  // first partial result; distance of the second stream's
   int c0 = 0, n_prefix = 0, streams = 1;
-  if (pages > 0) {
-    const int e0 = a.cu_groups[g], pairs = (a.cu_groups[g + 1] - e0) * a.G;
-    const int h = hq / a.G, pr = (a.entry[b] - e0) * a.G + hq - h * a.G;
+  if (info.x >= 0) {
+    const int4 group = a.info[info.x];
+    const int e0 = group.y, pairs = group.z;
+    const int h = hq / a.G, pr = info.y + hq - h * a.G;
     const int mt = pr / a.tile_rows;
     const int rows = min(a.tile_rows, pairs - mt * a.tile_rows);
-    const int mts = (pairs + a.tile_rows - 1) / a.tile_rows;
-    const int tiles = (pages + a.tile_pages - 1) / a.tile_pages;
-    const long long u = a.base[g] + (static_cast<long long>(h) * mts + mt) * tiles;
+    const int mts = ceil_div(pairs, a.tile_rows), tiles = ceil_div(group.x, a.tile_pages);
+    const long long u = a.base[info.x] + (static_cast<long long>(h) * mts + mt) * tiles;
     // the CTAs whose runs hold the item's units: runs that start at or before the first and
-    // the last of them
+    // the last of them (those without units start past all)
     int first = 0, last = 0;
-#pragma unroll 1
-    for (int c = lane; c < a.ctas; c += 32) {
-      const long long start = a.runs[c];
-      const bool any = start < a.runs[c + 1];
-      first += any && start <= u;
-      last += any && start <= u + tiles - 1;
+#pragma unroll
+    for (int i = 0; i <= kSharedMaxCtas / 32; ++i) {
+      first += runs[i] <= u;
+      last += runs[i] <= u + tiles - 1;
     }
     c0 = __reduce_add_sync(0xffffffffu, first) - 1;
     n_prefix = __reduce_add_sync(0xffffffffu, last) - c0;
@@ -774,8 +798,9 @@ __global__ void __launch_bounds__(kMergeThreads)
         src = i < n_prefix ? a.part_o + prefix_row(i) * D
                            : dec.ws_o + (static_cast<long long>(row) * S + i - n_prefix) * D;
       wsum += w;
+      if (src != nullptr) src += column;
       const int m = min(32, n - i0);
-#pragma unroll 4
+#pragma unroll 8
       for (int j = 0; j < m; ++j) {
         const float wj = __shfl_sync(0xffffffffu, w, j);
         const float* from = reinterpret_cast<const float*>(
@@ -786,14 +811,11 @@ __global__ void __launch_bounds__(kMergeThreads)
           acc[0] = fmaf(wj, v.x, acc[0]);
           acc[1] = fmaf(wj, v.y, acc[1]);
         } else {
-#pragma unroll
-          for (int e = 0; e < kPer; e += 4) {
-            const float4 v = reinterpret_cast<const float4*>(from)[lane * (kPer / 4) + e / 4];
-            acc[e] = fmaf(wj, v.x, acc[e]);
-            acc[e + 1] = fmaf(wj, v.y, acc[e + 1]);
-            acc[e + 2] = fmaf(wj, v.z, acc[e + 2]);
-            acc[e + 3] = fmaf(wj, v.w, acc[e + 3]);
-          }
+          const float4 v = reinterpret_cast<const float4*>(from)[lane];
+          acc[0] = fmaf(wj, v.x, acc[0]);
+          acc[1] = fmaf(wj, v.y, acc[1]);
+          acc[2] = fmaf(wj, v.z, acc[2]);
+          acc[3] = fmaf(wj, v.w, acc[3]);
         }
       }
     }
@@ -807,14 +829,12 @@ __global__ void __launch_bounds__(kMergeThreads)
   for (int e = 0; e < kPer / 2; ++e)
     out[e] = seen ? pack_bf16x2(acc[2 * e] / wsum, acc[2 * e + 1] / wsum) : 0u;
   uint32_t* o = reinterpret_cast<uint32_t*>(dec.o) +
-                static_cast<size_t>(row) * (D / 2) + lane * (kPer / 2);
+                static_cast<size_t>(row) * (D / 2) + column / 2 + lane * (kPer / 2);
   if constexpr (kPer == 2)
     o[0] = out[0];
-  else if constexpr (kPer == 4)
-    *reinterpret_cast<uint2*>(o) = make_uint2(out[0], out[1]);
   else
-    *reinterpret_cast<uint4*>(o) = make_uint4(out[0], out[1], out[2], out[3]);
-  if (dec.lse && lane == 0) dec.lse[row] = seen ? M + logf(wsum) : -INFINITY;
+    *reinterpret_cast<uint2*>(o) = make_uint2(out[0], out[1]);
+  if (dec.lse && lane == 0 && column == 0) dec.lse[row] = seen ? M + logf(wsum) : -INFINITY;
 }
 
 template <typename... Params, typename... Args>
@@ -850,7 +870,8 @@ cudaError_t launch_shared(SharedArgs a, const DecodeLaunch& dec, int num_sms,
                        a.tmV, a);
   if (e != cudaSuccess) return e;
   if ((e = launch_attn_decode_own(dec, stream)) != cudaSuccess) return e;
-  const int blocks = (a.B * a.Hq + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
+  const int per = kMergeThreads / 32 / (D == 256 ? 2 : 1);  // rows of a block
+  const int blocks = (a.B * a.Hq + per - 1) / per;
   return launch_dependent(attn_shared_merge_kernel<D>, dim3(blocks), kMergeThreads, 0, stream, a,
                           dec);
 }

@@ -108,19 +108,19 @@ size_t mass_plan_bytes(int B, size_t kt) {
 
 // Workspace of attn_decode_paged_shared, in bytes from its start.
 struct SharedLayout {
-  size_t decode, base, ints, part_lse, part_o, bytes;
+  size_t part_o, part_lse, begin, base, ints, bytes;
 };
 
 SharedLayout shared_layout(int B, int Hq, int Hkv, int d, int n_groups, int n_rows, int max_pages,
                            int num_splits) {
   SharedLayout l;
   const size_t rows = shared_part_rows(Hq, Hkv, d, n_groups, n_rows, max_pages);
-  l.decode = 0;
   l.part_o = pad16(attn_decode_workspace_size(B, Hq, d, num_splits));
   l.part_lse = l.part_o + rows * d * sizeof(float);
-  l.base = pad16(l.part_lse + rows * sizeof(float));
-  l.ints = l.base + (static_cast<size_t>(n_groups) + kSharedMaxCtas + 2) * sizeof(long long);
-  l.bytes = l.ints + (2 * static_cast<size_t>(n_groups) + 4 * static_cast<size_t>(B)) * sizeof(int);
+  l.begin = pad16(l.part_lse + rows * sizeof(float));
+  l.base = l.begin + (kSharedMaxCtas + 1 + static_cast<size_t>(n_groups) + B) * sizeof(int4);
+  l.ints = l.base + (static_cast<size_t>(n_groups) + kSharedMaxCtas + 1) * sizeof(long long);
+  l.bytes = l.ints + 3 * static_cast<size_t>(B) * sizeof(int);
   return l;
 }
 
@@ -193,13 +193,13 @@ ATTN_API int attn_decode_paged_shared(const void* q, const void* k_pages, const 
   a.scale2 = scale * 1.4426950408889634f;
   a.part_o = reinterpret_cast<float*>(ws + l.part_o);
   a.part_lse = reinterpret_cast<float*>(ws + l.part_lse);
+  a.begin = reinterpret_cast<int4*>(ws + l.begin);
+  a.info = a.begin + kSharedMaxCtas + 1;
+  a.rowinfo = a.info + n_groups;
   a.base = reinterpret_cast<long long*>(ws + l.base);
-  a.runs = a.base + n_groups + 1;
-  a.pages = reinterpret_cast<int*>(ws + l.ints);
-  a.source = a.pages + n_groups;
-  a.entry = a.source + n_groups;
-  a.group = a.entry + B;
-  a.start = a.group + B;
+  a.runs = a.base + n_groups;
+  a.entry = reinterpret_cast<int*>(ws + l.ints);
+  a.start = a.entry + B;
   a.order = a.start + B;
   dec.ws_o = reinterpret_cast<float*>(ws);
   dec.ws_lse = dec.ws_o + rows * d;

@@ -949,6 +949,9 @@ def attn_pages_compact(page_table, seqlens, refs, k_pages, v_pages, *, workspace
 
 
 # ---------------------------------------------------------------- shared and thinned caches
+# As above: one expression checks what all calls have in common, and which part of it
+# failed is worked out by _explain.  Sizes that a 32-bit int does not hold become
+# ones that the library refuses.
 
 def _contiguous(t, name, dtype, index):
     torch = _torch()
@@ -958,34 +961,58 @@ def _contiguous(t, name, dtype, index):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{index}")
 
 
-def _paged_rows(page_table, seqlens, index):
-    """(B, max_pages)"""
-    _int_tensor(page_table, "page_table", index)
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    B, W = page_table.shape
-    _int_vector(seqlens, "seqlens", B, index)
-    return B, W
-
-
-def _pool(q, k_pages, v_pages, index):
-    """(P, page size, Hkv) of pools that fit q [.., Hq, d]."""
+def _explain(q, k_pages, v_pages, page_table, seqlens):
     torch = _torch()
+    index = q.get_device() if isinstance(q, torch.Tensor) else -1
+    _contiguous(q, "q", torch.bfloat16, index)
+    if q.dim() != 3:
+        raise ValueError("q must have 3 dimensions: rows, heads, d")
     _contiguous(k_pages, "k_pages", torch.bfloat16, index)
     if v_pages is not None:
         _contiguous(v_pages, "v_pages", torch.bfloat16, index)
-    shape = k_pages.shape
-    if len(shape) != 4 or (v_pages is not None and v_pages.shape != shape) or \
-            shape[3] != q.shape[-1]:
+    if k_pages.dim() != 4 or (v_pages is not None and v_pages.shape != k_pages.shape) or \
+            k_pages.shape[3] != q.shape[-1]:
         raise ValueError("k_pages/v_pages shapes disagree with q")
-    return shape[0], shape[1], shape[2]
+    _int_tensor(page_table, "page_table", index)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    _int_vector(seqlens, "seqlens", page_table.shape[0], index)
+    raise ValueError("q, pools, page_table and seqlens do not fit together")
+
+
+def _paged(q, k_pages, v_pages, page_table, seqlens):
+    """(device index, rows of q, Hq, d, P, page size, Hkv, B, max_pages)"""
+    torch = _torch_module or _torch()
+    bf16, i32 = torch.bfloat16, torch.int32
+    try:
+        index = q.get_device()
+        N, Hq, d = q.shape
+        pool = k_pages.shape
+        P, page, Hkv, dk = pool
+        B, W = page_table.shape
+        fine = (index >= 0 and dk == d and q.dtype is bf16 and k_pages.dtype is bf16 and
+                page_table.dtype is i32 and seqlens.dtype is i32 and
+                k_pages.get_device() == index and page_table.get_device() == index and
+                seqlens.get_device() == index and q.is_contiguous() and
+                k_pages.is_contiguous() and page_table.is_contiguous() and
+                seqlens.is_contiguous() and seqlens.shape == (B,) and
+                (v_pages is None or
+                 (v_pages.dtype is bf16 and v_pages.get_device() == index and
+                  v_pages.is_contiguous() and v_pages.shape == pool)))
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        _explain(q, k_pages, v_pages, page_table, seqlens)
+    if P > _INT_MAX or B > _INT_MAX or W > _INT_MAX or N > _INT_MAX or Hq > _INT_MAX:
+        N, Hq, P, B, W = map(_c_int, (N, Hq, P, B, W))
+    return index, N, Hq, d, P, page, Hkv, B, W
 
 
 def _bytes(n, index, workspace):
     """A workspace of n bytes, or the caller's."""
-    torch = _torch()
+    torch = _torch_module
     if workspace is None:
-        return torch.empty(max(n, 16), dtype=torch.uint8, device=torch.device("cuda", index))
+        return torch.empty_like(_vector_like(n if n > 16 else 16, torch.uint8, index))
     if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or \
             workspace.get_device() != index:
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
@@ -993,7 +1020,7 @@ def _bytes(n, index, workspace):
 
 
 def _decode_outputs(q, o, lse, want_lse, index):
-    torch = _torch()
+    torch = _torch_module
     if o is None:
         o = torch.empty_like(q)
     else:
@@ -1019,17 +1046,20 @@ def _sink(sink_logit, Hq, index):
     return sink_logit.data_ptr()
 
 
-def _mass_tensors(mass, mass_out, positions, last_positions, B, Hkv, index):
+def _masses(mass, mass_out, positions, last_positions, B, Hkv, index):
     """(mass_out, slots)"""
-    torch = _torch()
-    _contiguous(mass, "mass", torch.float32, index)
+    torch = _torch_module
+    f32 = torch.float32
+    if not isinstance(mass, torch.Tensor) or mass.dtype is not f32 or \
+            mass.get_device() != index or not mass.is_contiguous():
+        _contiguous(mass, "mass", f32, index)
     shape = mass.shape
     if len(shape) != 3 or shape[0] != B or shape[1] != Hkv:
         raise ValueError(f"mass must be [{B}, {Hkv}, slots], got {list(shape)}")
     if mass_out is None:
         mass_out = mass
-    else:
-        _contiguous(mass_out, "mass_out", torch.float32, index)
+    elif mass_out is not mass:
+        _contiguous(mass_out, "mass_out", f32, index)
         if mass_out.shape != shape:
             raise ValueError("mass_out must be shaped like mass")
     if positions is not None:
@@ -1038,7 +1068,7 @@ def _mass_tensors(mass, mass_out, positions, last_positions, B, Hkv, index):
             raise ValueError("positions must be shaped like mass")
     if last_positions is not None:
         _int_vector(last_positions, "last_positions", B, index)
-    return mass_out, shape[2]
+    return mass_out, _c_int(shape[2])
 
 
 @functools.lru_cache(maxsize=256)
@@ -1055,27 +1085,23 @@ def attn_decode_paged_shared(q, k_pages, v_pages, page_table, seqlens, cu_groups
     """attn_decode_paged (with sink_logit: attn_decode_paged_sink) for rows that share leading
     pages, whose keys are read once a group.  Group g is rows group_rows[cu_groups[g]:
     cu_groups[g+1]] (int32; None: the rows in order), which share the whole pages of their
-    first prefix_lens[g] tokens (int32).  Rows in no group are decoded by themselves.
-    num_splits: splits of each row's own keys (None: enough to fill the GPU) -> (o, lse)."""
-    torch = _torch()
-    index = q.get_device() if isinstance(q, torch.Tensor) else -1
-    _contiguous(q, "q", torch.bfloat16, index)
-    if q.dim() != 3:
-        raise ValueError("q must be [B, Hq, d]")
-    B, Hq, d = q.shape
-    P, page, Hkv = _pool(q, k_pages, v_pages, index)
-    Bt, W = _paged_rows(page_table, seqlens, index)
-    if Bt != B:
+    first prefix_lens[g] tokens (int32).  A group may hold a single row: its prefix is then
+    spread over the GPU by itself.  Rows in no group are decoded in num_splits splits, as are
+    all rows' own keys (None: enough to fill the GPU) -> (o, lse)."""
+    index, B, Hq, d, P, page, Hkv, rows, W = _paged(q, k_pages, v_pages, page_table, seqlens)
+    if rows != B:
         raise ValueError("page_table must be [B, max_pages] and seqlens [B]")
     _int_tensor(prefix_lens, "prefix_lens", index)
     n_groups = prefix_lens.numel()
-    _int_vector(prefix_lens, "prefix_lens", n_groups, index)
     _int_vector(cu_groups, "cu_groups", n_groups + 1, index)
     n_rows = B
     if group_rows is not None:
         _int_tensor(group_rows, "group_rows", index)
         n_rows = group_rows.numel()
-        _int_vector(group_rows, "group_rows", n_rows, index)
+        if n_rows > _INT_MAX:
+            n_rows = _INT_MAX
+    if n_groups > _INT_MAX:
+        n_groups = _INT_MAX
     sink = _sink(sink_logit, Hq, index)
     if stream is not None or index != _current_device():
         with _Call(index, stream):
@@ -1084,18 +1110,19 @@ def attn_decode_paged_shared(q, k_pages, v_pages, page_table, seqlens, cu_groups
                                             sink_logit=sink_logit, num_splits=num_splits,
                                             scale=scale, workspace=workspace, want_lse=want_lse)
     o, lse = _decode_outputs(q, o, lse, want_lse, index)
-    B, W, P, n_groups, n_rows = map(_c_int, (B, W, P, n_groups, n_rows))
     if num_splits is None:
-        # four CTAs an SM; rows' own keys are few next to the prefix
-        num_splits = max(1, min(8, -(-608 // max(1, B * Hkv))))
-    num_splits = _c_int(int(num_splits))
+        # three CTAs an SM: rows' own keys are few next to the prefix
+        num_splits = max(1, min(8, -(-456 // max(1, B * Hkv))))
+    else:
+        num_splits = _c_int(int(num_splits))
     ws = _bytes(attn_decode_shared_workspace_size(B, Hq, Hkv, d, n_groups, n_rows, W, num_splits),
                 index, workspace)
     rc = lib.attn_decode_paged_shared(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-        seqlens.data_ptr(), cu_groups.data_ptr(), prefix_lens.data_ptr(), _ptr(group_rows),
-        o.data_ptr(), _ptr(lse), B, Hq, Hkv, d, page, W, P, n_groups, n_rows, num_splits,
-        d ** -0.5 if scale is None else float(scale), sink, ws.data_ptr(), ws.nbytes,
+        seqlens.data_ptr(), cu_groups.data_ptr(), prefix_lens.data_ptr(),
+        None if group_rows is None else group_rows.data_ptr(), o.data_ptr(),
+        None if lse is None else lse.data_ptr(), B, Hq, Hkv, d, page, W, P, n_groups, n_rows,
+        num_splits, d ** -0.5 if scale is None else scale, sink, ws.data_ptr(), ws.nbytes,
         _raw_stream(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_paged_shared")
@@ -1118,17 +1145,10 @@ def attn_decode_paged_mass(q, k_pages, v_pages, page_table, seqlens, mass, posit
     (into mass_out if given, else in place).  The newest token's mass starts here, and its
     slot of positions [B,Hkv,slots] int32 becomes last_positions [B] (None: its slot's
     number) -> (o, lse)."""
-    torch = _torch()
-    index = q.get_device() if isinstance(q, torch.Tensor) else -1
-    _contiguous(q, "q", torch.bfloat16, index)
-    if q.dim() != 3:
-        raise ValueError("q must be [B, Hq, d]")
-    B, Hq, d = q.shape
-    P, page, Hkv = _pool(q, k_pages, v_pages, index)
-    Bt, W = _paged_rows(page_table, seqlens, index)
-    if Bt != B:
+    index, B, Hq, d, P, page, Hkv, rows, W = _paged(q, k_pages, v_pages, page_table, seqlens)
+    if rows != B:
         raise ValueError("page_table must be [B, max_pages] and seqlens [B]")
-    mass_out, slots = _mass_tensors(mass, mass_out, positions, last_positions, B, Hkv, index)
+    mass_out, slots = _masses(mass, mass_out, positions, last_positions, B, Hkv, index)
     sink = _sink(sink_logit, Hq, index)
     if stream is not None or index != _current_device():
         with _Call(index, stream):
@@ -1137,13 +1157,15 @@ def attn_decode_paged_mass(q, k_pages, v_pages, page_table, seqlens, mass, posit
                                           sink_logit=sink_logit, num_splits=num_splits,
                                           scale=scale, workspace=workspace, want_lse=want_lse)
     o, lse = _decode_outputs(q, o, lse, want_lse, index)
-    B, W, P, slots, num_splits = map(_c_int, (B, W, P, slots, int(num_splits)))
+    num_splits = _c_int(int(num_splits))
     ws = _bytes(attn_decode_mass_workspace_size(B, Hq, d, W, num_splits), index, workspace)
     rc = lib.attn_decode_paged_mass(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-        seqlens.data_ptr(), mass.data_ptr(), mass_out.data_ptr(), _ptr(positions),
-        _ptr(last_positions), o.data_ptr(), _ptr(lse), B, Hq, Hkv, d, page, W, P, slots,
-        num_splits, d ** -0.5 if scale is None else float(scale), sink, ws.data_ptr(), ws.nbytes,
+        seqlens.data_ptr(), mass.data_ptr(), mass_out.data_ptr(),
+        None if positions is None else positions.data_ptr(),
+        None if last_positions is None else last_positions.data_ptr(), o.data_ptr(),
+        None if lse is None else lse.data_ptr(), B, Hq, Hkv, d, page, W, P, slots, num_splits,
+        d ** -0.5 if scale is None else scale, sink, ws.data_ptr(), ws.nbytes,
         _raw_stream(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_paged_mass")
@@ -1164,19 +1186,12 @@ def attn_mass_paged(q, lse, k_pages, page_table, cu_seqlens_q, seqlens_k, mass, 
     last new_tokens [B] keys of a sequence (None: as many as its queries) start here: their
     slots of positions [B,Hkv,slots] int32 count up to last_positions [B] (None: to the last
     slot's number) -> mass_out."""
-    torch = _torch()
-    index = q.get_device() if isinstance(q, torch.Tensor) else -1
-    _contiguous(q, "q", torch.bfloat16, index)
-    if q.dim() != 3:
-        raise ValueError("q must be [Tq, Hq, d]")
-    Tq, Hq, d = q.shape
-    _contiguous(lse, "lse", torch.float32, index)
+    index, Tq, Hq, d, P, page, Hkv, B, W = _paged(q, k_pages, None, page_table, seqlens_k)
+    _contiguous(lse, "lse", _torch_module.float32, index)
     if lse.shape != (Hq, Tq):
         raise ValueError(f"lse must be [{Hq}, {Tq}]")
-    P, page, Hkv = _pool(q, k_pages, None, index)
-    B, W = _paged_rows(page_table, seqlens_k, index)
     _int_vector(cu_seqlens_q, "cu_seqlens_q", B + 1, index)
-    out, slots = _mass_tensors(mass, mass_out, positions, last_positions, B, Hkv, index)
+    out, slots = _masses(mass, mass_out, positions, last_positions, B, Hkv, index)
     if new_tokens is not None:
         _int_vector(new_tokens, "new_tokens", B, index)
     if max_seqlen_q is None:
@@ -1188,14 +1203,15 @@ def attn_mass_paged(q, lse, k_pages, page_table, cu_seqlens_q, seqlens_k, mass, 
                                    max_seqlen_q=max_seqlen_q, causal=causal, window=window,
                                    n_sink=n_sink, scale=scale, mass_out=mass_out,
                                    workspace=workspace)
-    B, W, P, slots, Tq = map(_c_int, (B, W, P, slots, Tq))
     ws = _bytes(attn_mass_workspace_size(B, Hkv, W), index, workspace)
     rc = lib.attn_mass_paged(
         q.data_ptr(), lse.data_ptr(), k_pages.data_ptr(), page_table.data_ptr(),
         cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), mass.data_ptr(), out.data_ptr(),
-        _ptr(positions), _ptr(last_positions), _ptr(new_tokens), B, Hq, Hkv,
+        None if positions is None else positions.data_ptr(),
+        None if last_positions is None else last_positions.data_ptr(),
+        None if new_tokens is None else new_tokens.data_ptr(), B, Hq, Hkv,
         _c_int(int(max_seqlen_q)), Tq, d, page, W, P, slots,
-        d ** -0.5 if scale is None else float(scale), int(bool(causal)), _c_int(int(window)),
+        d ** -0.5 if scale is None else scale, 1 if causal else 0, _c_int(int(window)),
         _c_int(int(n_sink)), ws.data_ptr(), ws.nbytes, _raw_stream(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_mass_paged")
@@ -1219,16 +1235,23 @@ def attn_evict_paged(mass, positions, page_table, seqlens, keep, k_pages, v_page
     index = mass.get_device() if isinstance(mass, torch.Tensor) else -1
     _contiguous(mass, "mass", torch.float32, index)
     _int_tensor(positions, "positions", index)
-    B, W = _paged_rows(page_table, seqlens, index)
-    _int_vector(keep, "keep", B, index)
+    _int_tensor(page_table, "page_table", index)
     shape = mass.shape
-    if positions.shape != shape or len(shape) not in (3, 4) or shape[-3] != B:
+    n = len(shape)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, W = page_table.shape
+    _int_vector(seqlens, "seqlens", B, index)
+    _int_vector(keep, "keep", B, index)
+    if positions.shape != shape or (n != 3 and n != 4) or shape[-3] != B:
         raise ValueError("mass and positions must both be [layers, B, Hkv, slots] or "
                          "[B, Hkv, slots]")
-    _rows_tensor(k_pages, "k_pages", (len(shape) + 1,), index)
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != n + 1:
+        raise ValueError("k_pages must be [layers, P, 16, Hkv, d], or [P, 16, Hkv, d] without "
+                         "layers")
     P = k_pages.shape[-4]
     layers, page, Hkv, d = _cache_pools(k_pages, v_pages, P, index)
-    if shape[-2] != Hkv or (len(shape) == 4 and shape[0] != layers):
+    if shape[-2] != Hkv or (n == 4 and shape[0] != layers):
         raise ValueError("mass and k_pages disagree in layers or heads")
     if refs is not None:
         _int_vector(refs, "refs", P, index)
@@ -1241,13 +1264,15 @@ def attn_evict_paged(mass, positions, page_table, seqlens, keep, k_pages, v_page
                                     workspace=workspace)
     if new_seqlens is None:
         new_seqlens = torch.empty_like(seqlens)
-    B, W, P, slots = map(_c_int, (B, W, P, shape[-1]))
+    slots = shape[-1]
+    if B > _INT_MAX or W > _INT_MAX or P > _INT_MAX or slots > _INT_MAX or layers > _INT_MAX:
+        layers, B, W, P, slots = map(_c_int, (layers, B, W, P, slots))
     ws = _bytes(attn_evict_workspace_size(layers, B, Hkv, slots, W), index, workspace)
     rc = lib.attn_evict_paged(
         mass.data_ptr(), positions.data_ptr(), page_table.data_ptr(), seqlens.data_ptr(),
-        keep.data_ptr(), _ptr(refs), new_seqlens.data_ptr(), k_pages.data_ptr(),
-        v_pages.data_ptr(), B, layers, Hkv, d, slots, page, W, P, _c_int(int(n_sink)),
-        _c_int(int(recent)), ws.data_ptr(), ws.nbytes, _raw_stream(index))
+        keep.data_ptr(), None if refs is None else refs.data_ptr(), new_seqlens.data_ptr(),
+        k_pages.data_ptr(), v_pages.data_ptr(), B, layers, Hkv, d, slots, page, W, P,
+        _c_int(int(n_sink)), _c_int(int(recent)), ws.data_ptr(), ws.nbytes, _raw_stream(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_evict_paged")
     return new_seqlens

@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(kAddThreads) attn_mass_add_kernel(const MassAr
   fresh = max(0, min(fresh, s.L));
   const int last = a.last_positions ? a.last_positions[b] : s.L - 1;
   const size_t row = (static_cast<size_t>(b) * a.Hkv + h) * a.slots;
-#pragma unroll
+#pragma unroll 1
   for (int j = 0; j < kAddTokens / kAddThreads; ++j) {
     const int t = t0 + j * kAddThreads + threadIdx.x;
     if (t >= s.L) break;

@@ -165,22 +165,21 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
 #pragma unroll 1
   for (int g = warp; g < n_groups; g += kPlanThreads / 32) {
     const int e0 = a.cu_groups[g], e1 = a.cu_groups[g + 1], prefix = a.prefix_lens[g];
-    int best = -1, at = INT_MAX, live = 0;
+    int best = -1, at = INT_MAX;
 #pragma unroll 1
     for (int e = e0 + lane; e < e1; e += 32) {
       const int b = a.rows ? a.rows[e] : e;
       if (b < 0 || b >= a.B || entry[b] != e) continue;
-      ++live;
       const int L = row_length(a, b);
       if (L > best) best = L, at = b;
     }
     const int longest = __reduce_max_sync(0xffffffffu, best);
     at = __reduce_min_sync(0xffffffffu, best == longest ? at : INT_MAX);
-    live = __reduce_add_sync(0xffffffffu, live);
     if (lane == 0 && (prefix < 0 || prefix > a.max_pages * kPage))
       atomicOr(a.status, kStatusBadInput);
-    // a group of one shares nothing: its row is done by the split decode alone
-    const int pages = live < 2 || prefix < 0 ? 0 : min(prefix, longest) / kPage;
+    // (also of a group of one: its long prefix is spread over the CTAs like any other, where
+    // the split decode's few CTAs for a row would be the last to finish)
+    const int pages = prefix < 0 ? 0 : min(prefix, max(longest, 0)) / kPage;
     if (lane == 0) a.info[g] = make_int4(pages, e0, (e1 - e0) * a.G, at);
 #pragma unroll 1
     for (int e = e0 + lane; e < e1; e += 32) {

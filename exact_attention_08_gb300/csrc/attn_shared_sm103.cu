@@ -716,9 +716,9 @@ __global__ void __launch_bounds__(kThr, 1)
 
 // ---------------------------------------------------------------- merge
 // A warp for each (row, query head), two at d = 256: the partial results of its group's prefix, CTA by
-// CTA, then those of its own pages, split by split.  The log-sum-exps are read a lane
-// each, so that all outputs can be under way together (read one behind the other, 20
-// partial results took 25 us).
+// CTA, then those of its own pages, split by split, 32 at a time: their log-sum-exps are
+// read a lane each, the outputs so far scaled to the new maximum, and four outputs are
+// under way together (read one behind the other, 20 partial results took 25 us).
 constexpr int kMergeThreads = 256;
 
 template <int D>
@@ -729,18 +729,13 @@ __global__ void __launch_bounds__(kMergeThreads)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int unit = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
-  const int row = unit / kWarps, column = unit % kWarps * 128;
+  const int row = unit / kWarps, column = unit % kWarps * 128 + lane * kPer;
   if (row >= a.B * a.Hq) return;
   const int b = row / a.Hq, hq = row - b * a.Hq, S = dec.num_splits;
   const int4 info = a.rowinfo[b];  // group (-1: none that shares pages), first pair
-  long long runs[kSharedMaxCtas / 32 + 1];  // this lane's CTAs, and the one behind each
-#pragma unroll
-  for (int i = 0; i <= kSharedMaxCtas / 32; ++i) {
-    const int c = i * 32 + lane;
-    runs[i] = c <= a.ctas ? a.runs[c] : LLONG_MAX;
-  }
-  long long part = 0, second = 0;  // first partial result; distance of the second stream's
-  int c0 = 0, n_prefix = 0, streams = 1;
+  // Rows of partial results fit in 32 bits without sign: 2 * 2^30 and the CTAs' 256 each.
+  uint32_t part = 0, second = 0;  // the first; distance of the second stream's
+  int n_prefix = 0, pairs_of = 0;
   if (info.x >= 0) {
     const int4 group = a.info[info.x];
     const int e0 = group.y, pairs = group.z;
@@ -748,92 +743,100 @@ __global__ void __launch_bounds__(kMergeThreads)
     const int mt = pr / a.tile_rows;
     const int rows = min(a.tile_rows, pairs - mt * a.tile_rows);
     const int mts = ceil_div(pairs, a.tile_rows), tiles = ceil_div(group.x, a.tile_pages);
-    const long long u = a.base[info.x] + (static_cast<long long>(h) * mts + mt) * tiles;
+    const long long u = a.base[info.x] + static_cast<long long>(h * mts + mt) * tiles;
     // the CTAs whose runs hold the item's units: runs that start at or before the first and
     // the last of them (those without units start past all)
     int first = 0, last = 0;
-#pragma unroll
-    for (int i = 0; i <= kSharedMaxCtas / 32; ++i) {
-      first += runs[i] <= u;
-      last += runs[i] <= u + tiles - 1;
+#pragma unroll 2
+    for (int c = lane; c < a.ctas; c += 32) {
+      const long long start = a.runs[c];
+      first += start <= u;
+      last += start < u + tiles;
     }
-    c0 = __reduce_add_sync(0xffffffffu, first) - 1;
+    const int c0 = __reduce_add_sync(0xffffffffu, first) - 1;
     n_prefix = __reduce_add_sync(0xffffffffu, last) - c0;
-    if (D != 256 && rows <= kRows) {
-      streams = 2;
-      second = rows;
-    }
-    part = 2 * (static_cast<long long>(e0) * a.Hq + static_cast<long long>(h) * pairs) +
-           2LL * mt * a.tile_rows + (pr - mt * a.tile_rows) +
-           static_cast<long long>(kItemRows) * c0;
-    n_prefix *= streams;
+    pairs_of = D != 256 && rows <= kRows;  // two partial results a CTA
+    second = rows;
+    part = 2u * (static_cast<uint32_t>(e0) * a.Hq + static_cast<uint32_t>(h) * pairs +
+                 mt * a.tile_rows) +
+           (pr - mt * a.tile_rows) + kItemRows * c0;
+    n_prefix <<= pairs_of;
   }
   const int n = n_prefix + S;
-  // partial result i: its log-sum-exp and output
-  auto prefix_row = [&](int i) -> long long {
-    return streams == 2 ? part + static_cast<long long>(kItemRows) * (i >> 1) + (i & 1) * second
-                        : part + static_cast<long long>(kItemRows) * i;
-  };
-  auto lse_of = [&](int i) -> float {
-    return i < n_prefix ? a.part_lse[prefix_row(i)]
-                        : dec.ws_lse[static_cast<long long>(row) * S + i - n_prefix];
-  };
   const float sg = dec.sink ? dec.sink[hq] : -INFINITY;
-  float M = sg;
-#pragma unroll 1
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, lse_of(i));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float acc[kPer], wsum = 0.f;
+  float M = sg, wsum = sg != -INFINITY && lane == 0 ? 1.f : 0.f, acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  if (M != -INFINITY) {
 #pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + lane;
-      const float w = i < n ? expf(lse_of(i) - M) : 0.f;
-      const float* src = nullptr;
-      if (w > 0.f)  // (the output of a part without a key is not written)
-        src = i < n_prefix ? a.part_o + prefix_row(i) * D
-                           : dec.ws_o + (static_cast<long long>(row) * S + i - n_prefix) * D;
-      wsum += w;
-      if (src != nullptr) src += column;
-      const int m = min(32, n - i0);
-#pragma unroll 8
-      for (int j = 0; j < m; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, w, j);
-        const float* from = reinterpret_cast<const float*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), j));
-        if (from == nullptr) continue;
-        if constexpr (kPer == 2) {
-          const float2 v = reinterpret_cast<const float2*>(from)[lane];
-          acc[0] = fmaf(wj, v.x, acc[0]);
-          acc[1] = fmaf(wj, v.y, acc[1]);
-        } else {
-          const float4 v = reinterpret_cast<const float4*>(from)[lane];
-          acc[0] = fmaf(wj, v.x, acc[0]);
-          acc[1] = fmaf(wj, v.y, acc[1]);
-          acc[2] = fmaf(wj, v.z, acc[2]);
-          acc[3] = fmaf(wj, v.w, acc[3]);
-        }
-      }
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    // a partial result a lane: its log-sum-exp, and where its output is
+    const int i = i0 + lane;
+    float l = -INFINITY;
+    const float* src = nullptr;
+    if (i < n_prefix) {
+      const uint32_t p = part + kItemRows * (i >> pairs_of) + (i & pairs_of) * second;
+      l = a.part_lse[p];
+      src = a.part_o + static_cast<size_t>(p) * D;
+    } else if (i < n) {
+      const size_t p = static_cast<size_t>(row) * S + (i - n_prefix);
+      l = dec.ws_lse[p];
+      src = dec.ws_o + p * D;
     }
+    float top = l;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
-    if (sg != -INFINITY) wsum += expf(sg - M);
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top == -INFINITY) continue;
+    top = fmaxf(top, M);
+    const float keep = M == -INFINITY ? 0.f : expf(M - top), w = expf(l - top);
+    M = top;
+    wsum = fmaf(wsum, keep, w);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] *= keep;
+    // (the output of a part without a key is not written)
+    uint32_t some = __ballot_sync(0xffffffffu, w > 0.f);
+#pragma unroll 1
+    while (some != 0) {
+      // four at a time
+      float v[4][kPer], wj[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = some != 0 ? __ffs(some) - 1 : 0;
+        wj[j] = some != 0 ? __shfl_sync(0xffffffffu, w, at) : 0.f;
+        const float* from = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), at)) + column;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) v[j][e] = 0.f;
+        if (some != 0) {
+          if constexpr (kPer == 2) {
+            const float2 x = *reinterpret_cast<const float2*>(from);
+            v[j][0] = x.x, v[j][1] = x.y;
+          } else {
+            const float4 x = *reinterpret_cast<const float4*>(from);
+            v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+          }
+        }
+        some &= some - 1;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wj[j], v[j][e], acc[e]);
+    }
   }
-  const bool seen = M != -INFINITY;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
+  const float inv = M != -INFINITY ? 1.f / wsum : 0.f;
   uint32_t out[kPer / 2];
 #pragma unroll
-  for (int e = 0; e < kPer / 2; ++e)
-    out[e] = seen ? pack_bf16x2(acc[2 * e] / wsum, acc[2 * e + 1] / wsum) : 0u;
-  uint32_t* o = reinterpret_cast<uint32_t*>(dec.o) +
-                static_cast<size_t>(row) * (D / 2) + column / 2 + lane * (kPer / 2);
+  for (int e = 0; e < kPer / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  uint32_t* o =
+      reinterpret_cast<uint32_t*>(dec.o) + (static_cast<size_t>(row) * D + column) / 2;
   if constexpr (kPer == 2)
     o[0] = out[0];
   else
     *reinterpret_cast<uint2*>(o) = make_uint2(out[0], out[1]);
-  if (dec.lse && lane == 0 && column == 0) dec.lse[row] = seen ? M + logf(wsum) : -INFINITY;
+  if (dec.lse && lane == 0 && unit % kWarps == 0)
+    dec.lse[row] = M != -INFINITY ? M + logf(wsum) : -INFINITY;
 }
 
 template <typename... Params, typename... Args>

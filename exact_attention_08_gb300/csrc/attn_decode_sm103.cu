@@ -143,7 +143,7 @@ struct DecParams {
   const int* seqlens;
   float* ws_o;
   float* ws_lse;
-  const int* order;  // [B] requests longest first (the grid's z order)
+  const int* order;  // [B] requests longest first (the grid's z order); kDecMass: may be null
   float* scores;     // kDecMass: [B, Hq, max_pages * 16] raw scores
   const int* start;  // kDecShared: [B] first page of a request's own
   int B, Hq, Hkv, G, n_hchunks, max_pages, num_pages, num_splits;
@@ -223,7 +223,8 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
   // overlaps it, and this waits for its result.  (kDecShared: of the prefix
   // kernel, which lets this one start only once it has itself seen the order.)
   if constexpr (kMode != kDecShared) asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int b = p.order[blockIdx.z];
+  int b = blockIdx.z;
+  if (kMode != kDecMass || p.order != nullptr) b = p.order[b];
   const int g0 = hchunk * kHeadsPerCta;                  // first group member served
   const int nh = min(kHeadsPerCta, p.G - g0);            // query heads served
   const int h0 = hkv * p.G + g0;                         // first query head served
@@ -505,7 +506,8 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   // overlaps it, and this waits for its result.  (kDecShared: of the prefix
   // kernel, which lets this one start only once it has itself seen the order.)
   if constexpr (kMode != kDecShared) asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int b = p.order[blockIdx.z];
+  int b = blockIdx.z;
+  if (kMode != kDecMass || p.order != nullptr) b = p.order[b];
   const int g0 = hchunk * kHeadsPerCta;
   const int nh = min(kHeadsPerCta, p.G - g0);
   const int h0 = hkv * p.G + g0;
@@ -922,21 +924,34 @@ cudaError_t launch_split(const DecodeLaunch& a, cudaStream_t stream) {
   }
 }
 
-// The request order, the splits, the merge (and the masses).
+// The request order, the splits, the merge.
 template <int D>
 cudaError_t launch_dec(const DecodeLaunch& a, cudaStream_t stream) {
   attn_decode_order_kernel<<<1, kOrderThreads, 0, stream>>>(a.seqlens, a.B, a.max_pages, a.order);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (a.mass_out == nullptr) {
-    e = launch_split<D, kDecPlain>(a, stream);
-    if (e != cudaSuccess) return e;
-    e = launch_combine<D>(a, stream);
-    return e != cudaSuccess ? e : cudaGetLastError();
-  }
-  e = launch_split<D, kDecMass>(a, stream);
+  e = launch_split<D, kDecPlain>(a, stream);
   if (e != cudaSuccess) return e;
+  e = launch_combine<D>(a, stream);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// The same with the keys' masses.  Where all split CTAs are resident at once their order
+// does not matter, and the order kernel's launch (3 us of 12 in the smallest call) is saved.
+template <int D>
+cudaError_t launch_dec_mass(DecodeLaunch a, int num_sms, cudaStream_t stream) {
   const int G = a.Hq / a.Hkv, per = kMassThreads / D;
+  const long long ctas = static_cast<long long>(a.num_splits) * a.B * a.Hkv *
+                         ((G + kHeadsPerCta - 1) / kHeadsPerCta);
+  cudaError_t e = cudaSuccess;
+  if (ctas > static_cast<long long>(D == 256 ? 2 : kDecCtasPerSm) * num_sms) {
+    attn_decode_order_kernel<<<1, kOrderThreads, 0, stream>>>(a.seqlens, a.B, a.max_pages,
+                                                              a.order);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  } else {
+    a.order = nullptr;
+  }
+  if ((e = launch_split<D, kDecMass>(a, stream)) != cudaSuccess) return e;
   const int merge_blocks = (G + per - 1) / per;
   const long long slots = std::min<long long>(static_cast<long long>(a.max_pages) * kPage,
                                               a.mass_slots);
@@ -952,6 +967,13 @@ cudaError_t launch_attn_decode(const DecodeLaunch& a, cudaStream_t stream) {
   if (a.d == 128) return launch_dec<128>(a, stream);
   if (a.d == 64) return launch_dec<64>(a, stream);
   if (a.d == 256) return launch_dec<256>(a, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_attn_decode_mass(const DecodeLaunch& a, int num_sms, cudaStream_t stream) {
+  if (a.d == 128) return launch_dec_mass<128>(a, num_sms, stream);
+  if (a.d == 64) return launch_dec_mass<64>(a, num_sms, stream);
+  if (a.d == 256) return launch_dec_mass<256>(a, num_sms, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -280,6 +280,7 @@ cudaError_t launch_attn_fwd(const FwdLaunch& a, cudaStream_t stream);
 cudaError_t launch_attn_fwd256(const FwdLaunch& a, cudaStream_t stream);
 cudaError_t launch_attn_fill_empty(const FwdLaunch& a, cudaStream_t stream);
 cudaError_t launch_attn_decode(const DecodeLaunch& a, cudaStream_t stream);
+cudaError_t launch_attn_decode_mass(const DecodeLaunch& a, int num_sms, cudaStream_t stream);
 // The splits of the requests' own pages, after the kernel of their shared ones.
 cudaError_t launch_attn_decode_own(const DecodeLaunch& a, cudaStream_t stream);
 cudaError_t launch_attn_rope(const RopeArgs& p, int num_sms, cudaStream_t stream);

@@ -257,7 +257,7 @@ ATTN_API int attn_decode_paged_mass(const void* q, const void* k_pages, const vo
   a.mass_slots = mass_slots;
   int num_sms = 0;
   if ((rc = decode_maps(&a, k_pages, v_pages, &num_sms)) != ATTN_OK) return rc;
-  const cudaError_t e = launch_attn_decode(a, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_attn_decode_mass(a, num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : cuda_error(e, "attn_decode_paged_mass launch");
 }
 

@@ -43,6 +43,10 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVecs = 4;
+// Selecting CTAs for every SM, and slots of a row, from and up to which the selecting CTA copies
+// too (512 units, 64 tokens over a budget of 1,024: 29.1 us on the device either way, and a
+// launch less; 3,000 over it, 100 by two kernels and 113 by one; 128 units, 41 and 76).
+constexpr int kFusedPerSm = 2, kFusedSlots = 2048;
 constexpr int kMaxCached = 40960;  // tokens whose keys fit in a CTA's shared memory (160 KB)
 // Threads of the selecting CTA: rows of up to 4,096 tokens take 256 (a longer block waits
 // longer at its barriers), longer ones 384, four CTAs an SM.
@@ -88,6 +92,34 @@ __device__ __forceinline__ int block_scan(int v, int* warp_part, int* total) {
   }
   *total = all;
   return base + x - v;
+}
+
+// Keys and values of a unit's moves (pool rows), by the threads of one CTA: 2 d / 8 vectors of
+// 16 bytes each, all in one index, four in flight a thread.
+__device__ __forceinline__ void copy_moves(const EvictArgs& a, int layer, int h, const int2* moves,
+                                           int count) {
+  const size_t layer0 = static_cast<size_t>(layer) * a.num_pages * kPage;
+  const int shift = a.vecs == 8 ? 4 : a.vecs == 16 ? 5 : 6;  // of 2 vecs
+  const int total = count << shift, step = blockDim.x;
+#pragma unroll 1
+  for (int i0 = threadIdx.x; i0 < total; i0 += step * kCopyVecs) {
+    uint4 v[kCopyVecs];
+    uint4* to[kCopyVecs];
+#pragma unroll
+    for (int j = 0; j < kCopyVecs; ++j) {
+      const int i = i0 + j * step;
+      to[j] = nullptr;
+      if (i >= total) continue;
+      const int2 m = moves[i >> shift];
+      const int r = i & (2 * a.vecs - 1);
+      uint4* base = (r < a.vecs ? a.k_pages : a.v_pages) + (r & (a.vecs - 1));
+      v[j] = base[((layer0 + m.x) * a.Hkv + h) * a.vecs];
+      to[j] = base + ((layer0 + m.y) * a.Hkv + h) * a.vecs;
+    }
+#pragma unroll
+    for (int j = 0; j < kCopyVecs; ++j)
+      if (to[j] != nullptr) *to[j] = v[j];
+  }
 }
 
 // Rows of any length: the keys are formed again for every step.
@@ -302,8 +334,9 @@ __device__ __forceinline__ uint32_t lowest_bits(uint32_t x, int n) {
 
 // Rows whose keys fit in shared memory: keys [slots rounded up to 32], then two words for
 // every 32 of them.
-// kFours: rows of mass and positions start on 16 bytes, four tokens a load.
-template <bool kFours>
+// kFours: rows of mass and positions start on 16 bytes, four tokens a load.  kCopies: the keys
+// and values are moved here too.
+template <bool kFours, bool kCopies>
 __global__ void __launch_bounds__(kLargeThreads, 4) attn_evict_select_kernel(const EvictArgs a,
                                                                              int words) {
   extern __shared__ uint32_t s_keys[];
@@ -529,10 +562,13 @@ __global__ void __launch_bounds__(kLargeThreads, 4) attn_evict_select_kernel(con
     pos[m.y] = pos[m.x];
     moves[i] = make_int2(pool_row(a, b, m.x), pool_row(a, b, m.y));
   }
+  if constexpr (kCopies) {
+    __syncthreads();
+    copy_moves(a, layer, h, moves, total);
+  }
 }
 
-// Keys and values of the moves: 2 d / 8 vectors of 16 bytes each, the vectors of
-// a unit's moves in one index.
+// The same by a.copy_blocks blocks a unit.
 template <int kVecs>
 __global__ void __launch_bounds__(kCopyThreads) attn_evict_copy_kernel(const EvictArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -569,14 +605,29 @@ __global__ void __launch_bounds__(kCopyThreads) attn_evict_copy_kernel(const Evi
 
 cudaError_t launch_attn_evict(EvictArgs a, int num_sms, cudaStream_t stream) {
   const int cap = std::min(a.slots, a.max_pages * kPage);
+  const bool cached = cap <= kMaxCached;
+  // Selecting CTAs that fill the GPU by themselves, of short rows, move their keys and values
+  // too; others leave that to a kernel of some sixteen blocks for every SM (and no more than
+  // there can be steps).
+  const int per_step = kCopyThreads * kCopyVecs;
+  const long long most = (static_cast<long long>(a.most_moves) * 2 * a.vecs + per_step - 1) /
+                         per_step;
+  a.copy_blocks = cap <= kFusedSlots && a.units >= kFusedPerSm * num_sms
+                      ? 0
+                      : static_cast<int>(std::max(
+                            1LL, std::min(most, (16LL * num_sms + a.units - 1) / a.units)));
   cudaError_t e;
-  if (cap <= kMaxCached) {
+  if (cached) {
     const int words = (cap + 31) / 32;
-    static SharedMemoryLimit limit, limit4;
+    static SharedMemoryLimit limits[4];
     const bool fours = a.slots % 4 == 0 && reinterpret_cast<uintptr_t>(a.mass) % 16 == 0 &&
                        reinterpret_cast<uintptr_t>(a.positions) % 16 == 0;
-    auto select = fours ? attn_evict_select_kernel<true> : attn_evict_select_kernel<false>;
-    e = (fours ? limit4 : limit).raise(select, (kMaxCached + 2 * kMaxCached / 32) * 4);
+    const bool copies = a.copy_blocks == 0;
+    auto select = fours ? (copies ? attn_evict_select_kernel<true, true>
+                                  : attn_evict_select_kernel<true, false>)
+                        : (copies ? attn_evict_select_kernel<false, true>
+                                  : attn_evict_select_kernel<false, false>);
+    e = limits[2 * fours + copies].raise(select, (kMaxCached + 2 * kMaxCached / 32) * 4);
     if (e != cudaSuccess) return e;
     select<<<a.units, cap <= kSmallRow ? kSmallThreads : kLargeThreads,
              static_cast<size_t>(words) * 34 * 4, stream>>>(a, words);
@@ -584,14 +635,9 @@ cudaError_t launch_attn_evict(EvictArgs a, int num_sms, cudaStream_t stream) {
     attn_evict_select_long_kernel<<<a.units, kThreads, 0, stream>>>(a);
   }
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // about sixteen blocks for every SM, no more than there can be steps
-  const int per_step = kCopyThreads * kCopyVecs;
-  const long long most = (static_cast<long long>(a.most_moves) * 2 * a.vecs + per_step - 1) /
-                         per_step;
-  a.copy_blocks = static_cast<int>(
-      std::max(1LL, std::min(most, (16LL * num_sms + a.units - 1) / a.units)));
+  if (e != cudaSuccess || a.copy_blocks == 0) return e;
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.copy_blocks) * a.units);
   cfg.blockDim = dim3(kCopyThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -599,7 +645,6 @@ cudaError_t launch_attn_evict(EvictArgs a, int num_sms, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.copy_blocks * a.units));
   auto copy = a.vecs == 8    ? attn_evict_copy_kernel<8>
               : a.vecs == 16 ? attn_evict_copy_kernel<16>
                              : attn_evict_copy_kernel<32>;

@@ -194,3 +194,13 @@ def test_many_equal_masses(L, K, values):
     c.mass = 0.5 + torch.randint(0, values, c.mass.shape, generator=g).float() / 1024
     c.run([K, min(K, L // 3)], 4, 20)
     assert ea.attn_device_status() == ea.ATTN_OK
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_short_rows(d):
+    """Enough rows and heads that each selecting CTA moves its own keys and values."""
+    g = np.random.default_rng(d)
+    lens = g.integers(1, 120, 180).tolist()
+    c = Cache(lens, 1, 2, d, seed=d)
+    c.run([int(g.integers(0, n + 2)) for n in lens], 2, 6)
+    assert ea.attn_device_status() == ea.ATTN_OK

@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(kThr, 1)
       const long long prow = it.part + (two ? pr : stream * it.rows + r);
       if (pr < it.rows) a.part_lse[prow] = seen ? fmaf(m_used, a.scale, logf(l)) : -INFINITY;
       if (last >= 0) {
-        float* dst = a.part_o + prow * D;
+        float* dst = a.part_o + prow * D;  // (32-byte stores: full sectors, 59.1 -> 57.3 us)
         const uint32_t tO = tmem + lanes + C::kColO + stream * D;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -689,12 +689,10 @@ __global__ void __launch_bounds__(kThr, 1)
           tmem_ld_wait_x32(o);
           if (pr < it.rows) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(dst + 32 * c + e) = make_float4(
-                  seen ? __uint_as_float(o[e]) * inv : 0.f,
-                  seen ? __uint_as_float(o[e + 1]) * inv : 0.f,
-                  seen ? __uint_as_float(o[e + 2]) * inv : 0.f,
-                  seen ? __uint_as_float(o[e + 3]) * inv : 0.f);
+            for (int e = 0; e < 32; ++e)
+              o[e] = seen ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) st_global_v8(dst + 32 * c + e, o + e);
           }
         }
         // the next item's first product waits for this warp's next p_ready

@@ -115,7 +115,8 @@ SharedLayout shared_layout(int B, int Hq, int Hkv, int d, int n_groups, int n_ro
                            int num_splits) {
   SharedLayout l;
   const size_t rows = shared_part_rows(Hq, Hkv, d, n_groups, n_rows, max_pages);
-  l.part_o = pad16(attn_decode_workspace_size(B, Hq, d, num_splits));
+  // (16 bytes more: from a 16-byte boundary up to one of 32, for the stores of the outputs)
+  l.part_o = pad16(attn_decode_workspace_size(B, Hq, d, num_splits)) + 16;
   l.part_lse = l.part_o + rows * d * sizeof(float);
   l.begin = pad16(l.part_lse + rows * sizeof(float));
   l.base = l.begin + (kSharedMaxCtas + 1 + static_cast<size_t>(n_groups) + B) * sizeof(int4);
@@ -191,7 +192,7 @@ ATTN_API int attn_decode_paged_shared(const void* q, const void* k_pages, const 
   a.num_pages = num_pages_total;
   a.scale = scale;
   a.scale2 = scale * 1.4426950408889634f;
-  a.part_o = reinterpret_cast<float*>(ws + l.part_o);
+  a.part_o = reinterpret_cast<float*>(reinterpret_cast<uintptr_t>(ws + l.part_o) & ~uintptr_t{31});
   a.part_lse = reinterpret_cast<float*>(ws + l.part_lse);
   a.begin = reinterpret_cast<int4*>(ws + l.begin);
   a.info = a.begin + kSharedMaxCtas + 1;

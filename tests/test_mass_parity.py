@@ -350,3 +350,20 @@ def test_block_captured_on_another_stream_and_empty():
     for b, n in enumerate(lens):
         assert torch.equal(none[b, :, :n], mass[b, :, :n])
     assert ea.attn_device_status() == ea.ATTN_OK
+
+
+@pytest.mark.parametrize("window,n_sink", [(40, 0), (40, 3), (300, 256), (700, 600), (5000, 1), (1, 4000)])
+def test_key_tiles_that_no_query_sees(window, n_sink):
+    """Between the sink keys and the windows: at the start, in the middle and at the end of the
+    rows, for rows without queries and rows shorter than the window."""
+    lens, nq, d = [2900, 700, 1700, 4001, 256, 513], [30, 0, 300, 1, 256, 2], 64
+    r = Rows(lens, 4, 2, d, seed=window + n_sink)
+    cu = np.concatenate([[0], np.cumsum(nq)]).tolist()
+    q = r.q(cu[-1])
+    lse, w = block_reference(r, q, cu, True, window, n_sink, d ** -0.5)
+    out = ea.attn_mass_paged(q.cuda(), torch.tensor(lse).float().cuda(), r.k.cuda(),
+                             i32(r.table), i32(cu), i32(lens), r.mass.cuda(), max_seqlen_q=300,
+                             window=window, n_sink=n_sink)
+    torch.cuda.synchronize()
+    check_block(r, w, out, nq)
+    assert ea.attn_device_status() == ea.ATTN_OK

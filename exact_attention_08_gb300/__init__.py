@@ -21,6 +21,13 @@ Around the attention calls, rotary positions and the paged cache's upkeep:
     q = attn_append_paged(q, k, v, k_pages, v_pages, page_table, seqlens, inv_freq=inv_freq)
     attn_pages_fork(page_table, seqlens, refs, src, dst, k_pages, v_pages)
     new_index, num_live = attn_pages_compact(page_table, seqlens, refs, k_pages, v_pages)
+
+Rows that share a prompt's pages, and caches cut to the keys that queries look at:
+
+    o, lse = attn_decode_paged_shared(q, k_pages, v_pages, page_table, seqlens, cu_groups, prefix_lens)
+    o, lse = attn_decode_paged_mass(q, k_pages, v_pages, page_table, seqlens, mass, positions)
+    attn_mass_paged(q, lse, k_pages, page_table, cu_q, seqlens, mass, max_seqlen_q=...)  # of a prompt
+    new_seqlens = attn_evict_paged(mass, positions, page_table, seqlens, keep, k_pages, v_pages, refs)
 """
 from __future__ import annotations
 

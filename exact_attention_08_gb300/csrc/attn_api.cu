@@ -130,10 +130,10 @@ int make_page_map(CUtensorMap* m, const void* ptr, int d, int Hkv, int pages, co
   auto fn = encode_fn();
   if (!fn) return set_error(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   const cuuint64_t row = static_cast<cuuint64_t>(d) * 2, token = row * Hkv;
-  cuuint64_t dims[5] = {64, 16, static_cast<cuuint64_t>(d) / 64, static_cast<cuuint64_t>(Hkv),
-                        static_cast<cuuint64_t>(pages)};
-  cuuint64_t strides[4] = {token, 128, row, token * 16};
-  cuuint32_t box[5] = {64, 16, static_cast<cuuint32_t>(d / 64), 1, 1};
+  cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(d) / 64, static_cast<cuuint64_t>(Hkv),
+                        2 * static_cast<cuuint64_t>(pages)};
+  cuuint64_t strides[4] = {token, 128, row, token * 8};
+  cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(d / 64), 1, 2};
   cuuint32_t es[5] = {1, 1, 1, 1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims,
                         strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -260,8 +260,10 @@ bool aligned16(const void* p);
 // columns.
 int page_pool_map(CUtensorMap* m, const void* pool, int d, int Hkv, int num_pages,
                   const char* what);
-// The same pool, boxes of a whole page of one head ([d / 64][16 rows][128 bytes] in shared
-// memory).  A copy takes its issuing warp about 100 cycles whatever its size.
+// The same pool, boxes of a whole page of one head: [2 halves][d / 64][8 rows][128 bytes] in
+// shared memory, so that the eight-row groups of consecutive pages are evenly spaced, as a
+// product's operand needs them; the last coordinate is 2 * page.  A copy takes its issuing
+// warp about 100 cycles whatever its size.
 int whole_page_map(CUtensorMap* m, const void* pool, int d, int Hkv, int num_pages,
                    const char* what);
 // Tensor map of packed rows [rows, H, d], boxes of box_rows x box_heads x 64 columns.

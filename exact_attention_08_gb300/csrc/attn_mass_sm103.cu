@@ -18,10 +18,9 @@
 // there as the A operand; the copy costs about a unit's time, which shorter runs
 // would not win back.
 //
-// Rows.  A page (16 tokens of one head) arrives in one copy: [d / 64 atoms][16 rows][128
-// bytes].  Its rows 0-7 belong to row tile 0 and 8-15 to row tile 1, so that the 16
-// eight-row groups of a row tile are evenly spaced, as the product's operand needs:
-// row r of row tile t is key (r / 8) * 16 + t * 8 + r % 8 of the key tile.
+// Rows.  A page (16 tokens of one head) arrives in one copy, as two halves of [d / 64
+// atoms][8 rows][128 bytes]: the eight-row groups of consecutive pages are evenly spaced,
+// as the product's operand needs.
 //
 // Tile.  256 keys (two row tiles) against each query tile: one row tile alone
 // would read 64 bytes of Q a cycle and SM from L2, more than it delivers.  Eight
@@ -80,8 +79,8 @@ struct Cfg {
   static constexpr int kQN = D == 256 ? 64 : 128;  // queries (token, head) of a query tile
   static constexpr int kKSlots = D == 256 ? 1 : 2;
   static constexpr int kQSlots = D == 64 ? 4 : 3;
-  static constexpr int kPageAtom = kPage * 128;    // a page's 64 columns
-  static constexpr int kPageBytes = kAtoms * kPageAtom;
+  static constexpr int kGroup = kAtoms * 1024;     // eight keys
+  static constexpr int kPageBytes = 2 * kGroup;
   static constexpr int kKBytes = kPagesPerTile * kPageBytes;  // a K slot
   static constexpr int kQAtom = kQN * 128;
   static constexpr int kQBytes = kAtoms * kQAtom;  // a Q slot
@@ -96,8 +95,6 @@ struct Cfg {
   static_assert(kSmem <= 227 * 1024 - 512, "shared memory (512 bytes of it static)");
 };
 
-// Key of row r of row tile t, in its key tile.
-__device__ __forceinline__ int row_key(int t, int r) { return (r / 8) * kPage + t * 8 + r % 8; }
 
 // One sequence: its queries and keys.  Lengths are at most 2^29 and the window at most the
 // longest row, so that sums of three of them stay below 2^31.
@@ -481,7 +478,7 @@ __global__ void __launch_bounds__(kThr, 1)
         mbar_arrive_expect_tx_w(&k_full[ks], pages * C::kPageBytes);
         if (lane < pages)
           tma_load_5d(smem + ks * C::kKBytes + lane * C::kPageBytes, &tmK, &k_full[ks], 0, 0, 0, h,
-                      page);
+                      2 * page);
         __syncwarp();
         ++kn;
         if (more) page = lookup();
@@ -528,7 +525,7 @@ __global__ void __launch_bounds__(kThr, 1)
       int buf = 0, sphase = 1;            // next S buffer (its first wait passes at once)
       int pb = -1, ph = -1, pu = -1;      // the query tile before
       const uint64_t dq0 = sdesc_sw128(smem_addr(smem + C::kOffQ), 16, 1024);
-      const uint64_t dk0 = sdesc_sw128(smem_addr(smem), 16, C::kPageBytes);
+      const uint64_t dk0 = sdesc_sw128(smem_addr(smem), 16, C::kGroup);
       const uint32_t tA = tmem + C::kColA;
       bool ok = true;
       do {
@@ -575,7 +572,7 @@ __global__ void __launch_bounds__(kThr, 1)
               if (ts)
                 mma_ts_atom_w(tS, tA + t * (D / 2) + 32 * at, q, idesc, at > 0);
               else
-                mma_ss_atom_w(tS, dk + ((t * 1024 + at * C::kPageAtom) >> 4), q, idesc, at > 0);
+                mma_ss_atom_w(tS, dk + ((t * (C::kKBytes / 2) + at * 1024) >> 4), q, idesc, at > 0);
             };
 #pragma unroll
             for (int at = 0; at < (C::kAtoms + 1) / 2; ++at) issue(at);
@@ -673,8 +670,8 @@ __global__ void __launch_bounds__(kThr, 1)
       const bool fours = a.GP % 4 == 0;
       bool ok = true;
       do {
-        const int ka = w.kt * kKeys, kb = ka + kKeys - 1;  // of this row tile too, nearly
-        const int key = ka + row_key(t, r);
+        const int ka = w.kt * kKeys + t * kRows, kb = ka + kRows - 1;  // of this row tile
+        const int key = ka + r;
         const int units = walk_units(w);
         if (units == 0) break;
         if (units >= kMinTs) {
@@ -686,8 +683,8 @@ __global__ void __launch_bounds__(kThr, 1)
             break;
           }
           constexpr int kChunks = D / 16;  // 16-byte chunks of half a row
-          const uint8_t* src = smem + ks * C::kKBytes + (r / 8) * C::kPageBytes + t * 1024 +
-                               (r % 8) * 128;
+          const uint8_t* src = smem + ks * C::kKBytes + t * (C::kKBytes / 2) +
+                               (r / 8) * C::kGroup + (r % 8) * 128;
           const uint32_t dst = taddr + C::kColA + t * (D / 2) + half * (D / 4);
 #pragma unroll
           for (int c = 0; c < kChunks; c += 4) {
@@ -696,7 +693,7 @@ __global__ void __launch_bounds__(kThr, 1)
             for (int e = 0; e < 4; ++e) {
               const int ch = half * kChunks + c + e;
               const uint4 v = *reinterpret_cast<const uint4*>(
-                  src + (ch / 8) * C::kPageAtom + (((ch % 8) ^ (r & 7)) << 4));
+                  src + (ch / 8) * 1024 + (((ch % 8) ^ (r & 7)) << 4));
               y[4 * e] = v.x, y[4 * e + 1] = v.y, y[4 * e + 2] = v.z, y[4 * e + 3] = v.w;
             }
             tmem_st_x16(dst + 4 * c, y);
@@ -760,7 +757,7 @@ __global__ void __launch_bounds__(kThr, 1)
         const size_t slot =
             (static_cast<size_t>(w.b) * a.Hkv + w.h) * a.max_kt + w.kt + blockIdx.x;
         const float2 sum = add2(acc[0], acc[1]);
-        a.ws_part[(slot * kHalves + half) * kKeys + row_key(t, r)] = sum.x + sum.y;
+        a.ws_part[(slot * kHalves + half) * kKeys + t * kRows + r] = sum.x + sum.y;
         w.left -= units;
       } while (walk_next(a, w));
       if (!ok && lane == 0) {

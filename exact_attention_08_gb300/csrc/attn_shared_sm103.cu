@@ -11,11 +11,10 @@
 // many short ones alike fill the GPU.  An item that several CTAs share has a partial
 // result from each.
 //
-// Keys.  A page (16 tokens of one head) arrives in one copy: [d / 64 atoms][16 rows][128
-// bytes].  As the second operand of S its eight-row groups are evenly spaced only if
-// the first eight tokens of every page are taken together, and the others: two products
-// side by side, so column c of S is token key_of(c), and P is put back in order
-// where it is packed.  As the operand of O a page is just one step of 16 tokens.
+// Keys.  A page (16 tokens of one head) arrives in one copy, as two halves of [d / 64
+// atoms][8 rows][128 bytes]: the eight-row groups of consecutive pages are evenly spaced,
+// as the second operand of S needs them, and a page is one step of 16 tokens of the operand of
+// O.
 //
 // With S = Q K^T and O += P V on the tensor cores and the online softmax between them, a
 // key tile keeps an SM busy for less time than HBM needs to bring its keys and values
@@ -60,8 +59,8 @@ struct Cfg {
   static constexpr int kAtoms = D / 64;
   static constexpr int kQAtom = kRows * 128;
   static constexpr int kQTile = kAtoms * kQAtom;
-  static constexpr int kPageAtom = kPage * 128;        // a page's 64 columns
-  static constexpr int kPageBytes = kAtoms * kPageAtom;
+  static constexpr int kGroup = kAtoms * 1024;         // eight keys
+  static constexpr int kPageBytes = 2 * kGroup;
   static constexpr int kSlot = kPages * kPageBytes;    // a K or V tile
   static constexpr int kSlots = D == 64 ? 8 : 5;
   static constexpr int kOffRing = kStreams * kQTile;
@@ -72,17 +71,6 @@ struct Cfg {
   static_assert(kSmem + kItemRows * 4 + 16 <= 227 * 1024, "shared memory");
   static constexpr uint32_t kColO = 256;
 };
-
-// Token of the key tile whose score stands in column c of S.
-template <int kKeys>
-__device__ __forceinline__ constexpr int key_of(int c) {
-  return (c % (kKeys / 2)) / 8 * kPage + c / (kKeys / 2) * 8 + c % 8;
-}
-// The column of token k.
-template <int kKeys>
-__device__ __forceinline__ constexpr int column_of(int k) {
-  return (k % kPage) / 8 * (kKeys / 2) + k / kPage * 8 + k % 8;
-}
 
 // ---------------------------------------------------------------- plan
 // One block: rows to groups, the pages that every group shares, units before each group,
@@ -406,7 +394,8 @@ __global__ void __launch_bounds__(kThr, 1)
         }
         mbar_arrive_expect_tx_w(&full[s], C::kSlot);
         if (lane < C::kPages)
-          tma_load_5d(ring + s * C::kSlot + lane * C::kPageBytes, map, &full[s], 0, 0, 0, it.h, page);
+          tma_load_5d(ring + s * C::kSlot + lane * C::kPageBytes, map, &full[s], 0, 0, 0, it.h,
+                      2 * page);
         __syncwarp();
         ++n_load;
       };
@@ -436,7 +425,7 @@ __global__ void __launch_bounds__(kThr, 1)
     }
   } else if (warp == kWarpIssuer) {
     // ============================================================ MMA issuer
-    constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, C::kKeys / 2, false);
+    constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, C::kKeys, false);
     constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, D, true);
     int n_load = 0;        // tiles of the ring before this item
     int jobs[2] = {0, 0};  // jobs of each S buffer so far
@@ -462,14 +451,11 @@ __global__ void __launch_bounds__(kThr, 1)
         tc_fence_after_sync();
         const uint64_t dq =
             sdesc_sw128(smem_addr(smem + (two ? (j & 1) * C::kQTile : 0)), 16, 1024);
-        const uint64_t dk = sdesc_sw128(smem_addr(ring + s * C::kSlot), 16, C::kPageBytes);
+        const uint64_t dk = sdesc_sw128(smem_addr(ring + s * C::kSlot), 16, C::kGroup);
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int at = 0; at < C::kAtoms; ++at)
-            mma_ss_atom_w(tmem + buf * C::kKeys + half * (C::kKeys / 2),
-                          dq + at * (C::kQAtom >> 4),
-                          dk + ((half * 1024 + at * C::kPageAtom) >> 4), idesc_s, at > 0);
+        for (int at = 0; at < C::kAtoms; ++at)
+          mma_ss_atom_w(tmem + buf * C::kKeys, dq + at * (C::kQAtom >> 4), dk + at * (1024 >> 4),
+                        idesc_s, at > 0);
         mma_commit_w(&s_full[buf]);
         if (!two || (j & 1)) mma_commit_w(&empty[s]);
         if (j == J - 1) mma_commit_w(q_empty);
@@ -491,7 +477,7 @@ __global__ void __launch_bounds__(kThr, 1)
         }
         ++jobs[buf];
         tc_fence_after_sync();
-        const uint64_t dv = sdesc_sw128(smem_addr(ring + s * C::kSlot), C::kPageAtom, 1024);
+        const uint64_t dv = sdesc_sw128(smem_addr(ring + s * C::kSlot), 1024, C::kGroup);
         const bool first = j < C::kStreams;  // the stream's first job of the item
 #pragma unroll
         for (int kk = 0; kk < C::kKeys / 16; ++kk)
@@ -597,7 +583,7 @@ __global__ void __launch_bounds__(kThr, 1)
         if (ka + C::kKeys > lim_min) {
 #pragma unroll
           for (int c = 0; c < C::kKeys; ++c)
-            if (ka + key_of<C::kKeys>(c) >= lim) x[c] = __float_as_uint(-INFINITY);
+            if (ka + c >= lim) x[c] = __float_as_uint(-INFINITY);
         }
         float mx[8];
 #pragma unroll
@@ -642,10 +628,8 @@ __global__ void __launch_bounds__(kThr, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            constexpr auto col = column_of<C::kKeys>;
-            const float p0 = ex2_approx(fmaf(__uint_as_float(x[col(2 * (c + e))]), a.scale2, nms));
-            const float p1 =
-                ex2_approx(fmaf(__uint_as_float(x[col(2 * (c + e) + 1)]), a.scale2, nms));
+            const float p0 = ex2_approx(fmaf(__uint_as_float(x[2 * (c + e)]), a.scale2, nms));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(x[2 * (c + e) + 1]), a.scale2, nms));
             if (e & 1)
               sum1 += p0 + p1;
             else

@@ -7,9 +7,9 @@
 // group) pairs, are the rows of a product with the prefix's keys: up to 256 of them
 // (two 128-row tiles) are an item.  The work is cut into units, a key tile of an item,
 // in the order (group, key head, query tile pair, key tile), and each of the
-// persistent CTAs (one an SM) takes an equal run of units, so one long prompt and
-// many short ones alike fill the GPU.  An item that several CTAs share has a partial
-// result from each.
+// persistent CTAs (at most one an SM) takes an equal run of units, so one long prompt
+// and many short ones alike fill the GPU.  An item that several CTAs share has a
+// partial result from each.
 //
 // Keys.  A page (16 tokens of one head) arrives in one copy, as two halves of [d / 64
 // atoms][8 rows][128 bytes]: the eight-row groups of consecutive pages are evenly spaced,
@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
   __shared__ int s_cnt[kBuckets];
   __shared__ int s_entry[kEntries];
   __shared__ long long s_part[kPlanThreads / 32];
+  __shared__ int s_items, s_longest;
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int* entry = a.B <= kEntries ? s_entry : a.entry;  // where a row stands in the list
@@ -128,6 +129,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     a.rowinfo[b] = make_int4(-1, 0, 0, 0);
   }
   s_cnt[tid] = 0;
+  if (tid == 0) s_items = s_longest = 0;
   // offsets that decrease or leave the list: no group is used
   bool bad = false;
 #pragma unroll 1
@@ -201,8 +203,13 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     long long v = 0, all;
     if (g < n_groups) {
       const int4 info = a.info[g];
-      v = static_cast<long long>(ceil_div(info.z, a.tile_rows)) * a.Hkv *
-          ceil_div(info.x, a.tile_pages);
+      const int tiles = ceil_div(info.x, a.tile_pages);
+      v = static_cast<long long>(ceil_div(info.z, a.tile_rows)) * a.Hkv;
+      if (tiles > 0) {
+        atomicMax(&s_longest, tiles);
+        atomicAdd(&s_items, static_cast<int>(min(v, 1024LL)));
+      }
+      v *= tiles;
     }
     const long long before = block_scan(v, s_part, &all);
     if (g < n_groups) a.base[g] = units + before;
@@ -221,9 +228,21 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     for (int b = tid; b < a.B; b += kPlanThreads)
       a.order[atomicAdd(&s_cnt[min(bucket(b), kBuckets - 1)], 1)] = b;
   }
-  // where each CTA begins; with fewer units than CTAs the last CTAs have none, the others one
+  // Where each CTA begins.  Every part of an item costs a load of its queries and a partial
+  // result that the merge reads, so p parts of t key tiles take about t / p + p: not fewer
+  // than sqrt(t) tiles a CTA, and where all items are alike, CTAs that end with an item.  CTAs
+  // without units leave their SMs to the rows' own keys.  (64 rows of 32 heads over 8,
+  // prefixes of 2,048 and 8,192 tokens: 40 and 46 us; with all CTAs and runs that end
+  // anywhere 47 and 57.)
   if (tid <= a.ctas) {
-    const long long n = min(units, static_cast<long long>(a.ctas));
+    // (items past 1,024 a group are not counted: then they are more than CTAs)
+    const int items = s_items;
+    const int least = max(static_cast<int>(ceilf(sqrtf(s_longest))), 1);
+    int n = a.ctas;
+    if (units < static_cast<long long>(least) * n)
+      n = min(n, max(items, static_cast<int>(units) / least));
+    if (items > 0 && items <= n && static_cast<long long>(s_longest) * items == units)
+      n -= n % items;
     const long long at = tid < n ? divide(units * tid, n) : units;
     a.runs[tid] = at;
     if (at < units) {

@@ -1145,13 +1145,13 @@ def attn_decode_mass_workspace_size(B: int, Hq: int, d: int, max_pages: int,
 
 def attn_decode_paged_mass(q, k_pages, v_pages, page_table, seqlens, mass, positions=None,
                            last_positions=None, o=None, lse=None, *, mass_out=None,
-                           sink_logit=None, num_splits=8, scale=None, workspace=None, stream=None,
-                           want_lse=True):
+                           sink_logit=None, num_splits=None, scale=None, workspace=None,
+                           stream=None, want_lse=True):
     """attn_decode_paged (with sink_logit: attn_decode_paged_sink), and the softmax weight of
     every key, summed over the query heads that read it, added to mass [B,Hkv,slots] fp32
     (into mass_out if given, else in place).  The newest token's mass starts here, and its
     slot of positions [B,Hkv,slots] int32 becomes last_positions [B] (None: its slot's
-    number) -> (o, lse)."""
+    number).  num_splits None: enough to fill the GPU -> (o, lse)."""
     index, B, Hq, d, P, page, Hkv, rows, W = _paged(q, k_pages, v_pages, page_table, seqlens)
     if rows != B:
         raise ValueError("page_table must be [B, max_pages] and seqlens [B]")
@@ -1164,7 +1164,13 @@ def attn_decode_paged_mass(q, k_pages, v_pages, page_table, seqlens, mass, posit
                                           sink_logit=sink_logit, num_splits=num_splits,
                                           scale=scale, workspace=workspace, want_lse=want_lse)
     o, lse = _decode_outputs(q, o, lse, want_lse, index)
-    num_splits = _c_int(int(num_splits))
+    if num_splits is None:
+        # 512 CTAs and more, of four pages and more each.  (One row of 30,000 tokens, 8 key
+        # heads: 32 splits 35 us, 8 splits 72; 16 rows of 500 to 2,000: 5 splits 30, 8
+        # splits 32; 200 rows of 100 to 2,000: 1 split 159, 8 splits 202.)
+        num_splits = max(1, min(32, W // 4, 512 // max(1, B * Hkv) + 1))
+    else:
+        num_splits = _c_int(int(num_splits))
     ws = _bytes(attn_decode_mass_workspace_size(B, Hq, d, W, num_splits), index, workspace)
     rc = lib.attn_decode_paged_mass(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),

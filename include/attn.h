@@ -573,7 +573,8 @@ ATTN_API int attn_pages_compact(int* page_table, const int* seqlens, int* refs, 
  *   used); a row index out of [0, B) (skipped) or listed twice (it belongs where
  *   it stands first); a prefix below 0 (0) or past the table (the longest row's
  *   length); a length out of range (taken into [0, max_pages_per_seq * 16]).  A
- *   page out of range reads page 0 in the prefix, zeros in a row's own pages.
+ *   page out of range reads zeros.
+ *   Groups that share too little to gain by it are decoded row by row.
  *   Partial results are merged in a fixed order: repeated calls give identical
  *   bits.
  *   workspace: attn_decode_shared_workspace_size(...) bytes (0 on invalid

@@ -178,6 +178,24 @@ def test_bad_groups_are_reported_and_change_nothing():
     b.run()
 
 
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 1, 64), (8, 2, 128), (6, 2, 256), (24, 3, 128)])
+def test_groups_large_enough_to_share(Hq, Hkv, d):
+    """Prefixes on both sides of what sharing is worth, and bad pages in them."""
+    b = Batch([(700, [700 + i for i in range(9)]), (16, [17 + i for i in range(40)]),
+               (260, [261, 300, 280, 259, 3, 0, 290, 266, 270]), (2100, [2120]), (48, [50, 60])],
+              Hq, Hkv, d, alone=[5, 700], seed=d + Hq)
+    b.run(sink=True)
+    c = Batch([(700, [704] * 40)], Hq, Hkv, d, seed=d)
+    for row in c.rows:
+        c.table[row][1], c.table[row][7] = -1, c.P
+    o, lse = c.run(status=ea.ATTN_ERR_BAD_INPUT, check=False)
+    unused = next(p for p in range(c.P) if all(p not in t for t in c.table))
+    c.k[unused] = c.v[unused] = 0
+    for row in c.rows:
+        c.table[row][1] = c.table[row][7] = unused
+    c.check(o, lse)
+
+
 def test_lengths_and_pages_out_of_range():
     b = Batch([(64, [70, 65, 64])], 4, 2, 128, seed=9)
     b.lens[b.rows[1]] = -7
@@ -189,8 +207,10 @@ def test_lengths_and_pages_out_of_range():
         for row in c.rows:
             c.table[row][1] = page
         o, lse = c.run(status=ea.ATTN_ERR_BAD_INPUT, check=False)
+        unused = next(p for p in range(c.P) if all(p not in t for t in c.table))
+        c.k[unused] = c.v[unused] = 0            # such a page reads zeros
         for row in c.rows:
-            c.table[row][1] = 0
+            c.table[row][1] = unused
         c.check(o, lse)
 
 

@@ -159,28 +159,42 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     }
   }
   __syncthreads();
-  // a warp for each group: its longest row, the pages it shares
+  // Some lanes for each group: its longest row, the pages it shares.  A warp, or as many lanes
+  // as a group has rows on average where there are more groups than warps (2,000 groups of one
+  // row by a warp each took 45 us).
+  int bits = 5;
+  if (n_groups > kPlanThreads / 32) {
+    const int entries = a.cu_groups[n_groups] - a.cu_groups[0];
 #pragma unroll 1
-  for (int g = warp; g < n_groups; g += kPlanThreads / 32) {
-    const int e0 = a.cu_groups[g], e1 = a.cu_groups[g + 1], prefix = a.prefix_lens[g];
-    int best = -1, at = INT_MAX;
+    while (bits > 0 && static_cast<long long>(n_groups) << (bits - 1) >= entries) --bits;
+  }
+  const int lanes = 1 << bits, part = tid & (lanes - 1);
 #pragma unroll 1
-    for (int e = e0 + lane; e < e1; e += 32) {
+  for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads >> bits) {
+    const int g = g0 + (tid >> bits);
+    int e0 = 0, e1 = 0, prefix = 0;
+    if (g < n_groups) e0 = a.cu_groups[g], e1 = a.cu_groups[g + 1], prefix = a.prefix_lens[g];
+    long long best = -1;  // length and, downwards, row
+#pragma unroll 1
+    for (int e = e0 + part; e < e1; e += lanes) {
       const int b = a.rows ? a.rows[e] : e;
       if (b < 0 || b >= a.B || entry[b] != e) continue;
-      const int L = row_length(a, b);
-      if (L > best) best = L, at = b;
+      best = max(best, static_cast<long long>(row_length(a, b)) << 32 | (INT_MAX - b));
     }
-    const int longest = __reduce_max_sync(0xffffffffu, best);
-    at = __reduce_min_sync(0xffffffffu, best == longest ? at : INT_MAX);
-    if (lane == 0 && (prefix < 0 || prefix > a.max_pages * kPage))
+#pragma unroll 1
+    for (int o = lanes / 2; o > 0; o >>= 1)
+      best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+    const int longest = static_cast<int>(best >> 32);
+    const int at = static_cast<int>(INT_MAX - static_cast<uint32_t>(best));  // of any row
+    if (g >= n_groups) continue;  // (the last groups' warps: nothing below is done together)
+    if (part == 0 && (prefix < 0 || prefix > a.max_pages * kPage))
       atomicOr(a.status, kStatusBadInput);
     int pages = prefix < 0 ? 0 : min(prefix, max(longest, 0)) / kPage;
     // Too little to share: every row for itself.
     if (static_cast<long long>(max(e1 - e0 - 1, 1)) * pages < a.least) pages = 0;
-    if (lane == 0) a.info[g] = make_int4(pages, e0, (e1 - e0) * a.G, at);
+    if (part == 0) a.info[g] = make_int4(pages, e0, (e1 - e0) * a.G, at);
 #pragma unroll 1
-    for (int e = e0 + lane; e < e1; e += 32) {
+    for (int e = e0 + part; e < e1; e += lanes) {
       const int b = a.rows ? a.rows[e] : e;
       if (b < 0 || b >= a.B || entry[b] != e) continue;
       a.start[b] = min(pages, (row_length(a, b) + kPage - 1) / kPage);

@@ -196,6 +196,15 @@ def test_groups_large_enough_to_share(Hq, Hkv, d):
     c.check(o, lse)
 
 
+@pytest.mark.parametrize("groups,most", [(40, 1), (100, 2), (70, 7), (600, 1), (33, 20)])
+def test_more_groups_than_warps(groups, most):
+    rows = [1 + 7 * g % most for g in range(groups)]
+    b = Batch([(16 * (g % 5) + 200 * (g % 9 == 8), [16 * (g % 5) + 200 * (g % 9 == 8) + g % 3 + i
+                                                    for i in range(n)])
+               for g, n in enumerate(rows)], 4, 2, 64, alone=[3, 40], seed=groups)
+    b.run()
+
+
 def test_lengths_and_pages_out_of_range():
     b = Batch([(64, [70, 65, 64])], 4, 2, 128, seed=9)
     b.lens[b.rows[1]] = -7

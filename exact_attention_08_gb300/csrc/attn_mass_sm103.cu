@@ -835,9 +835,16 @@ __global__ void __launch_bounds__(kAddThreads) attn_mass_add_kernel(const MassAr
 #pragma unroll
   for (int j = 0; j < kAddTiles; ++j) {
 #pragma unroll 1
-    for (int c = c0[j] + 1; c <= c1[j]; ++c)
+    for (int c = c0[j] + 1; c <= c1[j]; c += 4) {  // four CTAs' in flight
+      float v[4 * kHalves];
 #pragma unroll
-      for (int i = 0; i < kHalves; ++i) w[j] += part[(static_cast<size_t>(j + c) * kHalves + i) * kKeys];
+      for (int i = 0; i < 4 * kHalves; ++i)
+        v[i] = c + i / kHalves <= c1[j]
+                   ? part[(static_cast<size_t>(j + c) * kHalves + i) * kKeys]
+                   : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4 * kHalves; ++i) w[j] += v[i];
+    }
     const int t = t0 + j * kAddThreads + tid;
     if (t >= s.L) break;
     const bool is_new = t >= s.L - fresh;

@@ -86,8 +86,10 @@ constexpr int kLeastShared = 8192;
 // the order of their own pages, longest first.  Steps that depend on one another, so
 // latency is all of it: what later kernels would have to work out again is written down
 // as records of 16 bytes.
-constexpr int kPlanThreads = 1024;
-constexpr int kBuckets = kPlanThreads;
+// Threads of the plan's block: every instruction costs it eight cycles with 32 warps, four with
+// 16, and steps over the rows or groups take more of them only when those are many
+// (2,000 groups of one row: 69 us with 32 warps, 73 with 16; 64 rows 46.0 and 45.2).
+constexpr int kPlanThreads = 512, kPlanMost = 1024, kPlanRows = 1024;
 constexpr int kEntries = 4096;  // rows whose list entries fit in shared memory
 
 __device__ __forceinline__ int row_length(const SharedArgs& a, int b) {
@@ -100,6 +102,7 @@ __device__ __forceinline__ int ceil_div(int x, int y) { return (x + y - 1) / y; 
 __device__ __noinline__ long long divide(long long x, long long y) { return x / y; }
 
 // Sum before this thread and over the block.
+template <int kThreads>
 __device__ __noinline__ long long block_scan(long long v, long long* part, long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long x = v;
@@ -111,7 +114,7 @@ __device__ __noinline__ long long block_scan(long long v, long long* part, long 
   __syncthreads();
   if (lane == 31) part[warp] = x;
   __syncthreads();
-  const long long p = part[lane];
+  const long long p = lane < kThreads / 32 ? part[lane] : 0;
   long long sum = p;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -122,16 +125,17 @@ __device__ __noinline__ long long block_scan(long long v, long long* part, long 
   return __shfl_sync(0xffffffffu, sum - p, warp) + x - v;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const SharedArgs a) {
-  __shared__ int s_cnt[kBuckets];
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) attn_shared_plan_kernel(const SharedArgs a) {
+  __shared__ int s_cnt[kThreads];
   __shared__ int s_entry[kEntries];
-  __shared__ long long s_part[kPlanThreads / 32];
+  __shared__ long long s_part[kThreads / 32];
   __shared__ int s_items, s_longest;
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int* entry = a.B <= kEntries ? s_entry : a.entry;  // where a row stands in the list
 #pragma unroll 1
-  for (int b = tid; b < a.B; b += kPlanThreads) {
+  for (int b = tid; b < a.B; b += kThreads) {
     entry[b] = INT_MAX;
     a.start[b] = 0;
     a.rowinfo[b] = make_int4(-1, 0, 0, 0);
@@ -141,7 +145,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
   // offsets that decrease or leave the list: no group is used
   bool bad = false;
 #pragma unroll 1
-  for (int g = tid; g <= a.n_groups; g += kPlanThreads) {
+  for (int g = tid; g <= a.n_groups; g += kThreads) {
     const int c = a.cu_groups[g];
     bad |= c < 0 || c > a.n_rows || (g > 0 && c < a.cu_groups[g - 1]);
   }
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
   if (n_groups > 0) {
     const int e1 = a.cu_groups[n_groups];
 #pragma unroll 1
-    for (int e = a.cu_groups[0] + tid; e < e1; e += kPlanThreads) {
+    for (int e = a.cu_groups[0] + tid; e < e1; e += kThreads) {
       const int b = a.rows ? a.rows[e] : e;
       if (b < 0 || b >= a.B || atomicMin(&entry[b], e) != INT_MAX)
         atomicOr(a.status, kStatusBadInput);
@@ -163,14 +167,14 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
   // as a group has rows on average where there are more groups than warps (2,000 groups of one
   // row by a warp each took 45 us).
   int bits = 5;
-  if (n_groups > kPlanThreads / 32) {
+  if (n_groups > kThreads / 32) {
     const int entries = a.cu_groups[n_groups] - a.cu_groups[0];
 #pragma unroll 1
     while (bits > 0 && static_cast<long long>(n_groups) << (bits - 1) >= entries) --bits;
   }
   const int lanes = 1 << bits, part = tid & (lanes - 1);
 #pragma unroll 1
-  for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads >> bits) {
+  for (int g0 = 0; g0 < n_groups; g0 += kThreads >> bits) {
     const int g = g0 + (tid >> bits);
     int e0 = 0, e1 = 0, prefix = 0;
     if (g < n_groups) e0 = a.cu_groups[g], e1 = a.cu_groups[g + 1], prefix = a.prefix_lens[g];
@@ -205,22 +209,22 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
   // rows by own pages, longest first (a counting sort, of several page counts a bucket where
   // there are more than buckets; rows of one bucket in any order, which only says which
   // CTA runs first)
-  const int shift = max(0, 32 - __clz(a.max_pages) - 10);
+  const int shift = max(0, 32 - __clz(a.max_pages) - (kThreads == 512 ? 9 : 10));
   auto bucket = [&](int b) {
     return (a.max_pages - ((row_length(a, b) + kPage - 1) / kPage - a.start[b])) >> shift;
   };
-  const bool one = a.B <= kPlanThreads;  // a thread a row
-  const int mine = one && tid < a.B ? min(bucket(tid), kBuckets - 1) : 0;
+  const bool one = a.B <= kThreads;  // a thread a row
+  const int mine = one && tid < a.B ? min(bucket(tid), kThreads - 1) : 0;
   if (one) {
     if (tid < a.B) atomicAdd(&s_cnt[mine], 1);
   } else {
 #pragma unroll 1
-    for (int b = tid; b < a.B; b += kPlanThreads) atomicAdd(&s_cnt[min(bucket(b), kBuckets - 1)], 1);
+    for (int b = tid; b < a.B; b += kThreads) atomicAdd(&s_cnt[min(bucket(b), kThreads - 1)], 1);
   }
   // units before each group
   long long units = 0;
 #pragma unroll 1
-  for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
+  for (int g0 = 0; g0 < n_groups; g0 += kThreads) {
     const int g = g0 + tid;
     long long v = 0, all;
     if (g < n_groups) {
@@ -233,13 +237,13 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
       }
       v *= tiles;
     }
-    const long long before = block_scan(v, s_part, &all);
+    const long long before = block_scan<kThreads>(v, s_part, &all);
     if (g < n_groups) a.base[g] = units + before;
     units += all;
   }
   __syncthreads();
   long long all;
-  const int before = static_cast<int>(block_scan(s_cnt[tid], s_part, &all));
+  const int before = static_cast<int>(block_scan<kThreads>(s_cnt[tid], s_part, &all));
   __syncthreads();
   s_cnt[tid] = before;
   __syncthreads();
@@ -247,8 +251,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     if (tid < a.B) a.order[atomicAdd(&s_cnt[mine], 1)] = tid;
   } else {
 #pragma unroll 1
-    for (int b = tid; b < a.B; b += kPlanThreads)
-      a.order[atomicAdd(&s_cnt[min(bucket(b), kBuckets - 1)], 1)] = b;
+    for (int b = tid; b < a.B; b += kThreads)
+      a.order[atomicAdd(&s_cnt[min(bucket(b), kThreads - 1)], 1)] = b;
   }
   // Where each CTA begins.  Every part of an item costs a load of its queries and a partial
   // result that the merge reads, so p parts of t key tiles take about t / p + p: not fewer
@@ -890,7 +894,11 @@ cudaError_t launch_shared(SharedArgs a, const DecodeLaunch& dec, int num_sms,
   static SharedMemoryLimit limit;
   cudaError_t e = limit.raise(attn_shared_prefix_kernel<D>, C::kSmem);
   if (e != cudaSuccess) return e;
-  attn_shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  const int rows = std::max(a.B, a.n_groups);
+  if (rows <= kPlanRows)
+    attn_shared_plan_kernel<kPlanThreads><<<1, kPlanThreads, 0, stream>>>(a);
+  else
+    attn_shared_plan_kernel<kPlanMost><<<1, kPlanMost, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   e = launch_dependent(attn_shared_prefix_kernel<D>, dim3(a.ctas), kThr, C::kSmem, stream, a.tmK,
                        a.tmV, a);

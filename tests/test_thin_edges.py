@@ -165,3 +165,21 @@ def test_replays_on_other_lengths_and_groups():
         assert (a[0].float() - ro.float()).abs().max() <= 2e-3 + 2 * 2.0 ** -8 * ro.abs().max()
         seen = c.ln > 0
         assert (a[1] - rl)[seen].abs().max() <= 2e-5
+
+
+@pytest.mark.parametrize("B,size", [(1100, 1), (1500, 7), (5000, 5000), (1024, 512)])
+def test_many_rows(B, size):
+    """Groups of `size` rows of a cache whose rows all share 12 pages, against the decode row by
+    row: each within its bounds of the exact values."""
+    c = Cache(B, 4, 2, 64, [(37 * b) % 300 for b in range(B)], 12, seed=B)
+    g = torch.Generator().manual_seed(B)
+    rows = torch.randperm(B, generator=g).int().cuda()
+    cu = list(range(0, B, size)) + [B]
+    o, lse = ea.attn_decode_paged_shared(*c.paged(), i32(cu), i32([192] * (len(cu) - 1)), rows)
+    ro, rl = ea.attn_decode_paged(*c.paged(), num_splits=2)
+    torch.cuda.synchronize()
+    assert ea.attn_device_status() == ea.ATTN_OK
+    seen = c.ln > 0
+    assert (o.float() - ro.float()).abs().max() <= 2e-3 + 2 * 2.0 ** -8 * ro.abs().max()
+    assert (lse - rl)[seen].abs().max() <= 2e-5
+    assert torch.isneginf(lse[~seen]).all() and (o[~seen] == 0).all()

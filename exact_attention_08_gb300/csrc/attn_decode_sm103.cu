@@ -765,7 +765,7 @@ cudaError_t launch_combine(const DecodeLaunch& a, cudaStream_t stream) {
 // Accumulated attention weight of a decode step, and the merge, in one launch:
 // both need every split's log-sum-exp.  Of the blocks along x the first merge_blocks
 // merge (the arithmetic of attn_decode_combine_kernel, kMassThreads / D query heads
-// each), the others take kMassTokens tokens each: they merge the log-sum-exps
+// each), the others take kMassTokens tokens at a time: they merge the log-sum-exps
 // of the group's heads (a warp a head), then w = sum over the heads of
 // 2^(s scale2 - LSE log2 e), heads in order, and mass_out = mass + w.  The newest
 // token's mass is w alone, and its position is noted.  Bound by bytes: the raw scores
@@ -812,52 +812,55 @@ __global__ void __launch_bounds__(kMassThreads)
     if (tid == 0) atomicOr(a.status, kStatusBadInput);
     return;
   }
-  const int t0 = (blockIdx.x - merge_blocks) * kMassTokens;
-  if (t0 >= L) return;
   const size_t slots = static_cast<size_t>(a.max_pages) * kPage;
   const float scale2 = a.scale * kLog2eDec;
   const int warp = tid >> 5, lane = tid & 31;
-  float w[4] = {0.f, 0.f, 0.f, 0.f};
-  const int t = t0 + tid * 4;  // the raw scores of a token beyond L are -inf or not read
-  for (int c = 0; c < G; c += kMassHeads) {
-    const int n = min(G - c, kMassHeads);
-    __syncthreads();
-    for (int g = warp; g < n; g += kMassThreads / 32) {
-      const float* ls = a.ws_lse + (row0 + c + g) * S;
-      const float sg = a.sink ? a.sink[hkv * G + c + g] : -INFINITY;
-      const float l0 = lane < S ? ls[lane] : -INFINITY;
-      const float l1 = lane + 32 < S ? ls[lane + 32] : -INFINITY;
-      float M = fmaxf(fmaxf(l0, l1), sg);
+  bool merged = false;  // the log-sum-exps of all heads are in s_lse2
+#pragma unroll 1
+  for (int t0 = (blockIdx.x - merge_blocks) * kMassTokens; t0 < L;
+       t0 += (gridDim.x - merge_blocks) * kMassTokens) {
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
+    const int t = t0 + tid * 4;  // the raw scores of a token beyond L are -inf or not read
+    for (int c = 0; c < G; c += kMassHeads) {
+      const int n = min(G - c, kMassHeads);
+      if (!merged) __syncthreads();
+      for (int g = merged ? n : warp; g < n; g += kMassThreads / 32) {
+        const float* ls = a.ws_lse + (row0 + c + g) * S;
+        const float sg = a.sink ? a.sink[hkv * G + c + g] : -INFINITY;
+        const float l0 = lane < S ? ls[lane] : -INFINITY;
+        const float l1 = lane + 32 < S ? ls[lane + 32] : -INFINITY;
+        float M = fmaxf(fmaxf(l0, l1), sg);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      float sum = expf(l0 - M) + expf(l1 - M);
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float sum = expf(l0 - M) + expf(l1 - M);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      sum += expf(sg - M);
-      if (lane == 0) s_lse2[g] = (M + logf(sum)) * kLog2eDec;
-    }
-    __syncthreads();
-    if (t < L) {
-      const float* sc = a.ws_scores + (row0 + c) * slots + t;
-      for (int g = 0; g < n; ++g) {
-        const float4 x = *reinterpret_cast<const float4*>(sc + g * slots);
-        const float l2 = s_lse2[g];
-        w[0] += ex2_approx(fmaf(x.x, scale2, -l2));
-        w[1] += ex2_approx(fmaf(x.y, scale2, -l2));
-        w[2] += ex2_approx(fmaf(x.z, scale2, -l2));
-        w[3] += ex2_approx(fmaf(x.w, scale2, -l2));
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sum += expf(sg - M);
+        if (lane == 0) s_lse2[g] = (M + logf(sum)) * kLog2eDec;
+      }
+      if (!merged) __syncthreads();
+      merged = G <= kMassHeads;
+      if (t < L) {
+        const float* sc = a.ws_scores + (row0 + c) * slots + t;
+        for (int g = 0; g < n; ++g) {
+          const float4 x = *reinterpret_cast<const float4*>(sc + g * slots);
+          const float l2 = s_lse2[g];
+          w[0] += ex2_approx(fmaf(x.x, scale2, -l2));
+          w[1] += ex2_approx(fmaf(x.y, scale2, -l2));
+          w[2] += ex2_approx(fmaf(x.z, scale2, -l2));
+          w[3] += ex2_approx(fmaf(x.w, scale2, -l2));
+        }
       }
     }
-  }
-  if (t >= L) return;
-  const size_t at = (static_cast<size_t>(b) * a.Hkv + hkv) * a.mass_slots + t;
+    const size_t at = (static_cast<size_t>(b) * a.Hkv + hkv) * a.mass_slots + t;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (t + j >= L) break;
-    const bool newest = t + j == L - 1;
-    a.mass_out[at + j] = newest ? w[j] : a.mass[at + j] + w[j];
-    if (newest && a.positions != nullptr)
-      a.positions[at + j] = a.last_positions ? a.last_positions[b] : L - 1;
+    for (int j = 0; j < 4; ++j) {
+      if (t + j >= L) break;
+      const bool newest = t + j == L - 1;
+      a.mass_out[at + j] = newest ? w[j] : a.mass[at + j] + w[j];
+      if (newest && a.positions != nullptr)
+        a.positions[at + j] = a.last_positions ? a.last_positions[b] : L - 1;
+    }
   }
 }
 
@@ -955,8 +958,13 @@ cudaError_t launch_dec_mass(DecodeLaunch a, int num_sms, cudaStream_t stream) {
   const int merge_blocks = (G + per - 1) / per;
   const long long slots = std::min<long long>(static_cast<long long>(a.max_pages) * kPage,
                                               a.mass_slots);
-  const dim3 grid(static_cast<unsigned>(merge_blocks + (slots + kMassTokens - 1) / kMassTokens),
-                  a.Hkv, a.B);
+  // As many blocks as fill the GPU a few times: the table may be far wider than its rows are
+  // long (64 rows of 1,000 tokens in a table of 32,768 pages: 185 us with a block for every
+  // 1,024 slots).
+  const long long units = static_cast<long long>(a.Hkv) * a.B;
+  const long long tiles = std::min((slots + kMassTokens - 1) / kMassTokens,
+                                   (32LL * num_sms + units - 1) / units);
+  const dim3 grid(static_cast<unsigned>(merge_blocks + tiles), a.Hkv, a.B);
   return launch_dependent(attn_decode_mass_kernel<D>, grid, kMassThreads, 0, stream, a,
                           merge_blocks);
 }

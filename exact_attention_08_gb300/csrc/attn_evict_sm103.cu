@@ -122,6 +122,24 @@ __device__ __forceinline__ void copy_moves(const EvictArgs& a, int layer, int h,
   }
 }
 
+// Whether a row is to be cut that has more than `from` tokens and `to` at most.
+__device__ __forceinline__ bool any_row(const EvictArgs& a, int from, int to) {
+  bool any = false;
+#pragma unroll 1
+  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+    const int L = a.seqlens[b];
+    any |= L > from && L <= to;
+  }
+  return __syncthreads_or(any);
+}
+
+// Selecting kernels for other lengths run side by side (each started by the one before): the
+// first block of each leaves only when the kernel before it is done, so that what follows the
+// last one follows them all.
+__device__ __forceinline__ void leave_last() {
+  if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Rows of any length: the keys are formed again for every step.  What bounds it is the loads one
 // CTA has in flight: 1,024 threads with four tokens each take a row of 100,000 tokens in
 // 163 us, 512 threads with one in 575.
@@ -131,199 +149,195 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_long_kernel(const 
   __shared__ int s_flag, s_newest, s_bin, s_above;
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int unit = blockIdx.x;
-  const int h = unit % a.Hkv, b = (unit / a.Hkv) % a.B, layer = unit / (a.Hkv * a.B);
-  const int L = a.seqlens[b], K = a.keep[b];
-  const int cap = min(a.slots, a.max_pages * kPage);
-  const bool lead = h == 0 && layer == 0;
-  const bool bad = L < 0 || L > cap || K < 0;
-  if (bad || K >= L || K == 0) {
-    if (tid == 0) {
-      *unit_count(a, unit) = 0;
-      if (lead) a.new_seqlens[b] = (bad || K >= L) ? L : 0;
-      if (bad) atomicOr(a.status, kStatusBadInput);
-    }
-    return;
-  }
-  if (tid == 0) {
-    s_flag = 0;
-    s_newest = INT32_MIN;
-  }
-  __syncthreads();
-  // Every page of the row must be one of the pool, and the pages written to must
-  // be the row's alone.
-  {
-    const int* row = a.page_table + static_cast<size_t>(b) * a.max_pages;
-    const int pages = (L + kPage - 1) / kPage, written = (K + kPage - 1) / kPage;
-    bool wrong = false;
+  const bool any = any_row(a, kMaxCached, INT32_MAX);
 #pragma unroll 1
-    for (int i = tid; i < pages; i += kThreads) {
-      const int p = row[i];
-      if (p < 0 || p >= a.num_pages)
-        wrong = true;
-      else if (a.refs != nullptr && i < written && a.refs[p] > 1)
-        wrong = true;
-    }
-    if (wrong) s_flag = 1;
-  }
-  float* mass = a.mass + static_cast<size_t>(unit) * a.slots;
-  int* pos = a.positions + static_cast<size_t>(unit) * a.slots;
-  if (a.recent > 0) {
-    int newest = INT32_MIN;
-#pragma unroll 4
-    for (int t = tid; t < L; t += kThreads) newest = max(newest, pos[t]);
-    newest = __reduce_max_sync(0xffffffffu, newest);
-    if (lane == 0) atomicMax(&s_newest, newest);
-  }
-  __syncthreads();
-  if (s_flag) {
-    if (tid == 0) {
-      *unit_count(a, unit) = 0;
-      if (lead) a.new_seqlens[b] = L;
-      atomicOr(a.status, kStatusBadInput);
-    }
-    return;
-  }
-  const long long recent_from =
-      a.recent > 0 ? static_cast<long long>(s_newest) - a.recent : INT64_MAX;
-  // The keys of this lane's tokens of the 128 from t on: t + lane, t + 32 + lane, ...  All loads
-  // are in flight together; a token past the row's last gets the key of that one.
-  auto make_keys = [&](int t, uint32_t (&key)[4]) {
-    int p[4];
-    float m[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int at = min(t + 32 * j + lane, L - 1);
-      p[j] = pos[at];
-      m[j] = mass[at];
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      key[j] = (p[j] < a.n_sink || p[j] > recent_from) ? kProtected : mass_key(m[j]);
-  };
-
-  // ---- the K-th largest key: its bits from the top, 11, 11 and 10 of them
-  uint32_t prefix = 0;
-  int want = K;  // how many are still to be found among the keys that share the prefix
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const int bits = pass == 2 ? 10 : 11;
-#pragma unroll 1
-    for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
+  for (int unit = blockIdx.x; any && unit < a.units; unit += gridDim.x) {
     __syncthreads();
-    const uint32_t mask = (1u << bits) - 1u;
+    const int h = unit % a.Hkv, b = (unit / a.Hkv) % a.B, layer = unit / (a.Hkv * a.B);
+    const int L = a.seqlens[b], K = a.keep[b];
+    const int cap = min(a.slots, a.max_pages * kPage);
+    const bool lead = h == 0 && layer == 0;
+    if (L <= kMaxCached || L > cap || K <= 0 || K >= L) continue;  // not one of this kernel's
+    if (tid == 0) {
+      s_flag = 0;
+      s_newest = INT32_MIN;
+    }
+    __syncthreads();
+    // Every page of the row must be one of the pool, and the pages written to must
+    // be the row's alone.
+    {
+      const int* row = a.page_table + static_cast<size_t>(b) * a.max_pages;
+      const int pages = (L + kPage - 1) / kPage, written = (K + kPage - 1) / kPage;
+      bool wrong = false;
 #pragma unroll 1
-    for (int t = warp * 128; t < L; t += kWarps * 128) {
-      uint32_t key[4];
-      make_keys(t, key);
+      for (int i = tid; i < pages; i += kThreads) {
+        const int p = row[i];
+        if (p < 0 || p >= a.num_pages)
+          wrong = true;
+        else if (a.refs != nullptr && i < written && a.refs[p] > 1)
+          wrong = true;
+      }
+      if (wrong) s_flag = 1;
+    }
+    float* mass = a.mass + static_cast<size_t>(unit) * a.slots;
+    int* pos = a.positions + static_cast<size_t>(unit) * a.slots;
+    if (a.recent > 0) {
+      int newest = INT32_MIN;
+#pragma unroll 4
+      for (int t = tid; t < L; t += kThreads) newest = max(newest, pos[t]);
+      newest = __reduce_max_sync(0xffffffffu, newest);
+      if (lane == 0) atomicMax(&s_newest, newest);
+    }
+    __syncthreads();
+    if (s_flag) {
+      if (tid == 0) {
+        *unit_count(a, unit) = 0;
+        if (lead) a.new_seqlens[b] = L;
+        atomicOr(a.status, kStatusBadInput);
+      }
+      continue;
+    }
+    const long long recent_from =
+        a.recent > 0 ? static_cast<long long>(s_newest) - a.recent : INT64_MAX;
+    // The keys of this lane's tokens of the 128 from t on: t + lane, t + 32 + lane, ...  All loads
+    // are in flight together; a token past the row's last gets the key of that one.
+    auto make_keys = [&](int t, uint32_t (&key)[4]) {
+      int p[4];
+      float m[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t up = pass == 0 ? 0u : key[j] >> (shift + bits);
-        if (t + 32 * j + lane < L && up == prefix) atomicAdd(&s_hist[(key[j] >> shift) & mask], 1);
+        const int at = min(t + 32 * j + lane, L - 1);
+        p[j] = pos[at];
+        m[j] = mass[at];
       }
-    }
-    __syncthreads();
-    // from the largest bin down: the bin in which the want-th key falls
-    constexpr int kPer = kBins / kThreads;
-    int local[kPer], sum = 0;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      local[j] = s_hist[kBins - 1 - (tid * kPer + j)];
-      sum += local[j];
-    }
-    int all;
-    int before = block_scan(sum, s_part, &all);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (before < want && want <= before + local[j]) {
-        s_bin = kBins - 1 - (tid * kPer + j);
-        s_above = before;
-      }
-      before += local[j];
-    }
-    __syncthreads();
-    prefix = (prefix << bits) | static_cast<uint32_t>(s_bin);
-    want -= s_above;
-    __syncthreads();
-  }
-  const uint32_t T = prefix;  // `want` of the tokens with key T stay, the first by slot
+      for (int j = 0; j < 4; ++j)
+        key[j] = (p[j] < a.n_sink || p[j] > recent_from) ? kProtected : mass_key(m[j]);
+    };
 
-  // ---- ranks: every warp owns a run of slots
-  const int run = ((L + kWarps - 1) / kWarps + 31) / 32 * 32;
-  const int t0 = min(warp * run, L), t1 = min(t0 + run, L);
-  const uint32_t below = (1u << lane) - 1u;
-  int ties = 0;
+    // ---- the K-th largest key: its bits from the top, 11, 11 and 10 of them
+    uint32_t prefix = 0;
+    int want = K;  // how many are still to be found among the keys that share the prefix
 #pragma unroll 1
-  for (int t = t0; t < t1; t += 128) {
-    uint32_t key[4];
-    make_keys(t, key);
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const int bits = pass == 2 ? 10 : 11;
+#pragma unroll 1
+      for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
+      __syncthreads();
+      const uint32_t mask = (1u << bits) - 1u;
+#pragma unroll 1
+      for (int t = warp * 128; t < L; t += kWarps * 128) {
+        uint32_t key[4];
+        make_keys(t, key);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      ties += __popc(__ballot_sync(0xffffffffu, t + 32 * j + lane < t1 && key[j] == T));
-  }
-  if (lane == 0) s_part[warp] = ties;
-  __syncthreads();
-  int tie_base = 0;
-#pragma unroll 1
-  for (int w = 0; w < warp; ++w) tie_base += s_part[w];
-  __syncthreads();
-  int2* moves = unit_moves(a, unit);
-  int hole_base = 0, mover_base = 0, total = 0;
-#pragma unroll 1
-  for (int phase = 0; phase < 2; ++phase) {  // count, then write
-    int tie_rank = tie_base, holes = hole_base, movers = mover_base;
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t up = pass == 0 ? 0u : key[j] >> (shift + bits);
+          if (t + 32 * j + lane < L && up == prefix) atomicAdd(&s_hist[(key[j] >> shift) & mask], 1);
+        }
+      }
+      __syncthreads();
+      // from the largest bin down: the bin in which the want-th key falls
+      constexpr int kPer = kBins / kThreads;
+      int local[kPer], sum = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        local[j] = s_hist[kBins - 1 - (tid * kPer + j)];
+        sum += local[j];
+      }
+      int all;
+      int before = block_scan(sum, s_part, &all);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (before < want && want <= before + local[j]) {
+          s_bin = kBins - 1 - (tid * kPer + j);
+          s_above = before;
+        }
+        before += local[j];
+      }
+      __syncthreads();
+      prefix = (prefix << bits) | static_cast<uint32_t>(s_bin);
+      want -= s_above;
+      __syncthreads();
+    }
+    const uint32_t T = prefix;  // `want` of the tokens with key T stay, the first by slot
+
+    // ---- ranks: every warp owns a run of slots
+    const int run = ((L + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int t0 = min(warp * run, L), t1 = min(t0 + run, L);
+    const uint32_t below = (1u << lane) - 1u;
+    int ties = 0;
 #pragma unroll 1
     for (int t = t0; t < t1; t += 128) {
       uint32_t key[4];
       make_keys(t, key);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int at = t + 32 * j + lane;
-        const bool valid = at < t1, tie = valid && key[j] == T;
-        const uint32_t tie_mask = __ballot_sync(0xffffffffu, tie);
-        const bool stays =
-            valid && (key[j] > T || (tie && tie_rank + __popc(tie_mask & below) < want));
-        tie_rank += __popc(tie_mask);
-        const uint32_t hole = __ballot_sync(0xffffffffu, valid && !stays && at < K);
-        const uint32_t mover = __ballot_sync(0xffffffffu, stays && at >= K);
-        if (phase == 1) {
-          if ((hole >> lane) & 1u) moves[holes + __popc(hole & below)].y = at;
-          if ((mover >> lane) & 1u) moves[movers + __popc(mover & below)].x = at;
-        }
-        holes += __popc(hole);
-        movers += __popc(mover);
-      }
+      for (int j = 0; j < 4; ++j)
+        ties += __popc(__ballot_sync(0xffffffffu, t + 32 * j + lane < t1 && key[j] == T));
     }
-    if (phase == 0) {
-      int* s_movers = s_hist;  // free by now
-      if (lane == 0) {
-        s_part[warp] = holes;
-        s_movers[warp] = movers;
-      }
-      __syncthreads();
+    if (lane == 0) s_part[warp] = ties;
+    __syncthreads();
+    int tie_base = 0;
 #pragma unroll 1
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) {
-          hole_base += s_part[w];
-          mover_base += s_movers[w];
+    for (int w = 0; w < warp; ++w) tie_base += s_part[w];
+    __syncthreads();
+    int2* moves = unit_moves(a, unit);
+    int hole_base = 0, mover_base = 0, total = 0;
+#pragma unroll 1
+    for (int phase = 0; phase < 2; ++phase) {  // count, then write
+      int tie_rank = tie_base, holes = hole_base, movers = mover_base;
+#pragma unroll 1
+      for (int t = t0; t < t1; t += 128) {
+        uint32_t key[4];
+        make_keys(t, key);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = t + 32 * j + lane;
+          const bool valid = at < t1, tie = valid && key[j] == T;
+          const uint32_t tie_mask = __ballot_sync(0xffffffffu, tie);
+          const bool stays =
+              valid && (key[j] > T || (tie && tie_rank + __popc(tie_mask & below) < want));
+          tie_rank += __popc(tie_mask);
+          const uint32_t hole = __ballot_sync(0xffffffffu, valid && !stays && at < K);
+          const uint32_t mover = __ballot_sync(0xffffffffu, stays && at >= K);
+          if (phase == 1) {
+            if ((hole >> lane) & 1u) moves[holes + __popc(hole & below)].y = at;
+            if ((mover >> lane) & 1u) moves[movers + __popc(mover & below)].x = at;
+          }
+          holes += __popc(hole);
+          movers += __popc(mover);
         }
-        total += s_part[w];
+      }
+      if (phase == 0) {
+        int* s_movers = s_hist;  // free by now
+        if (lane == 0) {
+          s_part[warp] = holes;
+          s_movers[warp] = movers;
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) {
+            hole_base += s_part[w];
+            mover_base += s_movers[w];
+          }
+          total += s_part[w];
+        }
       }
     }
-  }
-  __syncthreads();
+    __syncthreads();
 #pragma unroll 2
-  for (int i = tid; i < total; i += kThreads) {
-    const int2 m = moves[i];
-    mass[m.y] = mass[m.x];
-    pos[m.y] = pos[m.x];
-    moves[i] = make_int2(pool_row(a, b, m.x), pool_row(a, b, m.y));
-  }
-  if (tid == 0) {
-    *unit_count(a, unit) = total;
-    if (lead) a.new_seqlens[b] = K;
-  }
+    for (int i = tid; i < total; i += kThreads) {
+      const int2 m = moves[i];
+      mass[m.y] = mass[m.x];
+      pos[m.y] = pos[m.x];
+      moves[i] = make_int2(pool_row(a, b, m.x), pool_row(a, b, m.y));
+    }
+    if (tid == 0) {
+      *unit_count(a, unit) = total;
+      if (lead) a.new_seqlens[b] = K;
+    }  }
+  leave_last();
 }
 
 // Sum before this thread and total over a block of up to 16 warps (part: 32 values).
@@ -361,31 +375,17 @@ __device__ __forceinline__ uint32_t lowest_bits(uint32_t x, int n) {
 // kFours: rows of mass and positions start on 16 bytes, four tokens a load.  kCopies: the keys
 // and values are moved here too.
 template <bool kFours, bool kCopies>
-__global__ void __launch_bounds__(kLargeThreads, 4) attn_evict_select_kernel(const EvictArgs a,
-                                                                             int words) {
+__device__ __forceinline__ void select_row(const EvictArgs& a, int words, int unit, int layer, int b,
+                                           int h, int L, int K) {
   extern __shared__ uint32_t s_keys[];
   __shared__ int s_hist[kBins];
   __shared__ int s_group[kBins / 32];
   __shared__ int s_part[32];
   __shared__ long long s_part2[32];
   __shared__ int s_flag, s_newest, s_bin, s_want;
-  asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   const int warps = threads >> 5;
-  const int unit = blockIdx.x;
-  const int h = unit % a.Hkv, b = (unit / a.Hkv) % a.B, layer = unit / (a.Hkv * a.B);
-  const int L = a.seqlens[b], K = a.keep[b];
-  const int cap = min(a.slots, a.max_pages * kPage);
   const bool lead = h == 0 && layer == 0;
-  const bool bad = L < 0 || L > cap || K < 0;
-  if (bad || K >= L || K == 0) {
-    if (tid == 0) {
-      *unit_count(a, unit) = 0;
-      if (lead) a.new_seqlens[b] = (bad || K >= L) ? L : 0;
-      if (bad) atomicOr(a.status, kStatusBadInput);
-    }
-    return;
-  }
   float* mass = a.mass + static_cast<size_t>(unit) * a.slots;
   int* pos = a.positions + static_cast<size_t>(unit) * a.slots;
   if (tid == 0) {
@@ -592,6 +592,45 @@ __global__ void __launch_bounds__(kLargeThreads, 4) attn_evict_select_kernel(con
   }
 }
 
+// Rows of `to` tokens at most, a CTA each, and those that are not cut.
+template <bool kFours, bool kCopies>
+__global__ void __launch_bounds__(kLargeThreads, 4) attn_evict_select_kernel(const EvictArgs a,
+                                                                             int words, int to) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int unit = blockIdx.x;
+  const int h = unit % a.Hkv, b = (unit / a.Hkv) % a.B, layer = unit / (a.Hkv * a.B);
+  const int L = a.seqlens[b], K = a.keep[b];
+  const bool bad = L < 0 || L > min(a.slots, a.max_pages * kPage) || K < 0;
+  if (bad || K >= L || K == 0) {
+    if (threadIdx.x == 0) {
+      *unit_count(a, unit) = 0;
+      if (h == 0 && layer == 0) a.new_seqlens[b] = (bad || K >= L) ? L : 0;
+      if (bad) atomicOr(a.status, kStatusBadInput);
+    }
+    return;
+  }
+  if (L <= to) select_row<kFours, kCopies>(a, words, unit, layer, b, h, L, K);
+}
+
+// Rows of more than kSmallRow tokens, `to` at most.  The table may be far wider than its rows are
+// long, so this kernel is launched beside the one above wherever it could be needed, with
+// as many CTAs as are resident.
+template <bool kFours>
+__global__ void __launch_bounds__(kLargeThreads, 4) attn_evict_select_wide_kernel(
+    const EvictArgs a, int words, int to) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  const bool any = any_row(a, kSmallRow, to);
+#pragma unroll 1
+  for (int unit = blockIdx.x; any && unit < a.units; unit += gridDim.x) {
+    const int h = unit % a.Hkv, b = (unit / a.Hkv) % a.B, layer = unit / (a.Hkv * a.B);
+    const int L = a.seqlens[b], K = a.keep[b];
+    if (L <= kSmallRow || L > to || K <= 0 || K >= L) continue;
+    __syncthreads();
+    select_row<kFours, false>(a, words, unit, layer, b, h, L, K);
+  }
+  leave_last();
+}
+
 // The same by a.copy_blocks blocks a unit.
 template <int kVecs>
 __global__ void __launch_bounds__(kCopyThreads) attn_evict_copy_kernel(const EvictArgs a) {
@@ -629,7 +668,6 @@ __global__ void __launch_bounds__(kCopyThreads) attn_evict_copy_kernel(const Evi
 
 cudaError_t launch_attn_evict(EvictArgs a, int num_sms, cudaStream_t stream) {
   const int cap = std::min(a.slots, a.max_pages * kPage);
-  const bool cached = cap <= kMaxCached;
   // Selecting CTAs that fill the GPU by themselves, of short rows, move their keys and values
   // too; others leave that to a kernel of some sixteen blocks for every SM (and no more than
   // there can be steps).
@@ -641,34 +679,49 @@ cudaError_t launch_attn_evict(EvictArgs a, int num_sms, cudaStream_t stream) {
                       : static_cast<int>(std::max(
                             1LL, std::min(most, (16LL * num_sms + a.units - 1) / a.units)));
   cudaError_t e;
-  if (cached) {
-    const int words = (cap + 31) / 32;
-    static SharedMemoryLimit limits[4];
-    const bool fours = a.slots % 4 == 0 && reinterpret_cast<uintptr_t>(a.mass) % 16 == 0 &&
-                       reinterpret_cast<uintptr_t>(a.positions) % 16 == 0;
-    const bool copies = a.copy_blocks == 0;
-    auto select = fours ? (copies ? attn_evict_select_kernel<true, true>
-                                  : attn_evict_select_kernel<true, false>)
-                        : (copies ? attn_evict_select_kernel<false, true>
-                                  : attn_evict_select_kernel<false, false>);
-    e = limits[2 * fours + copies].raise(select, (kMaxCached + 2 * kMaxCached / 32) * 4);
-    if (e != cudaSuccess) return e;
-    select<<<a.units, cap <= kSmallRow ? kSmallThreads : kLargeThreads,
-             static_cast<size_t>(words) * 34 * 4, stream>>>(a, words);
-  } else {
-    attn_evict_select_long_kernel<<<a.units, kThreads, 0, stream>>>(a);
-  }
-  e = cudaGetLastError();
-  if (e != cudaSuccess || a.copy_blocks == 0) return e;
+  const bool fours = a.slots % 4 == 0 && reinterpret_cast<uintptr_t>(a.mass) % 16 == 0 &&
+                     reinterpret_cast<uintptr_t>(a.positions) % 16 == 0;
+  const bool copies = a.copy_blocks == 0;
+  auto words_of = [](int tokens) { return (tokens + 31) / 32; };
+  auto bytes_of = [](int words) { return static_cast<size_t>(words) * 34 * 4; };
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.copy_blocks) * a.units);
-  cfg.blockDim = dim3(kCopyThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  {
+    const int to = std::min(cap, kSmallRow), words = words_of(to);
+    auto select = fours ? (copies ? attn_evict_select_kernel<true, true>
+                                  : attn_evict_select_kernel<true, false>)
+                        : (copies ? attn_evict_select_kernel<false, true>
+                                  : attn_evict_select_kernel<false, false>);
+    select<<<a.units, kSmallThreads, bytes_of(words), stream>>>(a, words, to);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (cap > kSmallRow) {
+    const int to = std::min(cap, kMaxCached), words = words_of(to);
+    static SharedMemoryLimit limits[2];
+    auto select = fours ? attn_evict_select_wide_kernel<true> : attn_evict_select_wide_kernel<false>;
+    e = limits[fours].raise(select, bytes_of(words_of(kMaxCached)));
+    if (e != cudaSuccess) return e;
+    const int resident =
+        std::max(1, std::min(4, static_cast<int>((224 << 10) / (bytes_of(words) + (11 << 10)))));
+    cfg.gridDim = dim3(std::min(a.units, resident * num_sms));
+    cfg.blockDim = dim3(kLargeThreads);
+    cfg.dynamicSmemBytes = bytes_of(words);
+    if ((e = cudaLaunchKernelEx(&cfg, select, a, words, to)) != cudaSuccess) return e;
+    cfg.dynamicSmemBytes = 0;
+  }
+  if (cap > kMaxCached) {
+    cfg.gridDim = dim3(std::min(a.units, 2 * num_sms));
+    cfg.blockDim = dim3(kThreads);
+    if ((e = cudaLaunchKernelEx(&cfg, attn_evict_select_long_kernel, a)) != cudaSuccess) return e;
+  }
+  if (copies) return cudaSuccess;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.copy_blocks) * a.units);
+  cfg.blockDim = dim3(kCopyThreads);
   auto copy = a.vecs == 8    ? attn_evict_copy_kernel<8>
               : a.vecs == 16 ? attn_evict_copy_kernel<16>
                              : attn_evict_copy_kernel<32>;

@@ -788,68 +788,70 @@ __global__ void __launch_bounds__(kAddThreads) attn_mass_add_kernel(const MassAr
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   Seq s;
   if (!load_seq(a, b, s)) return;
-  const int t0 = blockIdx.x * kAddTokens;
-  if (t0 >= s.L) return;
-  if (tid < kAddTiles) {
-    const int kt = t0 / kKeys + tid, tiles = key_tiles(s);
-    int2 c = make_int2(0, -1);
-    if (kt < tiles) {
-      const long long* cum = ws_cum(a, b);
-      const long long per_head = cum[a.max_kt], T = ws_base(a)[a.B], before = ws_base(a)[b];
-      const long long at = cum[kt], n = (kt + 1 < tiles ? cum[kt + 1] : per_head) - at - kItemCost;
-      if (n > 0) {
-        // of C CTAs with work, position u belongs to CTA ((u + 1) C - 1) / T
-        const long long u = before + per_head * h + at + kItemCost;
-        const long long C = min(T, static_cast<long long>(ctas));
-        c.x = static_cast<int>(((u + 1) * C - 1) / T);
-        c.y = static_cast<int>(((u + n) * C - 1) / T);
-      }
-    }
-    s_ctas[tid] = c;
-  }
   int fresh = a.new_tokens ? a.new_tokens[b] : s.Lq;
   fresh = max(0, min(fresh, s.L));
   const int last = a.last_positions ? a.last_positions[b] : s.L - 1;
   const size_t row = (static_cast<size_t>(b) * a.Hkv + h) * a.slots;
-  float old[kAddTiles];
-#pragma unroll
-  for (int j = 0; j < kAddTiles; ++j) {
-    const int t = t0 + j * kAddThreads + tid;
-    old[j] = t < s.L - fresh ? a.mass[row + t] : 0.f;
-  }
-  __syncthreads();
-  const float* part = a.ws_part +
-                      ((static_cast<size_t>(b) * a.Hkv + h) * a.max_kt + t0 / kKeys) * kHalves * kKeys +
-                      tid;
-  float w[kAddTiles];
-  const int4 c01 = *reinterpret_cast<const int4*>(s_ctas), c23 = *reinterpret_cast<const int4*>(s_ctas + 2);
-  const int c0[kAddTiles] = {c01.x, c01.z, c23.x, c23.z}, c1[kAddTiles] = {c01.y, c01.w, c23.y, c23.w};
-#pragma unroll
-  for (int j = 0; j < kAddTiles; ++j) {
-    const float* p = part + static_cast<size_t>(j + c0[j]) * kHalves * kKeys;
-    w[j] = 0.f;
-    if (c0[j] <= c1[j])
-#pragma unroll
-      for (int i = 0; i < kHalves; ++i) w[j] += p[i * kKeys];
-  }
-#pragma unroll
-  for (int j = 0; j < kAddTiles; ++j) {
 #pragma unroll 1
-    for (int c = c0[j] + 1; c <= c1[j]; c += 4) {  // four CTAs' in flight
-      float v[4 * kHalves];
-#pragma unroll
-      for (int i = 0; i < 4 * kHalves; ++i)
-        v[i] = c + i / kHalves <= c1[j]
-                   ? part[(static_cast<size_t>(j + c) * kHalves + i) * kKeys]
-                   : 0.f;
-#pragma unroll
-      for (int i = 0; i < 4 * kHalves; ++i) w[j] += v[i];
+  for (int t0 = blockIdx.x * kAddTokens; t0 < s.L; t0 += gridDim.x * kAddTokens) {
+    __syncthreads();  // (s_ctas of the tiles before has been read)
+    if (tid < kAddTiles) {
+      const int kt = t0 / kKeys + tid, tiles = key_tiles(s);
+      int2 c = make_int2(0, -1);
+      if (kt < tiles) {
+        const long long* cum = ws_cum(a, b);
+        const long long per_head = cum[a.max_kt], T = ws_base(a)[a.B], before = ws_base(a)[b];
+        const long long at = cum[kt], n = (kt + 1 < tiles ? cum[kt + 1] : per_head) - at - kItemCost;
+        if (n > 0) {
+          // of C CTAs with work, position u belongs to CTA ((u + 1) C - 1) / T
+          const long long u = before + per_head * h + at + kItemCost;
+          const long long C = min(T, static_cast<long long>(ctas));
+          c.x = static_cast<int>(((u + 1) * C - 1) / T);
+          c.y = static_cast<int>(((u + n) * C - 1) / T);
+        }
+      }
+      s_ctas[tid] = c;
     }
-    const int t = t0 + j * kAddThreads + tid;
-    if (t >= s.L) break;
-    const bool is_new = t >= s.L - fresh;
-    a.mass_out[row + t] = is_new ? w[j] : old[j] + w[j];
-    if (is_new && a.positions != nullptr) a.positions[row + t] = last - (s.L - 1 - t);
+    float old[kAddTiles];
+#pragma unroll
+    for (int j = 0; j < kAddTiles; ++j) {
+      const int t = t0 + j * kAddThreads + tid;
+      old[j] = t < s.L - fresh ? a.mass[row + t] : 0.f;
+    }
+    __syncthreads();
+    const float* part = a.ws_part +
+                        ((static_cast<size_t>(b) * a.Hkv + h) * a.max_kt + t0 / kKeys) * kHalves * kKeys +
+                        tid;
+    float w[kAddTiles];
+    const int4 c01 = *reinterpret_cast<const int4*>(s_ctas), c23 = *reinterpret_cast<const int4*>(s_ctas + 2);
+    const int c0[kAddTiles] = {c01.x, c01.z, c23.x, c23.z}, c1[kAddTiles] = {c01.y, c01.w, c23.y, c23.w};
+#pragma unroll
+    for (int j = 0; j < kAddTiles; ++j) {
+      const float* p = part + static_cast<size_t>(j + c0[j]) * kHalves * kKeys;
+      w[j] = 0.f;
+      if (c0[j] <= c1[j])
+#pragma unroll
+        for (int i = 0; i < kHalves; ++i) w[j] += p[i * kKeys];
+    }
+#pragma unroll
+    for (int j = 0; j < kAddTiles; ++j) {
+#pragma unroll 1
+      for (int c = c0[j] + 1; c <= c1[j]; c += 4) {  // four CTAs' in flight
+        float v[4 * kHalves];
+#pragma unroll
+        for (int i = 0; i < 4 * kHalves; ++i)
+          v[i] = c + i / kHalves <= c1[j]
+                     ? part[(static_cast<size_t>(j + c) * kHalves + i) * kKeys]
+                     : 0.f;
+#pragma unroll
+        for (int i = 0; i < 4 * kHalves; ++i) w[j] += v[i];
+      }
+      const int t = t0 + j * kAddThreads + tid;
+      if (t >= s.L) break;
+      const bool is_new = t >= s.L - fresh;
+      a.mass_out[row + t] = is_new ? w[j] : old[j] + w[j];
+      if (is_new && a.positions != nullptr) a.positions[row + t] = last - (s.L - 1 - t);
+    }
   }
 }
 
@@ -881,7 +883,12 @@ cudaError_t launch_mass(const MassArgs& a, int num_sms, cudaStream_t stream) {
                        a.tmQ, a);
   if (e != cudaSuccess) return e;
   const long long reach = std::min<long long>(static_cast<long long>(a.max_pages) * kPage, a.slots);
-  const dim3 grid(static_cast<unsigned>((reach + kAddTokens - 1) / kAddTokens), a.Hkv, a.B);
+  // (as many blocks as fill the GPU a few times: the table may be far wider than its rows are
+  // long)
+  const long long units = static_cast<long long>(a.Hkv) * a.B;
+  const long long blocks = std::min((reach + kAddTokens - 1) / kAddTokens,
+                                    (32LL * num_sms + units - 1) / units);
+  const dim3 grid(static_cast<unsigned>(blocks), a.Hkv, a.B);
   return launch_dependent(attn_mass_add_kernel, grid, kAddThreads, 0, stream, a, num_sms);
 }
 

@@ -204,3 +204,18 @@ def test_many_short_rows(d):
     c = Cache(lens, 1, 2, d, seed=d)
     c.run([int(g.integers(0, n + 2)) for n in lens], 2, 6)
     assert ea.attn_device_status() == ea.ATTN_OK
+
+
+@pytest.mark.parametrize("width", [340, 2600])
+def test_rows_of_all_lengths_in_a_wide_table(width):
+    """Short, longer and long rows side by side (selected by kernels of their own), in tables
+    wider than any of them."""
+    lens = [5000, 30, 4096, 4097, 0, 4700, 33, 1] + ([41100, 40960, 40961, 9000] if width > 340
+                                                     else [4500])
+    c = Cache(lens, 1, 2, 64, seed=width)
+    extra = width - len(c.table[0])
+    assert extra > 0
+    c.table = [list(t) + [-1] * extra for t in c.table]
+    keep = [4000, 10, 4095, 20, 0, 4700, 33, 0] + ([4096, 40900, 100, 4097] if width > 340 else [9])
+    c.run(keep, 3, 40)
+    assert ea.attn_device_status() == ea.ATTN_OK

@@ -815,7 +815,6 @@ __global__ void __launch_bounds__(kMassThreads)
   const size_t slots = static_cast<size_t>(a.max_pages) * kPage;
   const float scale2 = a.scale * kLog2eDec;
   const int warp = tid >> 5, lane = tid & 31;
-  bool merged = false;  // the log-sum-exps of all heads are in s_lse2
 #pragma unroll 1
   for (int t0 = (blockIdx.x - merge_blocks) * kMassTokens; t0 < L;
        t0 += (gridDim.x - merge_blocks) * kMassTokens) {
@@ -823,8 +822,8 @@ __global__ void __launch_bounds__(kMassThreads)
     const int t = t0 + tid * 4;  // the raw scores of a token beyond L are -inf or not read
     for (int c = 0; c < G; c += kMassHeads) {
       const int n = min(G - c, kMassHeads);
-      if (!merged) __syncthreads();
-      for (int g = merged ? n : warp; g < n; g += kMassThreads / 32) {
+      __syncthreads();
+      for (int g = warp; g < n; g += kMassThreads / 32) {
         const float* ls = a.ws_lse + (row0 + c + g) * S;
         const float sg = a.sink ? a.sink[hkv * G + c + g] : -INFINITY;
         const float l0 = lane < S ? ls[lane] : -INFINITY;
@@ -838,8 +837,7 @@ __global__ void __launch_bounds__(kMassThreads)
         sum += expf(sg - M);
         if (lane == 0) s_lse2[g] = (M + logf(sum)) * kLog2eDec;
       }
-      if (!merged) __syncthreads();
-      merged = G <= kMassHeads;
+      __syncthreads();
       if (t < L) {
         const float* sc = a.ws_scores + (row0 + c) * slots + t;
         for (int g = 0; g < n; ++g) {

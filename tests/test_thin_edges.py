@@ -183,3 +183,29 @@ def test_many_rows(B, size):
     assert (o.float() - ro.float()).abs().max() <= 2e-3 + 2 * 2.0 ** -8 * ro.abs().max()
     assert (lse - rl)[seen].abs().max() <= 2e-5
     assert torch.isneginf(lse[~seen]).all() and (o[~seen] == 0).all()
+
+
+def test_pools_past_32_bits():
+    """Rows on the last pages of pools of 2.3e9 elements (past 2^31), the same rows on small
+    pools: the same bits."""
+    c = Cache(6, 16, 8, 128, [300, 290, 17, 0, 256, 299], 15, seed=5)
+    P, n = 140000, c.k.shape[0]
+    big = [torch.empty(P, 16, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    want = {call: getattr(c, call)() for call in CALLS[:3]}
+    for x, pool in zip((c.k, c.v), big):
+        pool[P - n:] = x
+    small, c.k, c.v, c.pt = (c.k, c.v, c.pt), big[0], big[1], c.pt + (P - n)
+    for call in CALLS[:3]:
+        got = getattr(c, call)()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want[call])), call
+    # and the eviction: the first page's rows move on the large pools as on the small ones
+    keep, own = c.ln // 3, torch.arange(6 * c.W, dtype=torch.int32, device="cuda").view(6, c.W)
+    k, v = small[0].clone(), small[1].clone()
+    args = c.mass.clone(), c.pos.clone(), own, c.ln, keep, k, v
+    new = ea.attn_evict_paged(*args)
+    far = ea.attn_evict_paged(c.mass.clone(), c.pos.clone(), own + (P - n), c.ln, keep, *big)
+    torch.cuda.synchronize()
+    assert torch.equal(new, far)
+    assert torch.equal(big[0][P - n:], k) and torch.equal(big[1][P - n:], v)
+    assert ea.attn_device_status() == ea.ATTN_OK

@@ -744,11 +744,15 @@ __global__ void __launch_bounds__(kThr, 1)
 // ---------------------------------------------------------------- merge
 // A warp for each (row, query head), two at d = 256: the partial results of its group's prefix, CTA by
 // CTA, then those of its own pages, split by split, 32 at a time: their log-sum-exps are
-// read a lane each, the outputs so far scaled to the new maximum, and four outputs are
-// under way together (read one behind the other, 20 partial results took 25 us).
-constexpr int kMergeThreads = 256;
+// read a lane each, the outputs so far scaled to the new maximum, and kWide outputs are
+// under way together.  A chain of reads, so what does not depend on the last one is read beside
+// it, and of few (row, head) pairs eight outputs at a time (48 rows that share 65,519 tokens:
+// 115 us, with four 118); of more than kMergeFew four, whose registers leave room for more
+// warps (1,000 rows of 32 heads 132 us, with eight 141).
+constexpr int kMergeThreads = 256, kMergeFew = 4096;
+static_assert(kSharedMaxCtas % 32 == 0, "runs a lane holds");
 
-template <int D>
+template <int D, int kWide>
 __global__ void __launch_bounds__(kMergeThreads)
     attn_shared_merge_kernel(const SharedArgs a, const DecodeLaunch dec) {
   constexpr int kWarps = D == 256 ? 2 : 1;  // warps of a row: 128 columns each at most
@@ -760,6 +764,10 @@ __global__ void __launch_bounds__(kMergeThreads)
   if (row >= a.B * a.Hq) return;
   const int b = row / a.Hq, hq = row - b * a.Hq, S = dec.num_splits;
   const int4 info = a.rowinfo[b];  // group (-1: none that shares pages), first pair
+  long long runs[kSharedMaxCtas / 32];  // (read beside rowinfo, not behind it)
+#pragma unroll
+  for (int i = 0; i < kSharedMaxCtas / 32; ++i)
+    runs[i] = 32 * i + lane < a.ctas ? a.runs[32 * i + lane] : LLONG_MAX;
   // Rows of partial results fit in 32 bits without sign: 2 * 2^30 and the CTAs' 256 each.
   uint32_t part = 0, second = 0;  // the first; distance of the second stream's
   int n_prefix = 0, pairs_of = 0;
@@ -774,11 +782,10 @@ __global__ void __launch_bounds__(kMergeThreads)
     // the CTAs whose runs hold the item's units: runs that start at or before the first and
     // the last of them (those without units start past all)
     int first = 0, last = 0;
-#pragma unroll 2
-    for (int c = lane; c < a.ctas; c += 32) {
-      const long long start = a.runs[c];
-      first += start <= u;
-      last += start < u + tiles;
+#pragma unroll
+    for (int i = 0; i < kSharedMaxCtas / 32; ++i) {
+      first += runs[i] <= u;
+      last += runs[i] < u + tiles;
     }
     const int c0 = __reduce_add_sync(0xffffffffu, first) - 1;
     n_prefix = __reduce_add_sync(0xffffffffu, last) - c0;
@@ -823,10 +830,9 @@ __global__ void __launch_bounds__(kMergeThreads)
     uint32_t some = __ballot_sync(0xffffffffu, w > 0.f);
 #pragma unroll 1
     while (some != 0) {
-      // four at a time
-      float v[4][kPer], wj[4];
+      float v[kWide][kPer], wj[kWide];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kWide; ++j) {
         const int at = some != 0 ? __ffs(some) - 1 : 0;
         wj[j] = some != 0 ? __shfl_sync(0xffffffffu, w, at) : 0.f;
         const float* from = reinterpret_cast<const float*>(
@@ -845,7 +851,7 @@ __global__ void __launch_bounds__(kMergeThreads)
         some &= some - 1;
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < kWide; ++j)
 #pragma unroll
         for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wj[j], v[j][e], acc[e]);
     }
@@ -906,8 +912,9 @@ cudaError_t launch_shared(SharedArgs a, const DecodeLaunch& dec, int num_sms,
   if ((e = launch_attn_decode_own(dec, stream)) != cudaSuccess) return e;
   const int per = kMergeThreads / 32 / (D == 256 ? 2 : 1);  // rows of a block
   const int blocks = (a.B * a.Hq + per - 1) / per;
-  return launch_dependent(attn_shared_merge_kernel<D>, dim3(blocks), kMergeThreads, 0, stream, a,
-                          dec);
+  auto merge = a.B * a.Hq <= kMergeFew ? attn_shared_merge_kernel<D, 8>
+                                       : attn_shared_merge_kernel<D, 4>;
+  return launch_dependent(merge, dim3(blocks), kMergeThreads, 0, stream, a, dec);
 }
 
 }  // namespace

@@ -209,3 +209,16 @@ def test_pools_past_32_bits():
     assert torch.equal(new, far)
     assert torch.equal(big[0][P - n:], k) and torch.equal(big[1][P - n:], v)
     assert ea.attn_device_status() == ea.ATTN_OK
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,d", [(300, 16, 4, 128), (600, 8, 1, 256), (256, 16, 2, 64),
+                                        (257, 16, 2, 64)])
+def test_many_rows_and_heads(B, Hq, Hkv, d):
+    """4,096 merged (row, head) pairs and more."""
+    c = Cache(B, Hq, Hkv, d, [200 + (31 * b) % 150 for b in range(B)], 12, seed=B)
+    o, lse = ea.attn_decode_paged_shared(*c.paged(), i32([0, 90, B]), i32([192, 192]))
+    ro, rl = ea.attn_decode_paged(*c.paged(), num_splits=2)
+    torch.cuda.synchronize()
+    assert ea.attn_device_status() == ea.ATTN_OK
+    assert (o.float() - ro.float()).abs().max() <= 2e-3 + 2 * 2.0 ** -8 * ro.abs().max()
+    assert (lse - rl).abs().max() <= 2e-5

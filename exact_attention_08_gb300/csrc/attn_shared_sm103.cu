@@ -144,10 +144,12 @@ __global__ void __launch_bounds__(kThreads) attn_shared_plan_kernel(const Shared
   if (tid == 0) s_items = s_longest = 0;
   // offsets that decrease or leave the list: no group is used
   bool bad = false;
+  if (a.cu_groups != nullptr) {  // (may be null where there are no groups)
 #pragma unroll 1
-  for (int g = tid; g <= a.n_groups; g += kThreads) {
-    const int c = a.cu_groups[g];
-    bad |= c < 0 || c > a.n_rows || (g > 0 && c < a.cu_groups[g - 1]);
+    for (int g = tid; g <= a.n_groups; g += kThreads) {
+      const int c = a.cu_groups[g];
+      bad |= c < 0 || c > a.n_rows || (g > 0 && c < a.cu_groups[g - 1]);
+    }
   }
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) atomicOr(a.status, kStatusBadInput);

@@ -567,6 +567,7 @@ ATTN_API int attn_pages_compact(int* page_table, const int* seqlens, int* refs, 
  *     through the table of the group's longest row).  seqlens [B] counts all
  *     keys of a row, shared ones among them; a row may end inside the prefix
  *     or hold nothing.
+ *   n_groups may be 0; cu_groups and prefix_lens may then be NULL.
  *   num_splits (1..64): splits of each row's own keys.
  *   Device-side checks (ATTN_ERR_BAD_INPUT; the results stay those of
  *   attn_decode_paged): offsets that decrease or leave [0, n_rows] (no group is

@@ -181,30 +181,65 @@ __global__ void __launch_bounds__(kThreads) attn_shared_plan_kernel(const Shared
     int e0 = 0, e1 = 0, prefix = 0;
     if (g < n_groups) e0 = a.cu_groups[g], e1 = a.cu_groups[g + 1], prefix = a.prefix_lens[g];
     long long best = -1;  // length and, downwards, row
+    int shortest = INT_MAX;
 #pragma unroll 1
     for (int e = e0 + part; e < e1; e += lanes) {
       const int b = a.rows ? a.rows[e] : e;
       if (b < 0 || b >= a.B || entry[b] != e) continue;
-      best = max(best, static_cast<long long>(row_length(a, b)) << 32 | (INT_MAX - b));
+      const int L = row_length(a, b);
+      best = max(best, static_cast<long long>(L) << 32 | (INT_MAX - b));
+      shortest = min(shortest, L);
     }
 #pragma unroll 1
-    for (int o = lanes / 2; o > 0; o >>= 1)
+    for (int o = lanes / 2; o > 0; o >>= 1) {
       best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+      shortest = min(shortest, __shfl_xor_sync(0xffffffffu, shortest, o));
+    }
     const int longest = static_cast<int>(best >> 32);
     const int at = static_cast<int>(INT_MAX - static_cast<uint32_t>(best));  // of any row
+    int pages = prefix < 0 ? 0 : min(prefix, max(longest, 0)) / kPage;
+    int sharing = e1 - e0;  // rows that share them
+    // Only rows that reach the end of the shared pages share them: in the product with the values
+    // a weight of zero does not keep out what is not finite, so no row may meet a key behind
+    // its end.  Where some rows end before, the pages are those of the longest row or the
+    // whole ones of the shortest that holds any, whichever saves more reads.
+    if (__any_sync(0xffffffffu, shortest < pages * kPage)) {
+      int full = 0, some = 0, least = INT_MAX;
+#pragma unroll 1
+      for (int e = e0 + part; e < e1; e += lanes) {
+        const int b = a.rows ? a.rows[e] : e;
+        if (b < 0 || b >= a.B || entry[b] != e) continue;
+        const int L = row_length(a, b);
+        full += L >= pages * kPage;
+        if (L > 0) ++some, least = min(least, L);
+      }
+#pragma unroll 1
+      for (int o = lanes / 2; o > 0; o >>= 1) {
+        full += __shfl_xor_sync(0xffffffffu, full, o);
+        some += __shfl_xor_sync(0xffffffffu, some, o);
+        least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+      }
+      if (shortest < pages * kPage) {
+        const int all = least / kPage;
+        const bool fewer = static_cast<long long>(some - 1) * all >
+                           static_cast<long long>(full - 1) * pages;
+        sharing = fewer ? some : full;
+        pages = fewer ? all : pages;
+      }
+    }
     if (g >= n_groups) continue;  // (the last groups' warps: nothing below is done together)
     if (part == 0 && (prefix < 0 || prefix > a.max_pages * kPage))
       atomicOr(a.status, kStatusBadInput);
-    int pages = prefix < 0 ? 0 : min(prefix, max(longest, 0)) / kPage;
     // Too little to share: every row for itself.
-    if (static_cast<long long>(max(e1 - e0 - 1, 1)) * pages < a.least) pages = 0;
+    if (static_cast<long long>(max(sharing - 1, 1)) * pages < a.least) pages = 0;
     if (part == 0) a.info[g] = make_int4(pages, e0, (e1 - e0) * a.G, at);
+    if (pages == 0) continue;
 #pragma unroll 1
     for (int e = e0 + part; e < e1; e += lanes) {
       const int b = a.rows ? a.rows[e] : e;
-      if (b < 0 || b >= a.B || entry[b] != e) continue;
-      a.start[b] = min(pages, (row_length(a, b) + kPage - 1) / kPage);
-      if (pages > 0) a.rowinfo[b] = make_int4(g, (e - e0) * a.G, 0, 0);
+      if (b < 0 || b >= a.B || entry[b] != e || row_length(a, b) < pages * kPage) continue;
+      a.start[b] = pages;
+      a.rowinfo[b] = make_int4(g, (e - e0) * a.G, 0, 0);
     }
   }
   __syncthreads();
@@ -558,20 +593,16 @@ __global__ void __launch_bounds__(kThr, 1)
         ok = false;
         break;
       }
-      // This thread's pair, its row of q and the keys it sees (both streams' threads work out the
-      // same pairs where they share a tile).  The queries then come eight 16-byte chunks at
+      // This thread's pair and its row of q (both streams' threads work out the same pairs where
+      // they share a tile).  The queries then come eight 16-byte chunks at
       // a time: one by one, each behind its row's index, they took 15 us an item.
       const int pr = two ? tid : r;
-      int lim = 0;
       {
         int row = -1;
         if (pr < it.rows) {
           const int pair = it.row0 + pr, member = pair / a.G;
           const int b = a.rows ? a.rows[it.first + member] : it.first + member;
-          if (b >= 0 && b < a.B) {
-            row = b * a.Hq + it.h * a.G + pair - member * a.G;
-            lim = min(row_length(a, b), it.keys);
-          }
+          if (b >= 0 && b < a.B) row = b * a.Hq + it.h * a.G + pair - member * a.G;
         }
         s_row[pr] = row;
       }
@@ -609,7 +640,6 @@ __global__ void __launch_bounds__(kThr, 1)
       if (lane == 0) mbar_arrive(q_full);
       ++items;
       if (stream >= C::kStreams) continue;  // d = 256: the other warps only load queries
-      const int lim_min = __reduce_min_sync(0xffffffffu, pr < it.rows ? lim : INT_MAX);
       float m_run = -INFINITY, m_used = -INFINITY, l = 0.f, corr = 0.f;
       int last = -1;  // S buffer of this stream's last job
       for (int j = C::kStreams == 2 ? stream : 0; j < J; j += C::kStreams) {
@@ -627,10 +657,10 @@ __global__ void __launch_bounds__(kThr, 1)
 #pragma unroll
         for (int c = 0; c < C::kKeys / 32; ++c) tmem_ld_wait_x32(x + 32 * c);
         const int ka = (it.kt + i) * C::kKeys;
-        if (ka + C::kKeys > lim_min) {
+        if (ka + C::kKeys > it.keys) {
 #pragma unroll
           for (int c = 0; c < C::kKeys; ++c)
-            if (ka + c >= lim) x[c] = __float_as_uint(-INFINITY);
+            if (ka + c >= it.keys) x[c] = __float_as_uint(-INFINITY);
         }
         float mx[8];
 #pragma unroll

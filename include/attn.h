@@ -575,7 +575,11 @@ ATTN_API int attn_pages_compact(int* page_table, const int* seqlens, int* refs, 
  *   it stands first); a prefix below 0 (0) or past the table (the longest row's
  *   length); a length out of range (taken into [0, max_pages_per_seq * 16]).  A
  *   page out of range reads zeros.
- *   Groups that share too little to gain by it are decoded row by row.
+ *   Groups that share too little to gain by it are decoded row by row, and so
+ *   are rows that end before their group's shared pages do (fewer pages are
+ *   shared where that saves more): what another row holds behind this one's
+ *   last page does not reach its results.  Slots of a row's last page past its
+ *   length must hold finite values, as for attn_fwd_paged.
  *   Partial results are merged in a fixed order: repeated calls give identical
  *   bits.
  *   workspace: attn_decode_shared_workspace_size(...) bytes (0 on invalid

@@ -1,11 +1,16 @@
 """Calls on shared and thinned caches at the ends of what they accept."""
+import numpy as np
 import pytest
 import torch
 
 import exact_attention_08_gb300 as ea
+from tests import _thin_ref as ref
+from tests._parity import compare, np64
 from tests.test_shared_parity import Batch
 
 pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
@@ -24,3 +29,49 @@ def test_no_groups_and_no_lists(d, listed):
     torch.cuda.synchronize()
     assert rc == ea.ATTN_OK and ea.attn_device_status() == ea.ATTN_OK
     b.check(o, lse)
+
+
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+@pytest.mark.parametrize("d,prefix,lens", [
+    (64, 700, [710, 100, 700, 0, 730, 650, 16, 5, 709]),    # a few rows end inside the prefix
+    (128, 700, [690, 710, 670, 200, 30, 699, 660, 400, 688]),   # all but one do
+    (256, 300, [290, 310, 260, 300, 17, 299, 270, 400, 288, 1]),
+])
+def test_values_behind_a_rows_end_stay_out_of_it(d, prefix, lens, value):
+    """Keys and values of a shared prefix that are not finite: rows that end before them are
+    what they are without them."""
+    b = Batch([(prefix, lens)], 8, 2, d, seed=d)
+    table = b.table[b.rows[int(np.argmax(lens))]]
+    at = prefix // 16 * 16 - 5             # a token of the prefix's last whole pages
+    b.v[table[at // 16], at % 16] = value
+    b.k[table[at // 16], at % 16, :, ::3] = value
+    o, lse = b.run(check=False)
+    before = [r for r, n in zip(b.rows, lens) if n <= at // 16 * 16]  # no page of theirs holds it
+    assert len(before) >= 4
+    want = Batch([(prefix, lens)], 8, 2, d, seed=d)
+    ro, rl = np.zeros((len(before), 8, d)), np.zeros((len(before), 8))
+    for i, r in enumerate(before):
+        k, v = (ref.gather(x.float().numpy(), want.table[r], want.lens[r]) for x in (want.k, want.v))
+        ro[i], rl[i], _ = ref.attend(np64(want.q[r]), k, v, d ** -0.5)
+    compare(o[before], lse[before], ro, rl, "rows before a value that is not finite")
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens", [
+    [900] * 3 + [480, 496, 512] * 3,                 # many rows end inside: their whole pages
+    [900 + i for i in range(9)] + [480, 16, 0],      # few do: the longest rows' pages
+    [900, 48, 32, 48, 0, 16]])                       # hardly anything to share
+def test_rows_of_unequal_lengths(d, lens):
+    """Rows that end inside their group's prefix, on both sides of what sharing fewer pages saves;
+    a value that is not finite shows in the rows that see it, and in no other."""
+    b = Batch([(896, lens)], 8, 2, d, seed=len(lens))
+    o, lse = b.run()
+    for _ in range(2):
+        again = b.run(check=False)
+        assert torch.equal(o.view(torch.int16), again[0].view(torch.int16))
+        assert torch.equal(lse, again[1])
+    table = b.table[b.rows[0]]
+    b.v[table[55], 3] = NAN
+    o, _ = b.run(check=False)
+    for r, n in zip(b.rows, lens):
+        assert torch.isfinite(o[r]).all() == (n <= 55 * 16)

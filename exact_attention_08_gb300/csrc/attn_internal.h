@@ -161,7 +161,6 @@ struct MassArgs {
   const int* new_tokens;      // [B], may be null
   int B, Hq, Hkv, G, d;
   int GP, TQ, HC;  // heads and tokens of a query tile; tiles that the group's heads take
-  unsigned long long tq_mul;  // 2^40 / TQ, rounded up
   int max_Sq, total_q, max_pages, num_pages, slots, max_kt;
   float scale2;  // scale log2 e
   int causal, window, n_sink;

@@ -115,14 +115,6 @@ __device__ __forceinline__ bool load_seq(const MassArgs& a, int b, Seq& s) {
 
 __device__ __forceinline__ int key_tiles(const Seq& s) { return (s.L + kKeys - 1) / kKeys; }
 
-// x / TQ for 0 <= x < 2^31: the multiplier is 2^40 / TQ rounded up, so the error, x (TQ - 1)
-// / 2^40 at most, stays below 1 / TQ (a division by a run-time value is 100 cycles and
-// more, and stands in every step of the walk).
-__device__ __forceinline__ int in_tiles(const MassArgs& a, int x) {
-  return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(x)) * a.tq_mul) >>
-                          40);
-}
-
 // The query tile of a unit: its first token and its head group.
 __device__ __forceinline__ int tile_token(const MassArgs& a, int u) {
   return (a.HC == 1 ? u : u / a.HC) * a.TQ;
@@ -138,8 +130,8 @@ __device__ __forceinline__ int query_tiles(const MassArgs& a, const Seq& s, int 
   int lo = 0, hi = s.Lq - 1;
   if (a.causal) lo = max(lo, ka - s.off);
   if (a.window > 0 && ka >= a.n_sink) hi = min(hi, kb + a.window - 1 - s.off);
-  *first = in_tiles(a, lo);
-  return hi < lo ? 0 : in_tiles(a, hi) - *first + 1;
+  *first = lo / a.TQ;
+  return hi < lo ? 0 : hi / a.TQ - *first + 1;
 }
 
 __device__ __forceinline__ long long* ws_cum(const MassArgs& a, int b) {

@@ -316,7 +316,6 @@ ATTN_API int attn_mass_paged(const void* q, const float* lse, const void* k_page
   }
   a.TQ = tile / a.GP;
   a.HC = a.G / a.GP;
-  a.tq_mul = ((1ull << 40) + a.TQ - 1) / a.TQ;
   if ((rc = whole_page_map(&a.tmK, k_pages, d, Hkv, num_pages_total, "k_pages")) != ATTN_OK)
     return rc;
   // with no query at all the map is of nothing that is read

@@ -6,7 +6,8 @@ import torch
 import exact_attention_08_gb300 as ea
 from tests import _thin_ref as ref
 from tests._parity import compare, np64
-from tests.test_shared_parity import Batch
+from tests.test_mass_parity import Rows
+from tests.test_shared_parity import Batch, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +76,34 @@ def test_rows_of_unequal_lengths(d, lens):
     o, _ = b.run(check=False)
     for r, n in zip(b.rows, lens):
         assert torch.isfinite(o[r]).all() == (n <= 55 * 16)
+
+
+def test_queries_past_2_to_the_24():
+    """2^24 queries and more of 65 heads on one key head (a query tile is one token then), of
+    which the last few see keys: 140 GB, of which only those few are read."""
+    Lq, L, H, d = (1 << 24) + 300, 300, 65, 64
+    torch.cuda.empty_cache()
+    r = Rows([L], H, 1, d, seed=1)
+    few = r.q(L)
+    q = torch.empty(Lq, H, d, dtype=torch.bfloat16, device="cuda")
+    q[-L:] = few.cuda()
+    lse = torch.full((H, Lq), 7.0, device="cuda")
+    args = r.k.cuda(), i32(r.table)
+    got = ea.attn_mass_paged(q, lse, *args, i32([0, Lq]), i32([L]),
+                             torch.zeros_like(r.mass).cuda(), max_seqlen_q=Lq)
+    want = ea.attn_mass_paged(few.cuda(), lse[:, :L].contiguous(), *args, i32([0, L]), i32([L]),
+                              torch.zeros_like(r.mass).cuda(), max_seqlen_q=L)
+    torch.cuda.synchronize()
+    del q, lse
+    torch.cuda.empty_cache()
+    assert ea.attn_device_status() == ea.ATTN_OK
+    a, b = (x[0, 0, :L].double().cpu().numpy() for x in (want, got))
+    # the plain block against the formula, then the same sums in another order
+    k, _ = r.keys(0)
+    w = np.zeros((1, L))
+    for i in range(L):
+        x = d ** -0.5 * (k[:i + 1, 0] @ np64(few[i]).T)
+        w[0, :i + 1] += np.exp(x - 7.0).sum(1)
+    # (a thread adds 16 weights of each of 300 query tiles to one of its four sums)
+    for x in (a, b):
+        assert (np.abs(x - w[0]) <= (ref.WEIGHT + 4810 * 2.0 ** -24) * w[0]).all()

@@ -835,7 +835,8 @@ __global__ void __launch_bounds__(kMassThreads)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         sum += expf(sg - M);
-        if (lane == 0) s_lse2[g] = (M + logf(sum)) * kLog2eDec;
+        // a head whose scores are all -inf attends to nothing: +inf makes every weight zero
+        if (lane == 0) s_lse2[g] = M == -INFINITY ? INFINITY : (M + logf(sum)) * kLog2eDec;
       }
       __syncthreads();
       if (t < L) {

@@ -619,6 +619,7 @@ ATTN_API int attn_decode_paged_shared(const void* q, const void* k_pages, const 
  *                exp(scale q_i . k_t - LSE_i),              t < L
  *   mass_out(b, h, t) = mass(b, h, t) + w for t < L - 1;  w for t = L - 1,
  * whose token is new: its position becomes last_positions[b] (NULL: L - 1).
+ * A head with LSE = -inf (every score of it is) has no weights.
  * mass_out may be mass; positions may be NULL.  A row longer than mass_slots,
  * or with a length out of range, has its mass left as it was
  * (ATTN_ERR_BAD_INPUT).  Sums run over the heads in order, in fp32.

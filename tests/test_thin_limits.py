@@ -107,3 +107,34 @@ def test_queries_past_2_to_the_24():
     # (a thread adds 16 weights of each of 300 query tiles to one of its four sums)
     for x in (a, b):
         assert (np.abs(x - w[0]) <= (ref.WEIGHT + 4810 * 2.0 ** -24) * w[0]).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 1, 64), (8, 2, 128), (16, 2, 256)])
+def test_scores_of_minus_infinity_leave_no_weight(Hq, Hkv, d):
+    """A row whose scores are all -inf attends to nothing, O = 0 and LSE = -inf: its keys get no
+    weight from that step."""
+    lens = [40, 17, 300, 1]
+    r = Rows(lens, Hq, Hkv, d, seed=d)
+    for b in (1, 2, 3):
+        for page in r.table[b][:(lens[b] + 15) // 16]:
+            r.k[page] = -INF
+    q = r.q(4).abs() + 0.5
+    args = q.cuda(), r.k.cuda(), r.v.cuda(), i32(r.table), i32(lens)
+    for splits in (1, 5):
+        mass = r.mass.cuda()
+        o, lse = ea.attn_decode_paged_mass(*args, mass, num_splits=splits)
+        torch.cuda.synchronize()
+        assert ea.attn_device_status() == ea.ATTN_OK
+        k, v = r.keys(0)
+        ro, rl, w = ref.attend(np64(q[0]), k, v, d ** -0.5)
+        compare(o[:1], lse[:1], ro[None], rl[None])
+        assert (o[1:] == 0).all() and torch.isneginf(lse[1:]).all()
+        for b, n in enumerate(lens):
+            want = r.mass[b].clone()
+            want[:, n - 1] = 0
+            if b == 0:
+                base = want[:, :n].double().numpy()
+                ref.check_mass(mass[b, :, :n].double().cpu().numpy(), base,
+                               w.reshape(Hkv, Hq // Hkv, n).sum(1))
+            else:
+                assert torch.equal(mass[b].cpu(), want), b

@@ -595,8 +595,9 @@ __global__ void __launch_bounds__(kThr, 1)
       mbar_wait(drain, 0, nullptr, kWaitLimitNs);
     } else if (warp == kWarpLse) {
       // ============================================================ LSEs
-      // -LSE log2 e of every column of a query tile, -inf where there is no query; the loads of
-      // a tile are in flight while the one before waits for its buffer.
+      // -LSE log2 e of every column of a query tile, -inf where there is no query or one that
+      // attended to nothing (LSE = -inf); the loads of a tile are in flight while the one
+      // before waits for its buffer.
       constexpr int kPer = C::kQN / 32;
       int tok[kPer], head[kPer];  // of this lane's columns
 #pragma unroll
@@ -625,7 +626,8 @@ __global__ void __launch_bounds__(kThr, 1)
       if (more) fetch();
       while (more) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) v[j] = next[j] * -kLog2e;
+        for (int j = 0; j < kPer; ++j)
+          v[j] = next[j] == -INFINITY ? -INFINITY : next[j] * -kLog2e;
         if (++i == units) {
           w.left -= units;
           more = walk_next(a, w);

@@ -646,7 +646,8 @@ ATTN_API int attn_decode_paged_mass(const void* q, const void* k_pages, const vo
  *   mass_out(b, h, t) = mass(b, h, t) + w, for the sequence's new tokens w.
  * q [total_q, Hq, d] bf16, lse [Hq, total_q] fp32 (attn_fwd_paged's, a logit
  * sink included if there was one), page_table, cu_seqlens_q, seqlens_k, max_Sq,
- * causal, window and n_sink as attn_fwd_paged's.  The block may be the last
+ * causal, window and n_sink as attn_fwd_paged's.  A query with LSE = -inf
+ * attended to nothing and has no weights.  The block may be the last
  * queries of a prompt only: they are aligned to the end of the keys.
  *   new_tokens: DEVICE int32 [B], how many of the sequence's last keys are new
  *     (their old mass is not read); NULL: as many as it has queries.  Taken

@@ -138,3 +138,25 @@ def test_scores_of_minus_infinity_leave_no_weight(Hq, Hkv, d):
                                w.reshape(Hkv, Hq // Hkv, n).sum(1))
             else:
                 assert torch.equal(mass[b].cpu(), want), b
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 1, 64), (8, 2, 128), (16, 2, 256)])
+def test_queries_without_a_key_have_no_weight(Hq, Hkv, d):
+    """LSE = -inf is a query that attended to nothing, whatever its scores: as if it were not
+    there."""
+    lens, nq = [300, 40], [50, 7]
+    r = Rows(lens, Hq, Hkv, d, seed=d)
+    q = r.q(57)
+    cu = i32([0, 50, 57])
+    lse = torch.full((Hq, 57), 6.0)
+    out = {}
+    for drop in (-INF, INF):             # a weight exp(s - inf) is none in any case
+        z = lse.clone()
+        z[:, 3:20], z[1, 55] = drop, drop
+        out[drop] = ea.attn_mass_paged(q.cuda(), z.cuda(), r.k.cuda(), i32(r.table), cu, i32(lens),
+                                       torch.zeros_like(r.mass).cuda(), max_seqlen_q=50)
+    torch.cuda.synchronize()
+    assert ea.attn_device_status() == ea.ATTN_OK
+    for b, n in enumerate(lens):
+        assert torch.isfinite(out[INF][b, :, :n]).all()
+        assert torch.equal(out[-INF][b, :, :n], out[INF][b, :, :n])

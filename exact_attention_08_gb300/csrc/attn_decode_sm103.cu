@@ -221,10 +221,14 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
   const int hchunk = blockIdx.y % p.n_hchunks;
   // Launched as a programmatic dependent of the order kernel: the launch
   // overlaps it, and this waits for its result.  (kDecShared: of the prefix
-  // kernel, which lets this one start only once it has itself seen the order.)
+  // kernel, which lets this one start only once every CTA of it has seen the plan's
+  // order and passed it on by a fence; the loads of it here acquire.)
   if constexpr (kMode != kDecShared) asm volatile("griddepcontrol.wait;" ::: "memory");
   int b = blockIdx.z;
-  if (kMode != kDecMass || p.order != nullptr) b = p.order[b];
+  if (kMode == kDecShared)
+    b = ld_acquire(p.order + b);
+  else if (kMode != kDecMass || p.order != nullptr)
+    b = p.order[b];
   const int g0 = hchunk * kHeadsPerCta;                  // first group member served
   const int nh = min(kHeadsPerCta, p.G - g0);            // query heads served
   const int h0 = hkv * p.G + g0;                         // first query head served
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm)
     L = max(0, min(L, p.max_pages * kPage));
   }
   const int np = (L + kPage - 1) / kPage;
-  const int first = kMode == kDecShared ? min(p.start[b], np) : 0;
+  const int first = kMode == kDecShared ? min(ld_acquire(p.start + b), np) : 0;
   const int pps = (np - first + p.num_splits - 1) / p.num_splits;
   const int pg0 = min(first + split * pps, np);
   const int pg1 = min(pg0 + pps, np);
@@ -504,10 +508,14 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   const int hchunk = blockIdx.y % p.n_hchunks;
   // Launched as a programmatic dependent of the order kernel: the launch
   // overlaps it, and this waits for its result.  (kDecShared: of the prefix
-  // kernel, which lets this one start only once it has itself seen the order.)
+  // kernel, which lets this one start only once every CTA of it has seen the plan's
+  // order and passed it on by a fence; the loads of it here acquire.)
   if constexpr (kMode != kDecShared) asm volatile("griddepcontrol.wait;" ::: "memory");
   int b = blockIdx.z;
-  if (kMode != kDecMass || p.order != nullptr) b = p.order[b];
+  if (kMode == kDecShared)
+    b = ld_acquire(p.order + b);
+  else if (kMode != kDecMass || p.order != nullptr)
+    b = p.order[b];
   const int g0 = hchunk * kHeadsPerCta;
   const int nh = min(kHeadsPerCta, p.G - g0);
   const int h0 = hkv * p.G + g0;
@@ -518,7 +526,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     L = max(0, min(L, p.max_pages * kPage));
   }
   const int np = (L + kPage - 1) / kPage;
-  const int first = kMode == kDecShared ? min(p.start[b], np) : 0;
+  const int first = kMode == kDecShared ? min(ld_acquire(p.start + b), np) : 0;
   const int pps = (np - first + p.num_splits - 1) / p.num_splits;
   const int pg0 = min(first + split * pps, np);
   const int pg1 = min(pg0 + pps, np);

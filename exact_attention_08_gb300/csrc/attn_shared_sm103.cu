@@ -436,7 +436,8 @@ __global__ void __launch_bounds__(kThr, 1)
   // The plan.  Only then may the decode of the rows' own pages start (it does not wait for
   // the plan itself, but for every CTA here to have seen it).
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
+  __threadfence();  // what the plan wrote, to the grid that this lets start
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();

@@ -165,6 +165,14 @@ __device__ __forceinline__ bool mbar_wait_far(uint64_t* bar, uint32_t parity,
   return mbar_wait_slow(bar, parity, abort_flag, limit_ns);
 }
 
+// For data of a grid that this one does not wait for itself: orders this load, and the ones
+// behind it, after what another grid passed on by a fence.
+__device__ __forceinline__ int ld_acquire(const int* ptr) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(ptr) : "memory");
+  return v;
+}
+
 // 32-byte global store (sm_100 and later); the address must be 32-byte aligned.
 __device__ __forceinline__ void st_global_v8(void* ptr, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(v[0]),

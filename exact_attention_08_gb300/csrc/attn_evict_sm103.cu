@@ -378,7 +378,7 @@ __device__ __forceinline__ uint32_t lowest_bits(uint32_t x, int n) {
 template <bool kFours, bool kCopies>
 __device__ __forceinline__ void select_row(const EvictArgs& a, int words, int unit, int layer, int b,
                                            int h, int L, int K) {
-  extern __shared__ uint32_t s_keys[];
+  extern __shared__ __align__(16) uint32_t s_keys[];  // (read four keys at a time)
   __shared__ int s_hist[kBins];
   __shared__ int s_group[kBins / 32];
   __shared__ int s_part[32];

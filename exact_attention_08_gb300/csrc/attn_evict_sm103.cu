@@ -337,7 +337,8 @@ __global__ void __launch_bounds__(kThreads) attn_evict_select_long_kernel(const 
     if (tid == 0) {
       *unit_count(a, unit) = total;
       if (lead) a.new_seqlens[b] = K;
-    }  }
+    }
+  }
   leave_last();
 }
 
@@ -687,13 +688,6 @@ cudaError_t launch_attn_evict(EvictArgs a, int num_sms, cudaStream_t stream) {
   const bool copies = a.copy_blocks == 0;
   auto words_of = [](int tokens) { return (tokens + 31) / 32; };
   auto bytes_of = [](int words) { return static_cast<size_t>(words) * 34 * 4; };
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   {
     const int to = std::min(cap, kSmallRow), words = words_of(to);
     auto select = fours ? (copies ? attn_evict_select_kernel<true, true>
@@ -711,25 +705,21 @@ cudaError_t launch_attn_evict(EvictArgs a, int num_sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int resident =
         std::max(1, std::min(4, static_cast<int>((224 << 10) / (bytes_of(words) + (11 << 10)))));
-    cfg.gridDim = dim3(std::min(a.units, resident * num_sms));
-    cfg.blockDim = dim3(kLargeThreads);
-    cfg.dynamicSmemBytes = bytes_of(words);
-    if ((e = cudaLaunchKernelEx(&cfg, select, a, words, to)) != cudaSuccess) return e;
-    cfg.dynamicSmemBytes = 0;
+    e = launch_dependent(select, dim3(std::min(a.units, resident * num_sms)), kLargeThreads,
+                         bytes_of(words), stream, a, words, to);
+    if (e != cudaSuccess) return e;
   }
   if (cap > kMaxCached) {
-    cfg.gridDim = dim3(std::min(a.units, 2 * num_sms));
-    cfg.blockDim = dim3(kThreads);
-    if ((e = cudaLaunchKernelEx(&cfg, attn_evict_select_long_kernel, a)) != cudaSuccess) return e;
+    e = launch_dependent(attn_evict_select_long_kernel, dim3(std::min(a.units, 2 * num_sms)),
+                         kThreads, 0, stream, a);
+    if (e != cudaSuccess) return e;
   }
   if (copies) return cudaSuccess;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.copy_blocks) * a.units);
-  cfg.blockDim = dim3(kCopyThreads);
   auto copy = a.vecs == 8    ? attn_evict_copy_kernel<8>
               : a.vecs == 16 ? attn_evict_copy_kernel<16>
                              : attn_evict_copy_kernel<32>;
-  e = cudaLaunchKernelEx(&cfg, copy, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_dependent(copy, dim3(static_cast<unsigned>(a.copy_blocks) * a.units), kCopyThreads,
+                          0, stream, a);
 }
 
 }  // namespace attn

@@ -248,6 +248,25 @@ class SharedMemoryLimit {
   std::atomic<uint64_t> done_{0};
 };
 
+// Launches a kernel as a programmatic dependent of the launch before it: it may start before
+// that one has ended, and waits (griddepcontrol.wait) for what it needs of it.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // Host-side helpers shared by the C-ABI translation units.
 int set_error(int code, const char* fmt, ...);
 int cuda_error(cudaError_t e, const char* what);

@@ -905,23 +905,6 @@ __global__ void __launch_bounds__(kMergeThreads)
     dec.lse[row] = M != -INFINITY ? M + logf(wsum) : -INFINITY;
 }
 
-template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
-                             cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 template <int D>
 cudaError_t launch_shared(SharedArgs a, const DecodeLaunch& dec, int num_sms,
                           cudaStream_t stream) {

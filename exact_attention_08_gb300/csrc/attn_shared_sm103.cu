@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) attn_shared_plan_kernel(const Shared
         least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
       }
       if (shortest < pages * kPage) {
-        const int all = least / kPage;
+        const int all = min(pages, least / kPage);  // (only empty rows may end before)
         const bool fewer = static_cast<long long>(some - 1) * all >
                            static_cast<long long>(full - 1) * pages;
         sharing = fewer ? some : full;

@@ -160,3 +160,11 @@ def test_queries_without_a_key_have_no_weight(Hq, Hkv, d):
     for b, n in enumerate(lens):
         assert torch.isfinite(out[INF][b, :, :n]).all()
         assert torch.equal(out[-INF][b, :, :n], out[INF][b, :, :n])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("prefix,shortest", [(22, 82), (16, 500), (170, 333), (15, 400)])
+def test_an_empty_row_among_rows_longer_than_the_prefix(d, prefix, shortest):
+    """No more pages are shared than the prefix has, whatever the rows that are not empty hold."""
+    b = Batch([(prefix, [shortest + 7 * i for i in range(40)] + [0])], 4, 2, d, seed=prefix)
+    b.run()

@@ -188,3 +188,28 @@ def test_many_rows(B, size, pages, Hq, Hkv, d):
         assert shares(len(lens), pages, d)
     o, lse = b.run(check=False)
     check_rows(b, o, lse, some(b, 40))
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_random_groups(seed):
+    """Groups of any sizes with rows of any lengths: empty ones, some that end inside the prefix,
+    some that the prefix does not reach the end of."""
+    g = np.random.default_rng(seed)
+    d, Hkv = int(g.choice([64, 128, 256])), int(g.choice([1, 2, 3]))
+    W = int(g.integers(2, 90))
+    groups = []
+    for _ in range(int(g.integers(1, 7))):
+        prefix = int(g.choice([g.integers(0, 60), g.integers(0, 16 * W + 1), 16 * W]))
+        prefix = min(prefix, 16 * W)
+        least = int(g.choice([0, 0, prefix]))
+        groups.append((prefix, g.integers(least, 16 * W + 1, int(g.choice([1, 2, 8, 17, 40]))).tolist()))
+        if g.random() < 0.5:
+            groups[-1][1][0] = 0
+    for prefix, lens in groups:        # (a page that several rows end in would be scaled by each)
+        lens[:] = [n if n >= prefix else n // 16 * 16 for n in lens]
+    b = Batch(groups, Hkv * int(g.choice([1, 2, 5, 8])), Hkv, d, alone=[0, 33], seed=seed)
+    b.W = max(b.W, W)
+    b.table = [t + [-1] * (b.W - len(t)) for t in b.table]
+    sink = seed % 3 == 0
+    o, lse = b.run(check=False, sink=sink)
+    check_rows(b, o, lse, some(b, 30), sink=sink)

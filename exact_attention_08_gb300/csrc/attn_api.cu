@@ -124,8 +124,9 @@ int make_map(CUtensorMap* m, const void* ptr, uint64_t d, uint64_t n1, uint64_t 
   return ATTN_OK;
 }
 
-// Page pool [pages, 16, Hkv, d] as (64 columns, 16 tokens, d / 64 atoms, Hkv, pages): a box is
-// a whole page of one head, atom by atom, each 16 rows of 128 bytes with the 128-byte swizzle.
+// Page pool [pages, 16, Hkv, d] as (64 columns, 8 tokens, d / 64 atoms, Hkv, 2 * pages): a box
+// is a whole page of one head as two halves of eight tokens, each atom by atom, 8 rows of 128
+// bytes with the 128-byte swizzle.
 int make_page_map(CUtensorMap* m, const void* ptr, int d, int Hkv, int pages, const char* what) {
   auto fn = encode_fn();
   if (!fn) return set_error(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available");

@@ -24,6 +24,9 @@
 // with M the largest split lse, summed in ascending split order, so the
 // result does not depend on which CTA finished first.
 //
+// P is rounded to bf16, the form in which mma takes it beside V; scores, maxima, sums and O are
+// fp32.
+//
 // The work is bound by HBM bandwidth: every KV byte is read once.  Small CTAs
 // (three warps, a 48 KB ring at d = 128) run four to an SM, so that one CTA's
 // ramp-up and drain overlap the others' streaming: 192 KB of pages in flight

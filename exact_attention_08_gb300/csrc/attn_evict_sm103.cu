@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kLargeThreads, 4) attn_evict_select_wide_kerne
   leave_last();
 }
 
-// The same by a.copy_blocks blocks a unit.
+// copy_moves by a.copy_blocks blocks a unit.
 template <int kVecs>
 __global__ void __launch_bounds__(kCopyThreads) attn_evict_copy_kernel(const EvictArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -164,7 +164,10 @@ struct MassArgs {
   int max_Sq, total_q, max_pages, num_pages, slots, max_kt;
   float scale2;  // scale log2 e
   int causal, window, n_sink;
-  long long* ws_plan;  // [B, max_kt + 1] units before a key tile; [B + 1] before a sequence
+  // [B, max_kt + 1] positions (units, and what entering a key tile costs) before a key tile of a
+  // sequence; [B + 1] before a sequence; [B, max_kt] pairs of int, a key tile's first query
+  // tile and its units
+  long long* ws_plan;
   float* ws_part;      // partial sums [B * Hkv * max_kt + CTAs, mass_partial_floats]
   int* status;
 };

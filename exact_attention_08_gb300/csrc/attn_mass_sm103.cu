@@ -11,6 +11,10 @@
 // (query, key), and the tensor cores' 512 cycles for 128 x 128 x 128 against 512
 // of the exponential units.
 //
+// Precision.  Scores, exponents and sums are fp32 (ex2.approx: 2^-22 of a weight), products
+// of bf16 exact: a mass of thousands of weights is some 3.4e-7 of itself off fp64, where fp32
+// torch operations on the same inputs are 4.4e-8 off.
+//
 // Operands.  With both in shared memory, M = N = 128, the tensor cores read 128 bytes
 // of it a cycle, all there is, and the tiles' arrival and the LSEs come on top: 1,570
 // cycles a unit (two row tiles against one query tile) instead of 1,024.  So a key
@@ -66,8 +70,10 @@ constexpr int kWarpProducer = kSumWarps;
 constexpr int kWarpIssuer = kSumWarps + 1;
 constexpr int kWarpLse = kSumWarps + 2;
 constexpr int kThr = 32 * (kSumWarps + 3);
-// What starting a key tile costs, in units (8,192 tokens, causal, 32 heads over 8: 258 us
-// at 0, 242 at 2, 236 at 4, 237 at 6; short blocks of 300 queries 39.9, 36.9, 38.3, 40.3).
+// What starting a key tile costs, in units (8,192 tokens, causal, 32 heads over 8: 245.1 us
+// at 0, 235.4 at 2, 234.5 at 3, 234.9 at 4, 236.1 at 6; eight chunks of 8 to 512 queries, d =
+// 256, 36.9, 35.6, 36.9, 37.4, 39.0; 64 prompts of 300 tokens 76.6, 80.1, 80.1, 80.0, 82.0; 8 of
+// 2,000, 16 heads over 4, 81.2, 78.3, 78.0, 78.4, 79.5).
 constexpr int kItemCost = 3;
 // Query tiles from which a key tile is copied to tensor memory (8,192 tokens, causal: 257 us, 261
 // without; from 8, 16 or 32 tiles on: within 1 % there, up to 3 % either way on short blocks).

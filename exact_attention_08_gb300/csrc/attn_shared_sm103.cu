@@ -16,6 +16,10 @@
 // as the second operand of S needs them, and a page is one step of 16 tokens of the operand of
 // O.
 //
+// Precision.  P is rounded to bf16, the form in which the tensor cores take it beside V, as in the
+// split decode; sums, maxima and O are fp32.  O is 2.3e-3 of itself off fp64 by norm, where
+// its own rounding to bf16 makes 1.65e-3.
+//
 // With S = Q K^T and O += P V on the tensor cores and the online softmax between them, a
 // key tile keeps an SM busy for less time than HBM needs to bring its keys and values
 // while an item has at most 256 rows; more rows find them in L2.
@@ -74,12 +78,19 @@ struct Cfg {
 
 // ---------------------------------------------------------------- plan
 // A group shares its prefix where (rows - 1) pages d reaches this.  Rows that read the same
-// pages one after the other find them in L2, so sharing costs more than it saves up to some
-// 9 pages for 8 rows at d = 128 (64 groups of 8, 8 key heads: 1 page 1.19 of the time row by
-// row, 8 pages 1.02, 16 pages 0.91, 128 pages 0.48) and some 64 for two.  A single row counts
-// as two: nothing is read less often, but a long row is spread over the CTAs, where its few
-// splits would be the last to finish (16 groups of 1 to 7 rows, 64 to 256 pages: 70 us, with
-// single rows from 128 pages on 96, by themselves 126).
+// pages one after the other find them in L2, so sharing a few pages costs more than it saves.
+// Its time over that of the rows one by one, 32 heads over 8:
+//   64 groups of 8  d = 64   8 pages 1.05, 16 0.95, 32 0.79, 128 0.48
+//                   d = 128  1 page 1.30, 8 1.05, 10 1.08, 16 0.93, 128 0.46
+//                   d = 256  2 pages 1.07, 4 0.96, 16 0.63
+//   200 groups of 2 d = 64   64 pages 1.17, 128 1.10, 192 1.11
+//                   d = 128  32 pages 1.20, 64 1.04, 96 1.00
+//                   d = 256  16 pages 0.93, 32 0.78
+// The border goes by d, as the bytes do; only for pairs the rule is early at d = 64 (by a tenth of
+// the time) and late at d = 256.  A single row counts as two: nothing is read less often, but a
+// long row is spread over the CTAs, where its few splits would be the last to finish (16 groups
+// of 1 to 7 rows, 64 to 256 pages: 70 us, with single rows from 128 pages on 96, by
+// themselves 126).
 constexpr int kLeastShared = 8192;
 // One block: rows to groups, the pages that every group shares, units before each group,
 // where each CTA of the prefix kernel begins, first own page of every row, and the rows in

@@ -624,8 +624,10 @@ ATTN_API int attn_decode_paged_shared(const void* q, const void* k_pages, const 
  * or with a length out of range, has its mass left as it was
  * (ATTN_ERR_BAD_INPUT).  Sums run over the heads in order, in fp32.
  *   workspace: attn_decode_mass_workspace_size(...) bytes (the decode's, and
- *   the raw scores, fp32 [B, Hq, max_pages_per_seq * 16]), 16-byte aligned.
- *   B and Hq at most 65,535, B * Hq at most 2^30.
+ *   the raw scores, fp32 [B, Hq, max_pages_per_seq * 16]: by the table's width,
+ *   not by the rows' lengths, so a table far wider than its rows (32,768 pages,
+ *   64 rows of 32 heads: 4.3 GB) is better passed cut to the longest of them),
+ *   16-byte aligned.  B and Hq at most 65,535, B * Hq at most 2^30.
  */
 ATTN_API size_t attn_decode_mass_workspace_size(int B, int Hq, int d, int max_pages_per_seq,
                                                 int num_splits);
